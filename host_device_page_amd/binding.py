@@ -45,6 +45,13 @@ HC_FLAG_PROFILE = 2
 HC_MAX_SUBBUFS = 4
 HC_DUPLEX_LOAD_BACK_CTAS = 8
 HC_NOALLOC_MAX_TOKENS = 262144
+HC_BF16 = 0
+HC_F16 = 1
+HC_ROPE_NONE = 0
+HC_ROPE_LINEAR = 1
+HC_ROPE_LLAMA3 = 2
+HC_ROPE_YARN = 3
+HC_MAX_ROT_DIM = 256
 
 # hc_pool_kernel_time kinds
 KIND_GATHER, KIND_ZC_WRITE, KIND_ZC_READ, KIND_PADS, KIND_COMPARE, KIND_COPY_ENGINE, KIND_PACK, KIND_UNPACK = range(8)
@@ -74,8 +81,34 @@ class hc_pool_stats(ctypes.Structure):
         "load_back_calls", "load_back_tokens", "load_back_bytes", "device_errors")]
 
 
-_D = ctypes.POINTER(hc_pool_desc)
 _V = ctypes.c_void_p
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
+
+
+class hc_rope_desc(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("rot_dim", "rot_offset", "interleaved", "scaling")]
+                + [(n, ctypes.c_double) for n in ("base", "factor", "low_freq_factor", "high_freq_factor",
+                                                  "beta_fast", "beta_slow", "magnitude")]
+                + [("original_context", _I64)])
+
+
+class hc_store_desc(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("layer", "dtype", "q_heads", "kv_heads", "head_dim", "value_dim")]
+                + [("n", _I64)] + [(n, _V) for n in ("slots", "positions", "q", "q_out", "k", "v")]
+                + [(n, _I64 * 2) for n in ("q_stride", "q_out_stride", "k_stride", "v_stride")] + [("rope", _V)])
+
+
+class hc_attend_desc(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("layer", "dtype", "q_heads", "kv_heads", "head_dim", "value_dim",
+                                     "value_in_key", "causal", "entry_tokens")]
+                + [("scale", ctypes.c_float)]
+                + [(n, _I64) for n in ("window", "sinks", "num_seqs", "q_rows", "max_q", "max_kv", "table_width",
+                                       "table_stride")]
+                + [(n, _V) for n in ("q", "out", "lse", "q_start", "kv_len", "table")]
+                + [("q_stride", _I64 * 2), ("out_stride", _I64 * 2), ("workspace", _V), ("workspace_bytes", _I64)])
+
+
+_D = ctypes.POINTER(hc_pool_desc)
 
 LOAD_LAYER_FN = ctypes.CFUNCTYPE(ctypes.c_int, _V, ctypes.c_int32, _V, _V, ctypes.c_int64, _V)
 WAIT_EVENT_FN = ctypes.CFUNCTYPE(ctypes.c_int, _V, _V)
@@ -108,6 +141,17 @@ _SIGS = {
     "hc_layer_pack_bytes": (ctypes.c_int, [_V, ctypes.c_int64, _I64P]),
     "hc_layer_pack": (ctypes.c_int, [_V, ctypes.c_int32, _V, ctypes.c_int64, _V, ctypes.c_int64, _V]),
     "hc_layer_unpack": (ctypes.c_int, [_V, ctypes.c_int32, _V, ctypes.c_int64, _V, ctypes.c_int64, _V]),
+    "hc_rope_create": (ctypes.c_int, [ctypes.POINTER(hc_rope_desc), ctypes.POINTER(_V)]),
+    "hc_rope_destroy": (ctypes.c_int, [_V]),
+    "hc_rope_frequencies": (ctypes.c_int, [_V, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+    "hc_store_tokens": (ctypes.c_int, [_V, ctypes.POINTER(hc_store_desc), _V]),
+    "hc_attend_workspace_bytes": (ctypes.c_int, [_V, ctypes.POINTER(hc_attend_desc), _I64P]),
+    "hc_attend": (ctypes.c_int, [_V, ctypes.POINTER(hc_attend_desc), _V]),
+    "hc_copy_pages": (ctypes.c_int, [_V, _V, _V, _I64, _V]),
+    "hc_fork_pages": (ctypes.c_int, [_V, _V, _I64, _I64, _I64, _V, _V, _I64, _V, _I64, _V, _I64, _V, _V]),
+    "hc_pages_workspace_bytes": (ctypes.c_int, [_V, _I64P]),
+    "hc_free_pages": (ctypes.c_int, [_V, _V, _I64, _I64, _I64, _V, _V, _V, _V, _I64, _V]),
+    "hc_compact_pages": (ctypes.c_int, [_V, _V, _I64, _I64, _I64, _V, _V, _I64, _V, _V, _I64, _V]),
     "hc_load_back_graph_create": (ctypes.c_int, [_V, _V, _V, ctypes.c_int64, ctypes.POINTER(_V),
                                                  ctypes.POINTER(_V)]),
     "hc_load_back_graph_launch": (ctypes.c_int, [_V]),
@@ -366,9 +410,81 @@ def _in_use_on(stream, *tensors):
             t.record_stream(stream)
 
 
-def _torch_int64():
+def _torch():
     import torch
-    return torch.int64
+    return torch
+
+
+def _torch_int64():
+    return _torch().int64
+
+
+class Rope:
+    """hc_rope: rotary positions, with their scaling for long contexts (see hc_rope_desc).
+    scaling: "none", "linear", "llama3" or "yarn"; magnitude None: the scaling's own."""
+
+    SCALINGS = {"none": HC_ROPE_NONE, "linear": HC_ROPE_LINEAR, "llama3": HC_ROPE_LLAMA3, "yarn": HC_ROPE_YARN}
+
+    def __init__(self, *, rot_dim: int, base: float = 10000.0, rot_offset: int = 0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original_context: int = 0, low_freq_factor: float = 1.0,
+                 high_freq_factor: float = 4.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 magnitude: float | None = None):
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"unknown scaling {scaling!r}")
+        self.handle = _V()
+        self.rot_dim = rot_dim
+        d = hc_rope_desc(rot_dim, rot_offset, 1 if interleaved else 0, self.SCALINGS[scaling], base, factor,
+                         low_freq_factor, high_freq_factor, beta_fast, beta_slow, magnitude or 0.0, original_context)
+        check(lib.hc_rope_create(ctypes.byref(d), ctypes.byref(self.handle)), "hc_rope_create")
+
+    def frequencies(self):
+        """(radians per position of each pair, the factor on sines and cosines)."""
+        f, m = (ctypes.c_double * (self.rot_dim // 2))(), ctypes.c_double()
+        check(lib.hc_rope_frequencies(self.handle, f, ctypes.byref(m)), "hc_rope_frequencies")
+        return list(f), m.value
+
+    def close(self) -> None:
+        if self.handle.value:
+            check(lib.hc_rope_destroy(self.handle), "hc_rope_destroy")
+            self.handle = _V()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _heads(x, what: str, like=None):
+    """A (rows, heads, dim) CUDA tensor of bf16 or fp16 with contiguous heads, `like` another's dtype."""
+    if not getattr(x, "is_cuda", False) or x.dim() != 3:
+        raise TypeError(f"{what} must be a CUDA tensor of (rows, heads, dim)")
+    if str(x.dtype) not in _DTYPES or (like is not None and x.dtype != like.dtype):
+        raise TypeError(f"{what} has dtype {x.dtype}" + (f", not {like.dtype}" if like is not None else ""))
+    if x.shape[2] > 1 and x.stride(2) != 1:
+        raise TypeError(f"{what}: the elements of a head must be contiguous")
+    return x
+
+
+_DTYPES = {"torch.bfloat16": HC_BF16, "torch.float16": HC_F16}
+
+
+def _table(x, what: str):
+    """(address, rows, width, row stride) of an int64 CUDA table with contiguous rows."""
+    if not getattr(x, "is_cuda", False) or x.dtype != _torch_int64() or x.dim() != 2:
+        raise TypeError(f"{what} must be an int64 CUDA tensor of (rows, entries)")
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise TypeError(f"{what}: the entries of a row must be contiguous")
+    return x.data_ptr(), x.shape[0], x.shape[1], max(x.stride(0), 0)
+
+
+def _on(stream, tensor, *used):
+    """The stream a forward-pass call runs on: `stream`, whose work the tensors are then marked
+    in use by, or torch's current stream of their device (as for torch's own operators)."""
+    if stream is None:
+        return _V(_torch().cuda.current_stream(tensor.device).cuda_stream)
+    _in_use_on(stream, tensor, *used)
+    return _V(stream.cuda_stream)
 
 
 class Pool:
@@ -383,6 +499,7 @@ class Pool:
         sub_specs = [(g, e, [_ptr(t) for t in device_layers[b]]) for b, (g, e) in enumerate(subs)]
         self.stream = stream
         self.layers = layers
+        self.page_size = page_size
         self.desc, self._keep = make_desc(
             layers=layers, page_size=page_size, subs=sub_specs, device_slots=device_slots,
             host_pages=host_pages, layout=layout, shard_align=shard_align, host_ptr=_ptr(host),
@@ -501,6 +618,147 @@ class Pool:
                                  event.handle if event else None)
         _in_use_on(self.stream, device_idx, src)
         check(rc, "hc_layer_unpack")
+
+    # The forward pass on the device side (hc.h: forward pass on the device pool).  `stream`:
+    # a torch stream, None for torch's current one.
+    def store_tokens(self, layer: int, slots, k, v=None, *, q=None, q_out=None, rope: Rope | None = None,
+                     positions=None, stream=None):
+        """Keys k (rotated) and values v of new tokens into their slots of one layer; queries q
+        rotated into q_out (q itself: in place; None: a new tensor).  k, v, q: (tokens, heads,
+        dim); v None for a latent cache.  Returns q_out."""
+        n = _index_list(slots, "slots", True)
+        _heads(k, "k")
+        for x, what in ((v, "v"), (q, "q"), (q_out, "q_out")):
+            if x is not None and _heads(x, what, k).shape[0] != n:
+                raise ValueError(f"{what} has {x.shape[0]} rows for {n} slots")
+        if k.shape[0] != n:
+            raise ValueError(f"k has {k.shape[0]} rows for {n} slots")
+        if v is not None and v.shape[1] != k.shape[1]:
+            raise ValueError("k and v differ in heads")
+        if q is not None and q_out is None:
+            q_out = q.new_empty(q.shape)
+        if q is None and q_out is not None:
+            raise ValueError("q_out without q")
+        if q is not None and (q.shape != q_out.shape or q.shape[2] != k.shape[2]):
+            raise ValueError("q, q_out and k must agree in heads and head_dim")
+        if rope is not None and _index_list(positions, "positions", True) != n:
+            raise ValueError("positions and slots differ in length")
+        pair = _I64 * 2
+        none = pair(0, 0)
+        d = hc_store_desc(layer, _DTYPES[str(k.dtype)], 0 if q is None else q.shape[1], k.shape[1], k.shape[2],
+                          0 if v is None else v.shape[2], n, _ptr(slots), _ptr(positions) if rope is not None else None,
+                          None if q is None else q.data_ptr(), None if q is None else q_out.data_ptr(), k.data_ptr(),
+                          None if v is None else v.data_ptr(), none if q is None else pair(*q.stride()[:2]),
+                          none if q is None else pair(*q_out.stride()[:2]), pair(*k.stride()[:2]),
+                          none if v is None else pair(*v.stride()[:2]), rope.handle if rope is not None else None)
+        s = _on(stream, k, slots, positions, q, q_out, v)
+        check(lib.hc_store_tokens(self.handle, ctypes.byref(d), s), "hc_store_tokens")
+        return q_out
+
+    def attend(self, layer: int, q, table, kv_len, *, kv_heads: int, q_start=None, max_q: int | None = None,
+               max_kv: int | None = None, entry_tokens: int | None = None, causal: bool = True, window: int = 0,
+               sinks: int = 0, scale: float | None = None, value_dim: int | None = None, out=None,
+               return_lse: bool = False, workspace=None, stream=None):
+        """Attention of q (rows, heads, head_dim) over the cached tokens of each sequence:
+        table (sequences, entries) of pages (entry_tokens: the pool's page_size, the default)
+        or slots (entry_tokens=1), kv_len cached tokens per sequence, q_start the first query
+        row of each sequence and the end of the last (None: one row each).  max_q, max_kv:
+        no sequence has more rows, or tokens (None: what q and the table hold).  value_dim
+        below head_dim: a latent cache, whose key rows hold the values.  scale None:
+        head_dim ** -0.5.  Returns (out, lse), lse None unless asked for."""
+        _heads(q, "q")
+        at, seqs, width, stride = _table(table, "table")
+        if _index_list(kv_len, "kv_len", True) != seqs:
+            raise ValueError("kv_len and table differ in sequences")
+        if q_start is not None and _index_list(q_start, "q_start", True) != seqs + 1:
+            raise ValueError("q_start must hold one entry more than there are sequences")
+        rows, heads, dim = q.shape
+        if out is None:
+            out = q.new_empty((rows, heads, dim if value_dim is None else value_dim))
+        elif _heads(out, "out", q).shape[:2] != (rows, heads):
+            raise ValueError("q and out differ in rows or heads")
+        elif value_dim is not None and out.shape[2] != value_dim:
+            raise ValueError("out is not value_dim wide")
+        entry = self.page_size if entry_tokens is None else entry_tokens
+        lse = q.new_empty((rows, heads), dtype=_torch().float32) if return_lse else None
+        pair = _I64 * 2
+        d = hc_attend_desc(layer, _DTYPES[str(q.dtype)], heads, kv_heads, dim, out.shape[2],
+                           1 if out.shape[2] != dim else 0, 1 if causal else 0, entry,
+                           dim ** -0.5 if scale is None else scale, window, sinks, seqs, rows,
+                           (1 if q_start is None else rows) if max_q is None else max_q,
+                           width * entry if max_kv is None else max_kv, width, stride, q.data_ptr(), out.data_ptr(),
+                           lse.data_ptr() if lse is not None else None,
+                           q_start.data_ptr() if q_start is not None else None, kv_len.data_ptr(), at,
+                           pair(*q.stride()[:2]), pair(*out.stride()[:2]))
+        if workspace is None:
+            need = _I64()
+            check(lib.hc_attend_workspace_bytes(self.handle, ctypes.byref(d), ctypes.byref(need)),
+                  "hc_attend_workspace_bytes")
+            if need.value:
+                workspace = q.new_empty(need.value, dtype=_torch().uint8)
+        if workspace is not None:
+            d.workspace, d.workspace_bytes = workspace.data_ptr(), _staging_bytes(workspace, "workspace")
+        s = _on(stream, q, table, kv_len, q_start, out, lse, workspace)
+        check(lib.hc_attend(self.handle, ctypes.byref(d), s), "hc_attend")
+        return out, lse
+
+    def copy_pages(self, src, dst, stream=None) -> None:
+        """Pages src[i] to pages dst[i], in every layer and sub-buffer."""
+        n = _index_list(src, "src", True)
+        if _index_list(dst, "dst", True) != n:
+            raise ValueError("src and dst differ in length")
+        s = _on(stream, src, dst)
+        check(lib.hc_copy_pages(self.handle, _V(_ptr(src)), _V(_ptr(dst)), n, s), "hc_copy_pages")
+
+    def fork_pages(self, table, lens, parents, free_pages, out, stream=None):
+        """Rows of `out` for children of the table rows `parents`: full pages shared, a partly
+        filled last page copied to the next of free_pages.  Returns the number of pages taken
+        (a one-element tensor)."""
+        at, rows, width, stride = _table(table, "table")
+        to, n, out_width, out_stride = _table(out, "out")
+        if _index_list(lens, "lens", True) != rows:
+            raise ValueError("lens and table differ in rows")
+        if _index_list(parents, "parents", True) != n or out_width != width:
+            raise ValueError("out must have a row per parent and the table's width")
+        n_free = _index_list(free_pages, "free_pages", True)
+        used = table.new_empty(1)
+        s = _on(stream, table, lens, parents, free_pages, out, used)
+        check(lib.hc_fork_pages(self.handle, _V(at), rows, width, stride, _V(_ptr(lens)), _V(_ptr(parents)), n,
+                                _V(_ptr(free_pages)), n_free, _V(to), out_stride, _V(_ptr(used)), s), "hc_fork_pages")
+        return used
+
+    def _pages_workspace(self, table):
+        need = _I64()
+        check(lib.hc_pages_workspace_bytes(self.handle, ctypes.byref(need)), "hc_pages_workspace_bytes")
+        return table.new_empty(need.value, dtype=_torch().uint8)
+
+    def free_pages(self, table, lens, stream=None):
+        """(pages, count): the pages that no table row names, ascending, in the first count[0]
+        entries of `pages`."""
+        at, rows, width, stride = _table(table, "table")
+        if _index_list(lens, "lens", True) != rows:
+            raise ValueError("lens and table differ in rows")
+        pages, count = table.new_empty(self.desc.device_slots // self.page_size), table.new_empty(1)
+        work = self._pages_workspace(table)
+        s = _on(stream, table, lens, pages, count, work)
+        check(lib.hc_free_pages(self.handle, _V(at), rows, width, stride, _V(_ptr(lens)), _V(_ptr(pages)),
+                                _V(_ptr(count)), _V(_ptr(work)), work.numel(), s), "hc_free_pages")
+        return pages, count
+
+    def compact_pages(self, table, lens, out, stream=None):
+        """Packs the named pages to the front of the pool; `out` (which may be `table`) gets the
+        table with their new numbers.  Returns the number of live pages (a one-element tensor)."""
+        at, rows, width, stride = _table(table, "table")
+        to, out_rows, out_width, out_stride = _table(out, "out")
+        if _index_list(lens, "lens", True) != rows:
+            raise ValueError("lens and table differ in rows")
+        if (out_rows, out_width) != (rows, width):
+            raise ValueError("out must have the table's shape")
+        count, work = table.new_empty(1), self._pages_workspace(table)
+        s = _on(stream, table, lens, out, count, work)
+        check(lib.hc_compact_pages(self.handle, _V(at), rows, width, stride, _V(_ptr(lens)), _V(to), out_stride,
+                                   _V(_ptr(count)), _V(_ptr(work)), work.numel(), s), "hc_compact_pages")
+        return count
 
     def sync(self) -> None:
         check(lib.hc_pool_sync(self.handle), "hc_pool_sync")

@@ -131,6 +131,8 @@ struct hc_pool {
   double kind_ms[kKinds] = {};
   hc_pool_stats stats{};
   std::vector<int64_t> wg_load;       // [max_ctas] host scratch of the zero-copy launchers' tile sizing
+  std::vector<uint64_t> bases;        // [nsub][L] layer addresses (what d_tables holds)
+  std::atomic<bool> other_streams{false};  // forward-pass operators ran, on streams of the caller's choice
   int64_t row_bytes_per_layer = 0;    // sum of token-row sub-buffers' elem_bytes
   int64_t block_bytes_per_layer = 0;  // sum of page-block sub-buffers' elem_bytes
 };
@@ -413,8 +415,8 @@ int refuse_capture(const char* what, const char* why) {
 
 int no_host_pool() {
   return set_err(HC_ERR_INVALID,
-                 "the pool has no host pages (a device-only pool): only the layer exchange and the round-trip "
-                 "check run on it");
+                 "the pool has no host pages (a device-only pool): only the layer exchange, the round-trip "
+                 "check and the forward-pass operators run on it");
 }
 
 int record_event(void* ev, hipStream_t s) {
@@ -447,7 +449,7 @@ int hc_desc_check(const hc_pool_desc* desc) {
   if (desc->flags & ~(HC_FLAG_VALIDATE | HC_FLAG_PROFILE)) return set_err(HC_ERR_INVALID, "unknown flags");
   if (desc->max_ctas < 0 || desc->max_ctas > 65536) return set_err(HC_ERR_INVALID, "max_ctas must be in [0, 65536]");
   if (L.H == 0) {
-    // a device-only pool: the layer exchange and the round-trip check, no host transfers
+    // a device-only pool: the layer exchange, the round-trip check and the forward pass, no host transfers
     if (desc->host_base) return set_err(HC_ERR_INVALID, "a pool without host pages takes no host_base");
     if (desc->write_back_mode == HC_MODE_STAGED || desc->staging)
       return set_err(HC_ERR_INVALID, "a pool without host pages has no write-back: no staging, no HC_MODE_STAGED");
@@ -643,6 +645,7 @@ int hc_pool_create(const hc_pool_desc* desc, hc_pool** out) {
       hipMemsetAsync((uint8_t*)p->d_err + 8, 0xFF, 8, p->stream) != hipSuccess)
     return bail(set_err(HC_ERR_HIP, "initial copies failed"));
   if (hipStreamSynchronize(p->stream) != hipSuccess) return bail(set_err(HC_ERR_HIP, "stream sync failed"));
+  p->bases = std::move(tables);  // copied to the device above
   p->planner.reset(L);
   fill_geom(p);
   for (int b = 0; b < L.nsub; b++)
@@ -659,6 +662,15 @@ int hc_pool_destroy(hc_pool* p) {
   if (p->d_tables && stream_capturing(p))
     return refuse_capture("hc_pool_destroy", "it waits for the copy stream before freeing (nothing was freed)");
   int rc = HC_OK;
+  if (p->other_streams.load()) {
+    // forward-pass operators read the tables on streams this pool does not know
+    if (use_device(p) != HC_OK) return HC_ERR_HIP;
+    if (hipDeviceSynchronize() != hipSuccess) {
+      (void)hipGetLastError();
+      return set_err(HC_ERR_HIP, "the device could not be waited for (a stream of it may be capturing): nothing was "
+                                 "freed");
+    }
+  }
   if (p->stream || p->d_tables) {
     if (hipStreamSynchronize(p->stream) != hipSuccess) rc = set_err(HC_ERR_HIP, "stream sync failed in destroy");
   }
@@ -704,9 +716,10 @@ int hc_pool_sync(hc_pool* p) {
     HIP_TRY(hipStreamSynchronize(p->stream));
     p->stats.device_errors++;
     return set_err(HC_ERR_DEVICE,
-                   "device-side check flagged an index list (code %d:%s%s first flagged list position %llu)", e,
+                   "device-side check flagged an index list (code %d:%s%s%s first flagged list position %llu)", e,
                    (e & 1) ? " index out of range;" : "",
-                   (e & 2) ? " page-block rows not one whole device page;" : "", (unsigned long long)pos);
+                   (e & 2) ? " page-block rows not one whole device page;" : "",
+                   (e & 4) ? " a sequence's lengths out of bounds;" : "", (unsigned long long)pos);
   }
   return HC_OK;
 }
@@ -1233,6 +1246,53 @@ int graph_matches(const hc_pool* pool, const void* graph, void* const* events, i
                        "only its own events)",
                        l);
   return HC_OK;
+}
+
+void pool_view(const hc_pool* p, PoolView* out) {
+  out->geom = &p->geom;
+  out->bases = p->bases.data();
+  out->err = p->d_err;
+  out->device = p->device;
+  out->num_cus = p->num_cus;
+  out->pages = p->lay.S % p->lay.P == 0;
+}
+
+int pool_forward(hc_pool* p, void* stream, PoolView* out) {
+  int rc = use_device(p);
+  if (rc != HC_OK) return rc;
+  if (stream) {
+    hipDevice_t sd = -1;
+    if (hipStreamGetDevice((hipStream_t)stream, &sd) != hipSuccess) {
+      (void)hipGetLastError();
+      return set_error(HC_ERR_INVALID, "stream is not a valid stream");
+    }
+    if (sd != p->device)
+      return set_error(HC_ERR_INVALID, "stream belongs to device %d, the pool's device is %d", sd, p->device);
+  }
+  p->other_streams.store(true);
+  pool_view(p, out);
+  return HC_OK;
+}
+
+int check_buffer(const void* q, int64_t bytes, int32_t device, int32_t align, bool host_ok, const char* what) {
+  if (bytes == 0) return HC_OK;
+  if (!q) return set_error(HC_ERR_INVALID, "%s is null", what);
+  if ((uintptr_t)q % (uintptr_t)align != 0)
+    return set_error(HC_ERR_UNSUPPORTED, "%s must be %d-byte aligned", what, align);
+  hipPointerAttribute_t attr;
+  if (hipPointerGetAttributes(&attr, q) != hipSuccess) {
+    (void)hipGetLastError();
+    return set_error(HC_ERR_INVALID, "%s is not memory known to HIP", what);
+  }
+  if (attr.type == hipMemoryTypeDevice) {
+    if (attr.device != device)
+      return set_error(HC_ERR_INVALID, "%s is on device %d, the pool's device is %d", what, attr.device, device);
+  } else if (!host_ok || attr.type != hipMemoryTypeHost) {
+    return set_error(HC_ERR_INVALID, "%s must be device memory%s", what, host_ok ? " (or pinned host memory)" : "");
+  } else if (attr.devicePointer != q) {
+    return set_error(HC_ERR_INVALID, "%s: pinned host memory not mapped at its host address", what);
+  }
+  return check_extent(q, bytes, true, what);
 }
 
 void pool_hold(hc_pool* pool) { pool->users.fetch_add(1); }

@@ -85,6 +85,24 @@ void pool_release(hc_pool* pool);
 // `events` (L entries, in layer order); else HC_ERR_INVALID with a message.
 int graph_matches(const hc_pool* pool, const void* graph, void* const* events, int32_t L);
 
+// What the forward-pass operators (hc_forward.cpp) see of a pool.
+struct PoolView {
+  const Geom* geom;
+  const uint64_t* bases;  // host copy of the layer addresses, [nsub][L]
+  int32_t* err;           // the pool's device error word
+  int32_t device, num_cus;
+  bool pages;             // device_slots is a multiple of page_size
+};
+// Makes the pool's device current, checks that `stream` is one of its streams, and notes that
+// work other than the copy stream's reads the pool's tables (hc_pool_destroy then waits for
+// the device).
+int pool_forward(hc_pool* pool, void* stream, PoolView* out);
+// The same view without touching a device (size queries).
+void pool_view(const hc_pool* pool, PoolView* out);
+// `bytes` of device memory of `device` at q, `align`-byte aligned (HC_ERR_UNSUPPORTED
+// otherwise), inside one allocation; a list may be pinned host memory too.
+int check_buffer(const void* q, int64_t bytes, int32_t device, int32_t align, bool host_ok, const char* what);
+
 // Optional timing of one kernel launch: two timing events that the launch itself
 // stamps with the kernel's start and end (hipExtLaunchKernel), so timing adds no
 // marker packets to the stream.  Both null: untimed.

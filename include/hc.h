@@ -106,7 +106,8 @@ typedef enum hc_status {
   HC_ERR_HIP = -3,         /* a HIP runtime call failed (the message names it) */
   HC_ERR_NOMEM = -4,       /* the library could not allocate its own scratch */
   HC_ERR_DEVICE = -5,      /* a kernel flagged an index list: an out-of-range entry (always checked),
-                              or page-block rows that are not one whole device page (HC_FLAG_VALIDATE) */
+                              page-block rows that are not one whole device page (HC_FLAG_VALIDATE), or
+                              a sequence's lengths out of bounds */
   HC_ERR_BUSY = -6         /* host-to-host queue capacity exhausted; nothing was submitted */
 } hc_status;
 
@@ -162,9 +163,9 @@ typedef struct hc_pool_desc {
   int64_t device_slots; /* S token slots per layer (a multiple of P when a sub-buffer holds page blocks) */
   int64_t host_pages;   /* H pages (shards) in the host pool.  0 makes a device-only pool: host_base
                            and staging are NULL, write-back and load-back are refused, and only the
-                           layer exchange and the round-trip check run on it (a TP rank's view of
-                           every layer of its replicated device pool, next to the pool of the host
-                           layers it owns) */
+                           layer exchange, the round-trip check and the forward-pass operators run on it
+                           (a TP rank's view of every layer of its replicated device pool, next to
+                           the pool of the host layers it owns) */
   int64_t shard_align;  /* shard layout: power of two >= 16 (4096 for Direct I/O); ignored otherwise */
   void* host_base;      /* pinned host memory (hc_host_alloc or hipHostMalloc), >= hc_host_pool_bytes */
   int64_t host_bytes;   /* size of host_base */
@@ -368,6 +369,210 @@ int hc_layer_pack(hc_pool* pool, int32_t layer, const int64_t* device_idx, int64
                   int64_t dst_bytes, void* event);
 int hc_layer_unpack(hc_pool* pool, int32_t layer, const void* src, int64_t src_bytes,
                     const int64_t* device_idx, int64_t n, void* event);
+
+/* ---------------------------------------------------------------- forward pass on the device pool
+ * What a forward pass does with the device pool between a load-back and the next
+ * write-back: new tokens' keys and values are rotated and stored in their slots,
+ * a chunk of new tokens attends over its sequence's cached tokens, and the pages
+ * of sequences are shared, copied, packed and found free.
+ *
+ * The calls take a stream of the pool's device (NULL: the null stream): they run
+ * beside the copy stream, and a caller orders the two with events (a load-back's
+ * layer event before hc_attend reads the layer, an event after hc_store_tokens
+ * before a write-back reads it).  They enqueue and return, allocate nothing, wait
+ * for nothing, and may be recorded into a caller's HIP graph; a replay reads every
+ * buffer as it is when it runs.  hc_pool_stats and hc_pool_kernel_time do not count
+ * them.  hc_pool_destroy waits for the whole device once one of them has run, and a
+ * graph that recorded one must not be replayed after it.
+ *
+ * Every buffer is device memory of the pool's device, lists and tables may also be
+ * pinned host memory, and the memory is checked before any launch like the transfer
+ * calls' lists.  What only the device can see (slots, table entries, lengths) is
+ * range-checked by the kernels: a bad one is skipped as stated at each call and
+ * reported as HC_ERR_DEVICE by an hc_pool_sync after the stream has passed the call.
+ *
+ * Two calls may run at once on two streams when neither writes what the other reads
+ * or writes; a workspace is written by the call that gets it, so calls that can run
+ * at once (two captured graphs among them) need their own.
+ *
+ * Elements are bf16 or fp16.  Sub-buffer 0 of the pool holds keys, a row of
+ * kv_heads * head_dim elements per token, sub-buffer 1 values, kv_heads * value_dim
+ * elements; both are token rows.  A latent cache (MLA) has one row per token that is
+ * key and value at once: kv_heads = 1, the value is the row's first value_dim
+ * elements, and sub-buffer 1 is not used (value_in_key, or value_dim = 0 when
+ * storing).  Other sub-buffers stay as they are. */
+enum { HC_BF16 = 0, HC_F16 = 1 };
+enum { HC_ROPE_NONE = 0, HC_ROPE_LINEAR = 1, HC_ROPE_LLAMA3 = 2, HC_ROPE_YARN = 3 };
+#define HC_MAX_ROT_DIM 256
+
+/* Rotary positions.  Pair i of rot_dim / 2 turns by position * f_i radians, with
+ * f_i = base^(-2 i / rot_dim) after scaling:
+ *   HC_ROPE_NONE    f_i
+ *   HC_ROPE_LINEAR  f_i / factor
+ *   HC_ROPE_LLAMA3  f_i where it makes more than high_freq_factor turns over
+ *                   original_context tokens, f_i / factor where it makes fewer than
+ *                   low_freq_factor, and a linear blend in the turns between
+ *   HC_ROPE_YARN    f_i up to pair lo, f_i / factor from pair hi, a linear blend
+ *                   between; lo and hi are the pairs that make beta_fast and beta_slow
+ *                   turns over original_context (rounded down and up, kept inside
+ *                   [0, rot_dim - 1]); sines and cosines times magnitude, which is
+ *                   0.1 ln(factor) + 1 when given as 0
+ * The pair's elements are rot_offset + i and rot_offset + rot_dim / 2 + i of a head,
+ * or with interleaved != 0 rot_offset + 2 i and the next; the head's other elements
+ * stay as they are.  (y1, y2) = magnitude * (x1 cos - x2 sin, x2 cos + x1 sin),
+ * computed in fp32 and rounded once; a position's angle is reduced to a fraction of
+ * a turn in 64-bit integers, so that far positions keep their precision.
+ *   rot_dim     a multiple of 16 up to HC_MAX_ROT_DIM; rot_offset a multiple of 8
+ *   base        > 1, factor > 0 (ignored by HC_ROPE_NONE), finite
+ *   magnitude   >= 0; 0 means the scaling's own (1 except for HC_ROPE_YARN)
+ * The handle holds numbers only (no device memory) and works on every device; a call
+ * copies what it needs, so the handle may be destroyed once the call has returned. */
+typedef struct hc_rope_desc {
+  int32_t rot_dim, rot_offset, interleaved, scaling;
+  double base, factor, low_freq_factor, high_freq_factor, beta_fast, beta_slow, magnitude;
+  int64_t original_context;
+} hc_rope_desc;
+typedef struct hc_rope hc_rope;
+int hc_rope_create(const hc_rope_desc* desc, hc_rope** out);
+int hc_rope_destroy(hc_rope* rope); /* NULL is a no-op */
+/* The scaled frequencies, radians per position of each pair (rot_dim / 2 values), and
+ * the factor on sines and cosines.  Host only. */
+int hc_rope_frequencies(const hc_rope* rope, double* out_frequencies, double* out_magnitude);
+
+/* Stores n new tokens in one layer of the pool: for token i < n
+ *   key row   [slots[i]] <- rope(k[i]) at positions[i]
+ *   value row [slots[i]] <- v[i], bit for bit
+ *   q_out[i]             <- rope(q[i]) at positions[i]
+ * Without a rope (NULL; positions ignored) keys and queries move bit for bit too.
+ *   slots      n int64, distinct; -1 marks a padding token: its rows and its q_out are
+ *              left as they were and nothing is reported.  Any other slot outside the
+ *              pool is skipped the same way and reported.
+ *   positions  n int64, any value.
+ *   q, q_out   queries of q_heads heads, or both NULL (q_heads 0).  q_out may be q itself
+ *              with the same strides (in place); otherwise inputs and outputs must not
+ *              overlap, nor k and v the pool's rows.
+ *   strides    in elements, of the token and of the head, >= 0 and multiples of 8; the
+ *              elements of a head are contiguous and every base address is 16-byte
+ *              aligned.  A stride of 0 (one token or head for all) is fine for inputs; the
+ *              heads of q_out must not overlap.
+ *   head_dim, value_dim  multiples of 8; value_dim 0: no value rows (a latent cache).
+ * kv_heads * head_dim and kv_heads * value_dim must be exactly the pool's rows. */
+typedef struct hc_store_desc {
+  int32_t layer, dtype;
+  int32_t q_heads, kv_heads, head_dim, value_dim;
+  int64_t n;
+  const int64_t* slots;
+  const int64_t* positions;
+  const void* q;
+  void* q_out;
+  const void* k;
+  const void* v;
+  int64_t q_stride[2], q_out_stride[2], k_stride[2], v_stride[2];
+  const hc_rope* rope;
+} hc_store_desc;
+int hc_store_tokens(hc_pool* pool, const hc_store_desc* desc, void* stream);
+
+/* Attention of a chunk of new tokens over the cached tokens of their sequences, in one
+ * layer.  Sequence s has query rows q_start[s] .. q_start[s + 1] - 1 of q and kv_len[s]
+ * cached tokens, the chunk's own among them (stored before this call); its query i of m
+ * stands at position p = kv_len[s] - m + i.  For each query head h, with KV head
+ * h / (q_heads / kv_heads):
+ *   out[row][h] = sum over visible j of softmax_j(scale * q . k_j) v_j
+ *   lse[row][h] = ln sum over visible j of exp(scale * q . k_j)
+ * Key j < kv_len[s] is visible when causal == 0, or j <= p and, with window > 0,
+ * p - j < window or j < sinks.  What stands in rows that a query does not see never
+ * reaches its output, infinities and NaN included.  A row that sees nothing (kv_len 0,
+ * or more new tokens than cached ones), or whose every visible score is -infinity, is
+ * zeros, its lse -infinity.
+ *   q_start    num_seqs + 1 int64, not decreasing, or NULL: one query row per sequence.
+ *              Rows of q behind the last sequence (a padded batch) leave out and lse as
+ *              they were.
+ *   kv_len     num_seqs int64.
+ *   table      where the tokens are: token j of sequence s is in slot
+ *              table[s * table_stride + j / entry_tokens] * entry_tokens + j % entry_tokens.
+ *              entry_tokens is 1 (token slots) or the pool's page_size (pages).  Entries
+ *              behind a sequence's last token are not read.
+ *   table_width  entries of a row.
+ *   max_q, max_kv  no sequence has more query rows, or more cached tokens, than this (the
+ *              launch is sized by them; max_kv <= table_width * entry_tokens).  A sequence
+ *              whose q_start or kv_len is out of these bounds is skipped, its rows left as
+ *              they were, and reported; a table entry outside the pool hides its tokens
+ *              and is reported.
+ *   head_dim, value_dim  64/64 or 128/128, or 576/512 with value_in_key and kv_heads = 1.
+ *   q_heads    a multiple of kv_heads; q_heads / kv_heads <= 128.
+ *   q, out     strides in elements of the row and of the head, as for hc_store_tokens.
+ *   lse        fp32 [q_rows][q_heads], contiguous, or NULL.
+ *   scale      finite.
+ *   workspace  hc_attend_workspace_bytes of device memory, 16-byte aligned; may be NULL
+ *              when that is 0.
+ * Scores, softmax statistics and sums are fp32; a probability is rounded to the element
+ * type once, as the operand of the product with the values, and the output once. */
+typedef struct hc_attend_desc {
+  int32_t layer, dtype;
+  int32_t q_heads, kv_heads, head_dim, value_dim;
+  int32_t value_in_key, causal;
+  int32_t entry_tokens;
+  float scale;
+  int64_t window, sinks;
+  int64_t num_seqs, q_rows, max_q, max_kv;
+  int64_t table_width, table_stride;
+  const void* q;
+  void* out;
+  float* lse;
+  const int64_t* q_start;
+  const int64_t* kv_len;
+  const int64_t* table;
+  int64_t q_stride[2], out_stride[2];
+  void* workspace;
+  int64_t workspace_bytes;
+} hc_attend_desc;
+/* Depends on the sizes in desc only (its pointers are not read). */
+int hc_attend_workspace_bytes(const hc_pool* pool, const hc_attend_desc* desc, int64_t* out_bytes);
+int hc_attend(hc_pool* pool, const hc_attend_desc* desc, void* stream);
+
+/* Page tables.  Row s of a table names the device pages (slots p * P .. p * P + P - 1 for
+ * page p < device_slots / P) of a sequence of lens[s] tokens: its first
+ * ceil(lens[s] / P) entries.  What stands behind them is not read.  Several rows may name
+ * one page.  A length outside [0, width * P], and an entry outside the pool, is reported;
+ * the row, or the entry, is then taken for empty (and copied as it is by
+ * hc_compact_pages).  The pool's device_slots must be a multiple of P.  Tables are read
+ * with a row stride of table_stride >= table_width entries.  Data moves bit for bit, in
+ * every layer and every sub-buffer (page blocks included). */
+
+/* Copies page src[i] to page dst[i], i < n.  The dst pages are distinct, and none of them is
+ * another pair's src (src[i] == dst[i] is allowed).  A pair with a page outside the pool is
+ * skipped and reported. */
+int hc_copy_pages(hc_pool* pool, const int64_t* src, const int64_t* dst, int64_t n, void* stream);
+
+/* Branches n new sequences off table rows: child i of row r = parents[i] gets the row's length
+ * and shares its full pages; when the last page is only partly filled, the child gets a page
+ * of its own, the next of free_pages in the order of the children, and the filled rows of the
+ * parent's page are copied to it (a page block as a whole).  out_table[i][0 .. table_width)
+ * is the child's row, -1 behind its pages; *used is the number of free pages the children need.
+ * A child that finds no free page left, or whose parent is out of range, is reported, its
+ * entry (its whole row) -1.  out_table and used must not overlap what is read. */
+int hc_fork_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64_t table_width, int64_t table_stride,
+                  const int64_t* lens, const int64_t* parents, int64_t n, const int64_t* free_pages, int64_t n_free,
+                  int64_t* out_table, int64_t out_stride, int64_t* used, void* stream);
+
+/* Device memory that the two calls below need as workspace (16-byte aligned). */
+int hc_pages_workspace_bytes(const hc_pool* pool, int64_t* out_bytes);
+
+/* Lists the pages that no table row names, ascending, in free_pages (room for
+ * device_slots / P entries; those behind the list stay as they were) and their number in
+ * *count. */
+int hc_free_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64_t table_width, int64_t table_stride,
+                  const int64_t* lens, int64_t* free_pages, int64_t* count, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
+/* Packs the pages that table rows name into pages 0 .. *count - 1: pages below *count stay
+ * where they are, and the k-th named page from *count on moves into the k-th unnamed page
+ * below it.  out_table (which may be table itself) is the table with the moved pages' new
+ * numbers; entries behind a row's length are copied as they are.  A page that has moved
+ * keeps its old bytes. */
+int hc_compact_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64_t table_width,
+                     int64_t table_stride, const int64_t* lens, int64_t* out_table, int64_t out_stride,
+                     int64_t* count, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- captured load-back bursts
  * The per-layer load-back chain of one burst, captured once into a HIP graph on
