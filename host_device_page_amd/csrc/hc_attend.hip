@@ -21,17 +21,26 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 struct Bf16 {
   typedef __bf16 elem;
   typedef bf16x8 v8;
+  static __device__ __forceinline__ f32x4 mfma16(v8 a, v8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
 };
 struct F16 {
   typedef _Float16 elem;
   typedef f16x8 v8;
+  static __device__ __forceinline__ f32x4 mfma16(v8 a, v8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
 };
 
 __device__ __forceinline__ void flag(int32_t* err, int bit, int64_t pos) {
@@ -41,29 +50,30 @@ __device__ __forceinline__ void flag(int32_t* err, int bit, int64_t pos) {
 
 // A sequence's rows and cached tokens; ok only when they are inside the call's bounds.
 struct Seq {
-  int64_t q0, kv;
-  int64_t m;
+  int64_t q0;
+  int kv, m;
   bool ok;
 };
 __device__ __forceinline__ Seq sequence(const AttendArgs& a, int64_t s) {
   Seq r;
   r.q0 = a.q_start ? a.q_start[s] : s;
   const int64_t q1 = a.q_start ? a.q_start[s + 1] : s + 1;
-  r.kv = a.kv_len[s];
-  r.m = q1 - r.q0;
-  r.ok = r.q0 >= 0 && r.m >= 0 && q1 <= a.q_rows && r.m <= a.max_q && r.kv >= 0 && r.kv <= a.max_kv;
+  const int64_t kv = a.kv_len[s];
+  r.ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= a.q_rows && q1 - r.q0 <= a.max_q && kv >= 0 && kv <= a.max_kv;
+  r.kv = r.ok ? (int)kv : 0;
+  r.m = r.ok ? (int)(q1 - r.q0) : 0;
   return r;
 }
 
 // The keys that rows at positions [p0, p1] can see, as a list: i < sk is key i, others key
-// lo + i - sk.
+// lo + i - sk.  Rows, keys and positions are below 2^30 in size, so 32 bits hold them.
 struct Span {
-  int64_t lo, sk, n;
-  __device__ __forceinline__ int64_t key(int64_t i) const { return i < sk ? i : lo + (i - sk); }
+  int lo, sk, n;
+  __device__ __forceinline__ int key(int i) const { return i < sk ? i : lo + (i - sk); }
 };
-__device__ __forceinline__ Span span_of(const AttendArgs& a, int64_t kv, int64_t p0, int64_t p1) {
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int kv, int p0, int p1) {
   Span s;
-  int64_t hi = kv;
+  int hi = kv;
   s.lo = 0;
   if (a.causal) {
     hi = p1 + 1 < kv ? p1 + 1 : kv;
@@ -75,23 +85,543 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int64_t kv, int64_t
   s.n = s.sk + hi - s.lo;
   return s;
 }
-__device__ __forceinline__ bool visible(const AttendArgs& a, int64_t p, int64_t j) {
-  if (!a.causal) return true;
-  return j <= p && (a.window == 0 || p - j < a.window || j < a.sinks);
+__device__ __forceinline__ bool visible(const AttendArgs& a, int p, int j) {
+  return !a.causal | ((j <= p) & ((a.window == 0) | (p - j < a.window) | (j < a.sinks)));
 }
 
-// Slot of key j, -1 for a bad table entry.
-__device__ __forceinline__ int64_t slot_of(const AttendArgs& a, int64_t s, int64_t j) {
-  const int64_t e = j / a.entry;
+constexpr uint32_t kNoSlot = 0xffffffffu;  // layers hold fewer rows: 2^32 of the smallest are 512 GiB
+
+// Slot of key j (below 2^31) of sequence s; kNoSlot for a bad table entry, which is reported.
+__device__ __forceinline__ uint32_t slot_of(const AttendArgs& a, int64_t s, uint32_t j) {
+  const uint32_t e = (uint32_t)(((uint64_t)j * a.entry_magic) >> a.entry_shift);  // j / entry
   const int64_t t = a.table[s * a.table_stride + e];
-  if (t < 0 || t >= a.S / a.entry) {
+  if (t < 0 || t >= a.entries) {
     flag(a.err, kErrIndex, s * a.table_stride + e);
-    return -1;
+    return kNoSlot;
   }
-  return t * a.entry + (j - e * a.entry);
+  return (uint32_t)(t * a.entry + (j - e * (uint32_t)a.entry));
 }
 
-// One wave per (row, head): lanes take keys for the scores and dims for the sum.
+// ---------------------------------------------------------------- one row, key by key
+// Softmax sums of one query row over positions [i0, i1) of its span, by one wave: lanes take keys
+// for the scores and dims for the sum, and nothing of a key that the row does not see is touched.
+// The tiled kernels multiply hidden keys' values by a weight of 0, which is NaN where the value is
+// not finite; they do the rows that came out NaN again with this.  s_q: DK floats of this wave's.
+template <class T, int DK, int DV>
+__device__ __forceinline__ void exact_row(const AttendArgs& a, int64_t s, int64_t row, int h, int p, Span span,
+                                       int i0, int i1, float* s_q, float* o, float* m_out, float* l_out) {
+  typedef typename T::elem elem;
+  const int lane = threadIdx.x & 63;
+  const int hk = h / a.group;
+  const elem* qp = reinterpret_cast<const elem*>(a.q) + row * a.q_stride[0] + h * a.q_stride[1];
+  __builtin_amdgcn_wave_barrier();
+  for (int i = lane; i < DK; i += 64) s_q[i] = (float)qp[i];
+  __builtin_amdgcn_wave_barrier();
+  constexpr int ND = DV / 64;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int c = 0; c < ND; c++) o[c] = 0.f;
+  const float scale = a.scale * kLog2e;
+  for (int base = i0; base < i1; base += 64) {
+    const int i = base + lane;
+    float x = -INFINITY;
+    uint32_t slot = kNoSlot;
+    if (i < i1) {
+      const int j = span.key(i);
+      if (visible(a, p, j)) slot = slot_of(a, s, (uint32_t)j);
+    }
+    if (slot != kNoSlot) {
+      const v4u* kp = reinterpret_cast<const v4u*>(a.k_rows + 2 * ((int64_t)slot * a.k_row + (int64_t)hk * DK));
+      x = 0.f;
+      for (int v = 0; v < DK / 8; v++) {
+        const f32x8 kv = __builtin_convertvector(__builtin_bit_cast(typename T::v8, kp[v]), f32x8);
+#pragma unroll
+        for (int c = 0; c < 8; c++) x += kv[c] * s_q[v * 8 + c];
+      }
+      x *= scale;
+    }
+    float top = x;
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    // a score that is NaN is not a maximum, and makes the sums NaN
+    const float next = fmaxf(m, top);
+    const float zero = next == -INFINITY ? 0.f : next;
+    const float keep = exp2f(m - zero), e = slot != kNoSlot ? exp2f(x - zero) : 0.f;
+    m = next;
+    float sum = e;
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    l = l * keep + sum;
+#pragma unroll
+    for (int c = 0; c < ND; c++) o[c] *= keep;
+    uint64_t todo = __ballot(slot != kNoSlot);
+    while (todo) {
+      const int j = __builtin_ctzll(todo);
+      todo &= todo - 1;
+      const float pj = __shfl(e, j);
+      const uint32_t sj = __shfl(slot, j);
+      const elem* vp = reinterpret_cast<const elem*>(a.v_rows) + (int64_t)sj * a.v_row + (int64_t)hk * (DK == DV ? DV : 0);
+#pragma unroll
+      for (int c = 0; c < ND; c++) o[c] += pj * (float)vp[c * 64 + lane];
+    }
+  }
+  *m_out = m;
+  *l_out = l;
+}
+
+// ---------------------------------------------------------------- the list of work items
+// A sequence's query rows times the heads of a KV head's group make row lists of m * group rows,
+// row r being token r / group and head r % group of the group; R rows make a row tile.  An item is
+// (sequence, KV head, row tile, split): `splits` items share a tile's keys.  Every workgroup works
+// out the list for itself from the lengths, so that its number of items follows the lengths as
+// they are on the device: a sequence gets a split per C keys, C being the whole call's keys over
+// the wanted number of items.
+struct Item {
+  int64_t s;
+  Seq q;
+  int32_t hk, tile, split, splits;
+  int64_t index;  // place in the list: where its partial result lies
+};
+
+struct PlanCount {
+  int64_t tiles, n;  // row tiles of the sequence, positions of the span of all its rows
+};
+__device__ __forceinline__ PlanCount plan_count(const AttendArgs& a, int64_t s, int R, Seq* q) {
+  *q = sequence(a, s);
+  PlanCount c = {0, 0};
+  if (!q->ok || q->m == 0) return c;
+  c.tiles = ((int64_t)q->m * a.group + R - 1) / R;
+  c.n = span_of(a, q->kv, q->kv - q->m, q->kv - 1).n;
+  return c;
+}
+
+__device__ __forceinline__ int64_t wave_prefix(int64_t x) {  // inclusive
+  const int lane = threadIdx.x & 63;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// Finds item `want` of the list (256 threads; s_plan: 8 int64); false when the list is shorter.
+__device__ bool find_item(const AttendArgs& a, int R, int64_t want, int64_t* s_plan, Item* it) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t work = 0;
+  Seq q;
+  for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
+    const PlanCount c = plan_count(a, s, R, &q);
+    if (blockIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
+    work += c.tiles * c.n;
+  }
+  for (int d = 1; d < 64; d <<= 1) work += __shfl_xor(work, d);
+  if (lane == 0) s_plan[wave] = work;
+  __syncthreads();
+  work = (s_plan[0] + s_plan[1] + s_plan[2] + s_plan[3]) * a.kv_heads;
+  int64_t C = (work + a.target - 1) / a.target;
+  C = C < a.min_split ? a.min_split : C;
+  int64_t before = 0;
+  bool found = false;
+  for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 256) {
+    const int64_t s = s0 + threadIdx.x;
+    PlanCount c = {0, 0};
+    if (s < a.num_seqs) c = plan_count(a, s, R, &q);
+    const int64_t splits = c.n <= C ? 1 : (c.n + C - 1) / C;
+    const int64_t mine = c.tiles * splits * a.kv_heads;
+    const int64_t incl = wave_prefix(mine);
+    __syncthreads();
+    if (lane == 63) s_plan[4 + wave] = incl;
+    __syncthreads();
+    int64_t at = before + incl - mine;
+    for (int w = 0; w < wave; w++) at += s_plan[4 + w];
+    for (int w = 0; w < 4; w++) before += s_plan[4 + w];
+    if (want >= at && want < at + mine) {
+      s_plan[0] = s;
+      s_plan[1] = splits;
+      s_plan[2] = want - at;
+      s_plan[3] = c.tiles;
+    }
+    if (want < before) {
+      found = true;
+      break;
+    }
+  }
+  __syncthreads();
+  if (!found) return false;
+  it->s = s_plan[0];
+  it->splits = (int32_t)s_plan[1];
+  const int64_t rest = s_plan[2];
+  const int64_t unit = rest / it->splits;
+  it->split = (int32_t)(rest - unit * it->splits);
+  it->tile = (int32_t)(unit / a.kv_heads);
+  it->hk = (int32_t)(unit - (int64_t)it->tile * a.kv_heads);
+  it->q = sequence(a, it->s);
+  it->index = want;
+  __syncthreads();
+  return true;
+}
+
+// Floats of a partial result: per row the sum over values, then maximum and sum of weights.
+template <int DV>
+__host__ __device__ constexpr int64_t partial_floats(int R) {
+  return (int64_t)R * (DV + 2);
+}
+
+// ---------------------------------------------------------------- few rows: decoding
+// Rows: up to 16 (token, head) pairs of one KV head, so K and V are read once for all of them.
+// What bounds it is memory: 2 * 16 * D operations on 4 * D bytes of a key.  So a wave works alone
+// on tiles of 32 keys, rows of K straight from memory into the operand registers of the
+// product, the next tile's K and V on their way while one is computed, and waves and splits are
+// joined only at the end.
+//
+//   S^T = K Q^T   (A: 16 keys, B: 16 rows): a lane ends with one row's scores of 8 of the 32 keys,
+//                 keys 16 t + 4 (lane / 16) + r, so a row's maximum and sum need two lane swaps
+//   O^T += V^T P^T (B: the same lane's 8 weights as they stand): the order of the keys inside the
+//                 product is free, so V^T is read in that order: V goes through LDS and comes
+//                 back transposed, four keys of a dim a lane
+constexpr int kRowTile = 16;
+constexpr int kKeys = 32;
+
+template <int D>
+__device__ __forceinline__ int v_swizzle(int row) {  // 16-byte chunks of a V row change places by its row:
+  return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3);  // the transposing reads then spread over all banks
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
+  typedef typename T::v8 v8;
+  typedef typename T::elem elem;
+  constexpr int KS = D / 32;            // product steps over the head
+  constexpr int DT = D / 16;            // 16-dim tiles of the output
+  constexpr int CH = D / 8;             // 16-byte chunks of a row
+  constexpr int VL = kKeys * CH / 64;   // V loads of a lane
+  __shared__ __align__(16) uint8_t s_v[4][kKeys * D * 2];
+  __shared__ float s_m[4][kRowTile], s_l[4][kRowTile];
+  __shared__ int64_t s_plan[8];
+  Item it;
+  if (!find_item(a, kRowTile, blockIdx.x, s_plan, &it)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = lane & 15, quad = lane >> 4;
+  const int rows_all = it.q.m * a.group;
+  const int r0 = it.tile * kRowTile;
+  const int rows = rows_all - r0 < kRowTile ? rows_all - r0 : kRowTile;
+  // this lane's row
+  const int r = r0 + (col < rows ? col : 0);
+  const int tok = r / a.group, h = it.hk * a.group + (r - tok * a.group);
+  const int64_t row = it.q.q0 + tok;
+  const int p = it.q.kv - it.q.m + tok;
+  const int p_first = it.q.kv - it.q.m + r0 / a.group, p_last = it.q.kv - it.q.m + (r0 + rows - 1) / a.group;
+  const Span span = span_of(a, it.q.kv, p_first, p_last);
+  // this split's part of the span
+  const int part = ((span.n + it.splits - 1) / it.splits + 127) / 128 * 128;
+  const int i0 = (int64_t)it.split * part < span.n ? it.split * part : span.n;
+  const int i1 = i0 + part < span.n ? i0 + part : span.n;
+  v8 q[KS];
+  {
+    const v4u* qp = reinterpret_cast<const v4u*>(a.q + 2 * (row * a.q_stride[0] + h * a.q_stride[1]));
+#pragma unroll
+    for (int i = 0; i < KS; i++) {
+      const v4u x = qp[i * 4 + quad];
+      q[i] = __builtin_bit_cast(v8, col < rows ? x : v4u{0, 0, 0, 0});
+    }
+  }
+  f32x4 o[DT] = {};
+  float m = -INFINITY, l = 0.f;
+  const float scale = a.scale * kLog2e;
+  const uint8_t* kb = a.k_rows + 2 * (int64_t)it.hk * D;
+  const uint8_t* vb = a.v_rows + 2 * (int64_t)it.hk * D;
+  const uint64_t k_row = 2 * a.k_row, v_row = 2 * a.v_row;
+  uint8_t* sv = s_v[wave];
+  // Slot of the tile's key lane % 32, kNoSlot past the end and for a key that no row sees: with one
+  // token a tile (decoding) that is every hidden key, whose values then are zeros in the product.
+  auto slots = [&](int base) {
+    const int i = base + (lane & 31);
+    if (i >= i1) return kNoSlot;
+    const int j = span.key(i);
+    if (p_first == p_last && !visible(a, p_first, j)) return kNoSlot;
+    return slot_of(a, it.s, (uint32_t)j);
+  };
+  v4u kreg[2][KS], vreg[VL];
+  auto load_k = [&](uint32_t slot) {
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      const uint32_t sl = __shfl(slot, t * 16 + col);
+      const v4u* kp = reinterpret_cast<const v4u*>(kb + (sl == kNoSlot ? 0 : sl * k_row));
+#pragma unroll
+      for (int i = 0; i < KS; i++) kreg[t][i] = kp[i * 4 + quad];
+    }
+  };
+  auto load_v = [&](uint32_t slot) {
+#pragma unroll
+    for (int c = 0; c < VL; c++) {
+      const int x = c * 64 + lane;
+      const uint32_t sl = __shfl(slot, x / CH);
+      const v4u y = *reinterpret_cast<const v4u*>(vb + (sl == kNoSlot ? 0 : sl * v_row) + (x % CH) * 16);
+      vreg[c] = sl == kNoSlot ? v4u{0, 0, 0, 0} : y;
+    }
+  };
+  int base = i0 + wave * kKeys;
+  uint32_t slot = base < i1 ? slots(base) : kNoSlot;
+  uint32_t slot_next = base + 128 < i1 ? slots(base + 128) : kNoSlot;
+  if (base < i1) {
+    load_k(slot);
+    load_v(slot);
+  }
+  for (; base < i1; base += 128) {
+    f32x4 st[2] = {};
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+      for (int i = 0; i < KS; i++) st[t] = T::mfma16(__builtin_bit_cast(v8, kreg[t][i]), q[i], st[t]);
+    const uint32_t there = (uint32_t)__ballot(slot != kNoSlot);
+    const bool more = base + 128 < i1;
+    if (more) load_k(slot_next);
+    const uint32_t slot_after = base + 256 < i1 ? slots(base + 256) : kNoSlot;
+    // V into LDS, and the next tile's on its way
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int c = 0; c < VL; c++) {
+      const int x = c * 64 + lane, key = x / CH;
+      *reinterpret_cast<v4u*>(sv + key * D * 2 + ((x % CH) ^ v_swizzle<D>(key)) * 16) = vreg[c];
+    }
+    if (more) load_v(slot_next);
+    // hidden keys: past the end, bad entries, and those that this row does not see
+    const bool whole = there == 0xffffffffu &&
+                       (!a.causal || (span.key(base + kKeys - 1) <= p_first &&
+                                      (a.window == 0 || p_last - span.key(base) < a.window)));
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) x[e] = st[e / 4][e % 4] * scale;
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const int k = (e / 4) * 16 + quad * 4 + e % 4;
+        const bool sees = ((there >> k) & 1) & visible(a, p, span.key(base + k));
+        x[e] = sees ? x[e] : -INFINITY;
+      }
+    }
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; e++) top = fmaxf(top, x[e]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float next = fmaxf(m, top);
+    const float zero = next == -INFINITY ? 0.f : next;
+    const float keep = __builtin_amdgcn_exp2f(m - zero);
+    m = next;
+    float sum = 0.f;
+    f32x8 w;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      w[e] = __builtin_amdgcn_exp2f(x[e] - zero);
+      sum += w[e];
+    }
+    l = l * keep + sum;  // this lane's keys; the quads are summed at the end
+    const v8 wt = __builtin_convertvector(w, v8);  // the weight's one rounding, as the product's operand
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int d = 0; d < DT; d++) {
+      s16x4 v[2];
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        const int key = t * 16 + quad * 4 + col / 4;
+        const int chunk = (d * 2 + (col & 3) / 2) ^ v_swizzle<D>(key);
+        v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(sv + key * D * 2 + chunk * 16 + (col & 1) * 8));
+      }
+      const v8 vt = __builtin_bit_cast(v8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      o[d] *= keep;
+      o[d] = T::mfma16(vt, wt, o[d]);
+    }
+    slot = slot_next;
+    slot_next = slot_after;
+  }
+  // Join the four waves: sums over values into LDS (over V, which is done with), 4 waves' of a row
+  // tile at a time in two halves of the dims.
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (lane < kRowTile) {
+    s_m[wave][lane] = m;
+    s_l[wave][lane] = l;
+  }
+  __syncthreads();
+  float m_all = s_m[0][col];
+  for (int w = 1; w < 4; w++) m_all = fmaxf(m_all, s_m[w][col]);
+  const float zero = m_all == -INFINITY ? 0.f : m_all;
+  float l_all = 0.f;
+  for (int w = 0; w < 4; w++) l_all += s_l[w][col] * __builtin_amdgcn_exp2f(s_m[w][col] - zero);
+  const float mine = __builtin_amdgcn_exp2f(m - zero);
+  // s_v holds [wave][16 rows][D] floats in halves of D/2 dims: 4 * 16 * D/2 * 4 bytes
+  float* so = reinterpret_cast<float*>(&s_v[0][0]);
+  constexpr int H = D / 2;
+  float acc[2][kRowTile * H / 256];
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    if (half) __syncthreads();
+#pragma unroll
+    for (int d = 0; d < DT / 2; d++)
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        so[(wave * kRowTile + col) * H + d * 16 + quad * 4 + e] = o[half * (DT / 2) + d][e] * mine;
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kRowTile * H / 256; c++) {
+      const int x = c * 256 + threadIdx.x;
+      acc[half][c] = so[x] + so[x + kRowTile * H] + so[x + 2 * kRowTile * H] + so[x + 3 * kRowTile * H];
+    }
+  }
+  // rows that came out NaN, one bit each
+  __syncthreads();
+  uint32_t* s_nan = reinterpret_cast<uint32_t*>(&s_v[0][0]);
+  if (threadIdx.x == 0) *s_nan = 0;
+  if (wave == 0 && lane < kRowTile) {
+    s_m[0][lane] = m_all;
+    s_l[0][lane] = l_all;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int half = 0; half < 2; half++)
+#pragma unroll
+    for (int c = 0; c < kRowTile * H / 256; c++)
+      if (acc[half][c] != acc[half][c]) atomicOr(s_nan, 1u << ((c * 256 + threadIdx.x) / H));
+  __syncthreads();
+  const uint32_t nan = *s_nan;
+  float* part_o = a.work + it.index * partial_floats<D>(kRowTile);
+  float* part_ml = part_o + kRowTile * D;
+#pragma unroll
+  for (int half = 0; half < 2; half++)
+#pragma unroll
+    for (int c = 0; c < kRowTile * H / 256; c++) {
+      const int x = c * 256 + threadIdx.x, rr = x / H, dim = half * H + x % H;
+      if (rr >= rows || ((nan >> rr) & 1)) continue;
+      if (it.splits > 1) {
+        part_o[rr * D + dim] = acc[half][c];
+      } else {
+        const int rt = (r0 + rr) / a.group, rh = it.hk * a.group + (r0 + rr - rt * a.group);
+        const float ll = s_l[0][rr];
+        reinterpret_cast<elem*>(a.out)[(it.q.q0 + rt) * a.out_stride[0] + rh * a.out_stride[1] + dim] =
+            (elem)(ll == 0.f ? 0.f : acc[half][c] / ll);
+      }
+    }
+  auto finish = [&](int rr, float mm, float ll) {
+    if (it.splits > 1) {
+      part_ml[rr * 2] = mm;
+      part_ml[rr * 2 + 1] = ll;
+    } else if (a.lse) {
+      const int rt = (r0 + rr) / a.group, rh = it.hk * a.group + (r0 + rr - rt * a.group);
+      a.lse[(it.q.q0 + rt) * a.q_heads + rh] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    }
+  };
+  if ((int)threadIdx.x < rows && !((nan >> threadIdx.x) & 1)) finish(threadIdx.x, s_m[0][threadIdx.x], s_l[0][threadIdx.x]);
+  if (nan) {
+    __syncthreads();  // s_nan is read; LDS is free
+    float* s_q = reinterpret_cast<float*>(s_v[wave]);
+    for (int rr = wave; rr < rows; rr += 4) {
+      if (!((nan >> rr) & 1)) continue;
+      const int rt = (r0 + rr) / a.group, rh = it.hk * a.group + (r0 + rr - rt * a.group);
+      float oo[D / 64], mm, ll;
+      exact_row<T, D, D>(a, it.s, it.q.q0 + rt, rh, it.q.kv - it.q.m + rt, span, i0, i1, s_q, oo, &mm, &ll);
+      for (int c = 0; c < D / 64; c++) {
+        if (it.splits > 1)
+          part_o[rr * D + c * 64 + lane] = oo[c];
+        else
+          reinterpret_cast<elem*>(a.out)[(it.q.q0 + rt) * a.out_stride[0] + rh * a.out_stride[1] + c * 64 + lane] =
+              (elem)(ll == 0.f ? 0.f : oo[c] / ll);
+      }
+      if (lane == 0) finish(rr, mm, ll);
+    }
+  }
+}
+
+// Joins the splits of a row tile: one wave per row.  Workgroups of tiles that were not split have
+// nothing to do.
+template <class T, int DV, int R>
+__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+  typedef typename T::elem elem;
+  __shared__ int64_t s_plan[8];
+  // item `splits * tile` of the list is found by walking tiles instead of items
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t work = 0;
+  Seq q;
+  for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
+    const PlanCount c = plan_count(a, s, R, &q);
+    work += c.tiles * c.n;
+  }
+  for (int d = 1; d < 64; d <<= 1) work += __shfl_xor(work, d);
+  if (lane == 0) s_plan[wave] = work;
+  __syncthreads();
+  work = (s_plan[0] + s_plan[1] + s_plan[2] + s_plan[3]) * a.kv_heads;
+  int64_t C = (work + a.target - 1) / a.target;
+  C = C < a.min_split ? a.min_split : C;
+  const int64_t want = blockIdx.x / (R / 4);  // a workgroup does four rows of a tile
+  int64_t tiles = 0, items = 0;
+  bool found = false;
+  for (int64_t s0 = 0; s0 < a.num_seqs && !found; s0 += 256) {
+    const int64_t s = s0 + threadIdx.x;
+    PlanCount c = {0, 0};
+    if (s < a.num_seqs) c = plan_count(a, s, R, &q);
+    const int64_t splits = c.n <= C ? 1 : (c.n + C - 1) / C;
+    const int64_t mine = c.tiles * a.kv_heads;
+    const int64_t t_incl = wave_prefix(mine), i_incl = wave_prefix(mine * splits);
+    __syncthreads();
+    if (lane == 63) {
+      s_plan[wave] = t_incl;
+      s_plan[4 + wave] = i_incl;
+    }
+    __syncthreads();
+    int64_t t_at = tiles + t_incl - mine, i_at = items + i_incl - mine * splits;
+    for (int w = 0; w < wave; w++) {
+      t_at += s_plan[w];
+      i_at += s_plan[4 + w];
+    }
+    for (int w = 0; w < 4; w++) {
+      tiles += s_plan[w];
+      items += s_plan[4 + w];
+    }
+    __syncthreads();
+    if (want >= t_at && want < t_at + mine) {
+      s_plan[0] = s;
+      s_plan[1] = splits;
+      s_plan[2] = want - t_at;
+      s_plan[3] = i_at;
+    }
+    found = want < tiles;
+  }
+  __syncthreads();
+  if (!found) return;
+  const int64_t s = s_plan[0], splits = s_plan[1], unit = s_plan[2];
+  if (splits <= 1) return;
+  const int64_t first = s_plan[3] + unit * splits;
+  // a q_start that goes back (reported) can make more items than the call has room for
+  if (first + splits > a.items) return;
+  q = sequence(a, s);
+  const int64_t tile = unit / a.kv_heads;
+  const int hk = (int)(unit - tile * a.kv_heads);
+  const int rr = (int)(blockIdx.x % (R / 4)) * 4 + wave;
+  const int64_t r = tile * R + rr;
+  if (r >= (int64_t)q.m * a.group) return;
+  constexpr int ND = DV / 64;
+  float m = -INFINITY, l = 0.f, o[ND] = {};
+  for (int64_t k = 0; k < splits; k++) {
+    const float* po = a.work + (first + k) * partial_floats<DV>(R);
+    const float pm = po[R * DV + rr * 2], pl = po[R * DV + rr * 2 + 1];
+    float v[ND];
+#pragma unroll
+    for (int c = 0; c < ND; c++) v[c] = po[rr * DV + c * 64 + lane];
+    const float next = fmaxf(m, pm);
+    const float zero = next == -INFINITY ? 0.f : next;
+    const float keep = __builtin_amdgcn_exp2f(m - zero), add = __builtin_amdgcn_exp2f(pm - zero);
+    m = next;
+    l = l * keep + pl * add;
+#pragma unroll
+    for (int c = 0; c < ND; c++) o[c] = o[c] * keep + v[c] * add;
+  }
+  const int64_t rt = r / a.group;
+  const int h = hk * a.group + (int)(r - rt * a.group);
+  elem* op = reinterpret_cast<elem*>(a.out) + (q.q0 + rt) * a.out_stride[0] + h * a.out_stride[1];
+#pragma unroll
+  for (int c = 0; c < ND; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
+  if (a.lse && lane == 0) a.lse[(q.q0 + rt) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- any call, one wave per (row, head)
 template <class T, int DK, int DV>
 __global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
   __shared__ float s_q[4][DK];
@@ -115,69 +645,56 @@ __global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
   if (s >= a.num_seqs) return;
   const Seq q = sequence(a, s);
   if (!q.ok || row < q.q0 || row >= q.q0 + q.m) return;
-  const int64_t p = q.kv - q.m + (row - q.q0);
+  const int p = q.kv - q.m + (int)(row - q.q0);
   const Span span = span_of(a, q.kv, p, p);
-  const int hk = h / a.group;
   typedef typename T::elem elem;
-  const elem* qp = reinterpret_cast<const elem*>(a.q) + row * a.q_stride[0] + h * a.q_stride[1];
-  for (int i = lane; i < DK; i += 64) s_q[wave][i] = (float)qp[i];
-  __builtin_amdgcn_wave_barrier();
-  constexpr int ND = DV / 64;
-  float o[ND] = {}, m = -INFINITY, l = 0.f;
-  const float scale = a.scale * kLog2e;
-  for (int64_t i0 = 0; i0 < span.n; i0 += 64) {
-    const int64_t i = i0 + lane;
-    float x = -INFINITY;
-    int64_t slot = -1;
-    if (i < span.n) {
-      const int64_t j = span.key(i);
-      if (visible(a, p, j)) slot = slot_of(a, s, j);
-    }
-    if (slot >= 0) {
-      const v4u* kp = reinterpret_cast<const v4u*>(a.k_rows + 2 * (slot * a.k_row + (int64_t)hk * DK));
-      x = 0.f;
-      for (int v = 0; v < DK / 8; v++) {
-        const f32x8 kv = __builtin_convertvector(__builtin_bit_cast(typename T::v8, kp[v]), f32x8);
-#pragma unroll
-        for (int c = 0; c < 8; c++) x += kv[c] * s_q[wave][v * 8 + c];
-      }
-      x *= scale;
-    }
-    float top = x;
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    // a score that is NaN is not a maximum, and makes the sums below NaN
-    const float next = fmaxf(m, top);
-    const float base = next == -INFINITY ? 0.f : next;
-    const float keep = exp2f(m - base), e = slot >= 0 ? exp2f(x - base) : 0.f;
-    m = next;
-    float sum = e;
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-    l = l * keep + sum;
-#pragma unroll
-    for (int c = 0; c < ND; c++) o[c] *= keep;
-    uint64_t todo = __ballot(slot >= 0);
-    while (todo) {
-      const int j = __builtin_ctzll(todo);
-      todo &= todo - 1;
-      const float pj = __shfl(e, j);
-      const int64_t sj = __shfl(slot, j);
-      const elem* vp = reinterpret_cast<const elem*>(a.v_rows) + sj * a.v_row + (int64_t)hk * (DK == DV ? DV : 0);
-#pragma unroll
-      for (int c = 0; c < ND; c++) o[c] += pj * (float)vp[c * 64 + lane];
-    }
-  }
+  float o[DV / 64], m, l;
+  exact_row<T, DK, DV>(a, s, row, h, p, span, 0, span.n, s_q[wave], o, &m, &l);
   elem* op = reinterpret_cast<elem*>(a.out) + row * a.out_stride[0] + h * a.out_stride[1];
-  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int c = 0; c < ND; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] * inv);
+  for (int c = 0; c < DV / 64; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
   if (a.lse && lane == 0) a.lse[row * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// Row tiles of R rows that a call can have at most: each sequence rounds up once.
+int64_t most_tiles(const AttendArgs& a, int R) {
+  return a.q_rows * a.group / R + (a.num_seqs < a.q_rows ? a.num_seqs : a.q_rows);
+}
+
+bool decodes(const AttendArgs& a, int32_t head_dim) {
+  return head_dim != 576 && a.max_q * a.group <= 2 * kRowTile;
+}
+
+// How the list of items is made for a call of tiles of R rows, and the number of items at most:
+// a split of C keys has at least `min_split` of them, and the whole call's keys over C is at
+// most `target`.
+int64_t plan(AttendArgs* a, int R, int32_t num_cus) {
+  a->min_split = 128;
+  a->target = (int64_t)num_cus * 8;
+  const int64_t tiles = most_tiles(*a, R) * a->kv_heads;
+  return a->max_kv <= a->min_split ? tiles : tiles + a->target;
+}
+
+template <class T, int D>
+hipError_t launch_decode(AttendArgs a, int32_t num_cus, hipStream_t stream) {
+  const int64_t items = a.items = plan(&a, kRowTile, num_cus);
+  if (items > 0x7fffffff) return hipErrorInvalidValue;
+  k_attend_decode<T, D><<<dim3((unsigned)items), 256, 0, stream>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.max_kv <= a.min_split) return e;
+  const int64_t joins = most_tiles(a, kRowTile) * a.kv_heads * (kRowTile / 4);
+  if (joins > 0x7fffffff) return hipErrorInvalidValue;
+  k_attend_join<T, D, kRowTile><<<dim3((unsigned)joins), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <class T>
-hipError_t launch_for(const AttendArgs& a, int32_t head_dim, hipStream_t stream) {
+hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hipStream_t stream) {
+  (void)hipGetLastError();
+  if (decodes(a, head_dim))
+    return head_dim == 64 ? launch_decode<T, 64>(a, num_cus, stream) : launch_decode<T, 128>(a, num_cus, stream);
   const int64_t units = a.q_rows * a.q_heads;
   const dim3 grid((unsigned)((units + 3) / 4));
-  (void)hipGetLastError();
   if (head_dim == 64) k_attend_rows<T, 64, 64><<<grid, 256, 0, stream>>>(a);
   else if (head_dim == 128) k_attend_rows<T, 128, 128><<<grid, 256, 0, stream>>>(a);
   else k_attend_rows<T, 576, 512><<<grid, 256, 0, stream>>>(a);
@@ -186,11 +703,17 @@ hipError_t launch_for(const AttendArgs& a, int32_t head_dim, hipStream_t stream)
 
 }  // namespace
 
-int64_t attend_workspace(const AttendArgs&, int32_t, int32_t) { return 0; }
+int64_t attend_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_cus) {
+  if (!decodes(args, head_dim) || args.q_rows <= 0 || args.num_seqs <= 0) return 0;
+  AttendArgs a = args;
+  const int64_t items = plan(&a, kRowTile, num_cus);
+  if (a.max_kv <= a.min_split) return 0;
+  return 4 * items * (head_dim == 64 ? partial_floats<64>(kRowTile) : partial_floats<128>(kRowTile));
+}
 
-hipError_t launch_attend(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t, hipStream_t stream) {
+hipError_t launch_attend(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t num_cus, hipStream_t stream) {
   if (a.q_rows <= 0 || a.num_seqs <= 0) return hipSuccess;
-  return dtype == HC_BF16 ? launch_for<Bf16>(a, head_dim, stream) : launch_for<F16>(a, head_dim, stream);
+  return dtype == HC_BF16 ? launch_for<Bf16>(a, head_dim, num_cus, stream) : launch_for<F16>(a, head_dim, num_cus, stream);
 }
 
 }  // namespace hc

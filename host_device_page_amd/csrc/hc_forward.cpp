@@ -42,6 +42,7 @@ int launched(hipError_t e, const char* what) {
 }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;      // rows, sequences and tokens of one call
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;    // of an attention call: 32-bit positions
 constexpr int64_t kMaxStride = (int64_t)1 << 40;    // keeps every offset far inside int64
 
 // The extent of an [n][heads][dim] tensor with strides in elements, in bytes from its first
@@ -275,9 +276,9 @@ int attend_sizes(const PoolView& v, const hc_attend_desc* d, hc::AttendArgs* a) 
   if (!isfinite(d->scale)) return set_error(HC_ERR_INVALID, "scale must be finite");
   if (d->window < 0 || d->sinks < 0) return set_error(HC_ERR_INVALID, "window and sinks must be >= 0");
   if (d->window > 0 && !d->causal) return set_error(HC_ERR_INVALID, "a window needs causal");
-  if (d->num_seqs < 0 || d->num_seqs >= kMaxRows || d->q_rows < 0 || d->q_rows >= kMaxRows || d->max_q < 0 ||
-      d->max_q >= kMaxRows || d->max_kv < 0 || d->max_kv >= kMaxRows)
-    return set_error(HC_ERR_INVALID, "num_seqs, q_rows, max_q and max_kv must be in [0, 2^31)");
+  if (d->num_seqs < 0 || d->num_seqs > kMaxTokens || d->q_rows < 0 || d->q_rows > kMaxTokens || d->max_q < 0 ||
+      d->max_q > kMaxTokens || d->max_kv < 0 || d->max_kv > kMaxTokens)
+    return set_error(HC_ERR_INVALID, "num_seqs, q_rows, max_q and max_kv must be in [0, 2^30]");
   if (d->table_width < 0 || d->table_width >= kMaxRows || d->table_stride < 0 || d->table_stride > kMaxStride ||
       (d->num_seqs > 1 && d->table_stride < d->table_width))
     return set_error(HC_ERR_INVALID, "bad table_width or table_stride");
@@ -292,17 +293,23 @@ int attend_sizes(const PoolView& v, const hc_attend_desc* d, hc::AttendArgs* a) 
   a->table_stride = d->table_stride;
   a->k_row = (int64_t)d->kv_heads * d->head_dim;
   a->v_row = latent ? a->k_row : (int64_t)d->kv_heads * d->value_dim;
-  a->S = v.geom->S;
   a->num_seqs = d->num_seqs;
   a->q_rows = d->q_rows;
   a->max_q = d->max_q < d->q_rows ? d->max_q : d->q_rows;
   a->max_kv = d->max_kv;
-  a->window = d->window;
-  a->sinks = d->window > 0 ? d->sinks : 0;
+  // a window that covers every sequence hides nothing
+  a->window = d->window < d->max_kv ? (int32_t)d->window : 0;
+  a->sinks = a->window > 0 ? (int32_t)(d->sinks < d->max_kv ? d->sinks : d->max_kv) : 0;
   a->q_heads = d->q_heads;
   a->kv_heads = d->kv_heads;
   a->group = d->q_heads / d->kv_heads;
   a->entry = d->entry_tokens;
+  a->entries = v.geom->S / d->entry_tokens;
+  // with 2^shift >= 2^31 * entry, ceil(2^shift / entry) is below 2^32 and off by less than 1 / entry
+  // over all j < 2^31
+  a->entry_shift = 31;
+  while (((int64_t)1 << (a->entry_shift - 31)) < a->entry) a->entry_shift++;
+  a->entry_magic = (uint32_t)((((uint64_t)1 << a->entry_shift) + (uint64_t)a->entry - 1) / (uint64_t)a->entry);
   a->causal = d->causal != 0;
   a->scale = d->scale;
   return HC_OK;

@@ -49,7 +49,11 @@ struct AttendArgs {
   float* work;  // partial results of split sequences
   int64_t q_stride[2], out_stride[2], table_width, table_stride;
   int64_t k_row, v_row;  // elements from token to token in the layer's rows
-  int64_t S, num_seqs, q_rows, max_q, max_kv, window, sinks;
+  int64_t num_seqs, q_rows, max_q, max_kv;
+  int32_t window, sinks;
+  int64_t entries;                     // table entries of the pool: S / entry
+  int64_t target, min_split, items;    // how the work is split (set by launch_attend)
+  uint32_t entry_magic, entry_shift;   // j / entry == (j * magic) >> shift for j < 2^31
   int32_t q_heads, kv_heads, group, entry, causal;
   float scale;
 };
