@@ -23,6 +23,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -34,12 +35,18 @@ struct Bf16 {
   static __device__ __forceinline__ f32x4 mfma16(v8 a, v8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
+  static __device__ __forceinline__ f32x16 mfma32(v8 a, v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
 };
 struct F16 {
   typedef _Float16 elem;
   typedef f16x8 v8;
   static __device__ __forceinline__ f32x4 mfma16(v8 a, v8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(v8 a, v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
 };
 
@@ -251,8 +258,9 @@ __device__ bool find_item(const AttendArgs& a, int R, int64_t want, int64_t* s_p
   const int64_t rest = s_plan[2];
   const int64_t unit = rest / it->splits;
   it->split = (int32_t)(rest - unit * it->splits);
-  it->tile = (int32_t)(unit / a.kv_heads);
-  it->hk = (int32_t)(unit - (int64_t)it->tile * a.kv_heads);
+  const int64_t back = unit / a.kv_heads;
+  it->tile = (int32_t)(s_plan[3] - 1 - back);  // the last rows see the most keys and come first
+  it->hk = (int32_t)(unit - back * a.kv_heads);
   it->q = sequence(a, it->s);
   it->index = want;
   __syncthreads();
@@ -530,7 +538,247 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   }
 }
 
-// Joins the splits of a row tile: one wave per row.  Workgroups of tiles that were not split have
+// ---------------------------------------------------------------- many rows: chunks and prompts
+// A workgroup takes 128 (token, head) rows of one KV head, 32 a wave, and walks its keys in tiles of
+// 64 whose K and V all four waves read from LDS.  4 * D operations on a pair make it bound by the
+// matrix cores, and next to them by the exponentials and by LDS, 2 * 64 * D * 2 bytes a wave and tile.
+//
+// The products are the decoding kernel's in their 32 x 32 form: S^T = K Q^T leaves a lane with one
+// row's scores of 32 of the 64 keys, 8 q + 4 (lane / 32) + r of each 32, which are the operand of
+// O^T += V^T P^T as they stand; V comes from LDS transposed, in that order of the keys.  The next tile
+// is loaded into registers while one is computed and goes to the other half of LDS: one barrier a tile.
+//
+// The maximum that a row's weights are relative to is replaced only when it grows by more than
+// 2^8: until then weights of up to 2^8 are summed, which loses nothing in fp32 or as operands, and the
+// sums need not be scaled.
+constexpr int kTileRows = 128;
+constexpr int kTileKeys = 64;
+constexpr float kGrow = 8.f;
+
+template <int D>
+__device__ __forceinline__ int k_place(int row, int chunk) {  // byte of a 16-byte chunk of a K row: 16
+  return row * D * 2 + (chunk ^ (D == 128 ? row & 15 : (row >> 1) & 7)) * 16;  // rows' same chunk in 16 places
+}
+template <int D>
+__device__ __forceinline__ int v_place(int row, int chunk) {  // of a V row: four rows' 32 dims side by side
+  return row * D * 2 + (chunk ^ (D == 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2)) * 16;
+}
+
+template <class T, int D>
+__global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
+  typedef typename T::v8 v8;
+  typedef typename T::elem elem;
+  constexpr int KS = D / 16;                    // product steps over the head
+  constexpr int DT = D / 32;                    // 32-dim tiles of the output
+  constexpr int CH = D / 8;                     // 16-byte chunks of a row
+  constexpr int LD = kTileKeys * CH / 256;      // loads of a lane, K and V each
+  constexpr int BUF = kTileKeys * D * 2;        // bytes of a K or V tile
+  __shared__ __align__(16) uint8_t s_k[2][BUF], s_v[2][BUF];
+  __shared__ int64_t s_plan[8];
+  Item it;
+  if (!find_item(a, kTileRows, blockIdx.x, s_plan, &it)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = lane & 31, half = lane >> 5;
+  const int64_t rows_all = (int64_t)it.q.m * a.group;
+  const int64_t t0 = (int64_t)it.tile * kTileRows;
+  const int rows_tile = rows_all - t0 < kTileRows ? (int)(rows_all - t0) : kTileRows;
+  // this lane's row, and the positions of the tile's and the wave's first and last rows
+  const int rr = wave * 32 + col;
+  const bool live = rr < rows_tile;
+  const int64_t r = t0 + (live ? rr : 0);
+  const int tok = (int)(r / a.group), h = it.hk * a.group + (int)(r - (int64_t)tok * a.group);
+  const int64_t row = it.q.q0 + tok;
+  const int before = it.q.kv - it.q.m;
+  const int p = before + tok;
+  const int p_first = before + (int)(t0 / a.group), p_last = before + (int)((t0 + rows_tile - 1) / a.group);
+  const Span span = span_of(a, it.q.kv, p_first, p_last);
+  const int part = ((span.n + it.splits - 1) / it.splits + kTileKeys - 1) / kTileKeys * kTileKeys;
+  const int i0 = (int64_t)it.split * part < span.n ? it.split * part : span.n;
+  const int i1 = i0 + part < span.n ? i0 + part : span.n;
+  // weights are exp2(c * score - c * maximum) with c > 0; a negative scale turns the queries' sign, and
+  // for 0 every finite score times c is 0
+  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+  v8 q[KS];
+  {
+    const v4u* qp = reinterpret_cast<const v4u*>(a.q + 2 * (row * a.q_stride[0] + h * a.q_stride[1]));
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < KS; i++) {
+      const v4u x = qp[i * 2 + half] ^ flip;
+      q[i] = __builtin_bit_cast(v8, live ? x : v4u{0, 0, 0, 0});
+    }
+  }
+  const uint8_t* kb = a.k_rows + 2 * (int64_t)it.hk * D;
+  const uint8_t* vb = a.v_rows + 2 * (int64_t)it.hk * D;
+  const uint64_t k_row = 2 * a.k_row, v_row = 2 * a.v_row;
+  auto slots = [&](int base) -> uint32_t {  // of key `lane` of the tile
+    const int i = base + lane;
+    return i < i1 ? slot_of(a, it.s, (uint32_t)span.key(i)) : kNoSlot;
+  };
+  v4u kr[LD], vr[LD];
+  auto load = [&](uint32_t slot) {
+#pragma unroll
+    for (int x = 0; x < LD; x++) {
+      const int at = x * 256 + threadIdx.x;
+      const uint32_t sl = __shfl(slot, at / CH);
+      const uint64_t s64 = sl == kNoSlot ? 0 : sl;
+      kr[x] = *reinterpret_cast<const v4u*>(kb + s64 * k_row + (at % CH) * 16);
+      const v4u v = *reinterpret_cast<const v4u*>(vb + s64 * v_row + (at % CH) * 16);
+      vr[x] = sl == kNoSlot ? v4u{0, 0, 0, 0} : v;
+    }
+  };
+  auto keep_tile = [&](int buf) {
+#pragma unroll
+    for (int x = 0; x < LD; x++) {
+      const int at = x * 256 + threadIdx.x;
+      *reinterpret_cast<v4u*>(s_k[buf] + k_place<D>(at / CH, at % CH)) = kr[x];
+      *reinterpret_cast<v4u*>(s_v[buf] + v_place<D>(at / CH, at % CH)) = vr[x];
+    }
+  };
+  f32x16 o[DT] = {};
+  float m = -INFINITY, l = 0.f;
+  uint32_t slot = slots(i0), slot_next = slots(i0 + kTileKeys);
+  if (i0 < i1) {
+    load(slot);
+    keep_tile(0);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (int base = i0; base < i1; base += kTileKeys) {
+    const uint64_t there = __ballot(slot != kNoSlot);
+    const bool more = base + kTileKeys < i1;
+    if (more) load(slot_next);
+    slot = slot_next;
+    slot_next = slots(base + 2 * kTileKeys);
+    f32x16 st[2] = {};
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int i = 0; i < KS; i++) {
+        const v8 k = *reinterpret_cast<const v8*>(s_k[buf] + k_place<D>(u * 32 + col, i * 2 + half));
+        st[u] = T::mfma32(k, q[i], st[u]);
+      }
+    float x[32];
+#pragma unroll
+    for (int e = 0; e < 32; e++) x[e] = st[e / 16][e % 16];
+    const bool whole = there == ~0ull && (!a.causal || (span.key(base + kTileKeys - 1) <= p_first &&
+                                                        (a.window == 0 || p_last - span.key(base) < a.window)));
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 32; e++) {
+        const int k = (e / 16) * 32 + (e % 16) / 4 * 8 + half * 4 + e % 4;
+        const bool sees = ((there >> k) & 1) & visible(a, p, span.key(base + k));
+        x[e] = sees ? x[e] : -INFINITY;
+      }
+    }
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < 32; e++) top = fmaxf(top, x[e]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__any((top - m) * c > kGrow || (m == -INFINITY && top != -INFINITY))) {
+      const float next = fmaxf(m, top);
+      const float keep = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - next) * c);
+      m = next;
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < DT; d++) o[d] *= keep;
+    }
+    const float zero = m == -INFINITY ? 0.f : m * c;
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 32; e++) {
+      x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -zero));
+      sum += x[e];
+    }
+    l += sum;
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      f32x8 w;
+#pragma unroll
+      for (int e = 0; e < 8; e++) w[e] = x[s * 8 + e];
+      const v8 wt = __builtin_convertvector(w, v8);
+#pragma unroll
+      for (int d = 0; d < DT; d++) {
+        s16x4 v[2];
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+          const int key = s * 16 + t * 8 + half * 4 + (lane & 15) / 4;
+          const int at = d * 32 + (lane & 16) + (lane & 3) * 4;  // dim
+          v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4)(s_v[buf] + v_place<D>(key, at / 8) + (at & 4) * 2));
+        }
+        const v8 vt = __builtin_bit_cast(v8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        o[d] = T::mfma32(vt, wt, o[d]);
+      }
+    }
+    buf ^= 1;
+    if (more) keep_tile(buf);
+    __syncthreads();
+  }
+  l += __shfl_xor(l, 32);
+  bool nan = false;
+#pragma unroll
+  for (int d = 0; d < DT; d++)
+#pragma unroll
+    for (int e = 0; e < 16; e++) nan |= o[d][e] != o[d][e];
+  nan |= l != l;
+  uint64_t again = __ballot(nan && live);
+  again = (again | again >> 32) & 0xffffffffu;
+  const bool mine = live && !((again >> col) & 1);
+  const float log2_max = m == -INFINITY ? -INFINITY : m * c;  // of the weights, in the joining kernel's unit
+  float* part_o = a.work + it.index * partial_floats<D>(kTileRows);
+  float* part_ml = part_o + kTileRows * D;
+  elem* op = reinterpret_cast<elem*>(a.out) + row * a.out_stride[0] + h * a.out_stride[1];
+  if (mine) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const int dim = d * 32 + e * 8 + half * 4;
+        f32x4 y = {o[d][e * 4], o[d][e * 4 + 1], o[d][e * 4 + 2], o[d][e * 4 + 3]};
+        if (it.splits > 1) {
+          *reinterpret_cast<f32x4*>(part_o + rr * D + dim) = y;
+        } else {
+          typedef elem e4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<e4*>(op + dim) = __builtin_convertvector(y * inv, e4);
+        }
+      }
+    if (half == 0) {
+      if (it.splits > 1) {
+        part_ml[rr * 2] = log2_max;
+        part_ml[rr * 2 + 1] = l;
+      } else if (a.lse) {
+        a.lse[row * a.q_heads + h] = l == 0.f ? -INFINITY : (log2_max + log2f(l)) * kLn2;
+      }
+    }
+  }
+  // rows that came out NaN, one after the other (a wave's own LDS: the tiles are done with)
+  float* s_q = reinterpret_cast<float*>(s_k[0]) + wave * D;
+  while (again) {
+    const int w = __builtin_ctzll(again);
+    again &= again - 1;
+    const int64_t ra = t0 + wave * 32 + w;
+    const int ta = (int)(ra / a.group), ha = it.hk * a.group + (int)(ra - (int64_t)ta * a.group);
+    float oo[D / 64], mm, ll;
+    exact_row<T, D, D>(a, it.s, it.q.q0 + ta, ha, before + ta, span, i0, i1, s_q, oo, &mm, &ll);
+    elem* oa = reinterpret_cast<elem*>(a.out) + (it.q.q0 + ta) * a.out_stride[0] + ha * a.out_stride[1];
+    for (int x = 0; x < D / 64; x++) {
+      if (it.splits > 1) part_o[(wave * 32 + w) * D + x * 64 + lane] = oo[x];
+      else oa[x * 64 + lane] = (elem)(ll == 0.f ? 0.f : oo[x] / ll);
+    }
+    if (lane == 0) {
+      if (it.splits > 1) {
+        part_ml[(wave * 32 + w) * 2] = mm;
+        part_ml[(wave * 32 + w) * 2 + 1] = ll;
+      } else if (a.lse) {
+        a.lse[(it.q.q0 + ta) * a.q_heads + ha] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      }
+    }
+  }
+}
+
+// Joins the splits of a row tile, a wave a row.  Workgroups of tiles that were not split have
 // nothing to do.
 template <class T, int DV, int R>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
@@ -550,7 +798,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   work = (s_plan[0] + s_plan[1] + s_plan[2] + s_plan[3]) * a.kv_heads;
   int64_t C = (work + a.target - 1) / a.target;
   C = C < a.min_split ? a.min_split : C;
-  const int64_t want = blockIdx.x / (R / 4);  // a workgroup does four rows of a tile
+  const int64_t want = blockIdx.x;
   int64_t tiles = 0, items = 0;
   bool found = false;
   for (int64_t s0 = 0; s0 < a.num_seqs && !found; s0 += 256) {
@@ -581,6 +829,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
       s_plan[1] = splits;
       s_plan[2] = want - t_at;
       s_plan[3] = i_at;
+      s_plan[4] = c.tiles;
     }
     found = want < tiles;
   }
@@ -592,33 +841,36 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   // a q_start that goes back (reported) can make more items than the call has room for
   if (first + splits > a.items) return;
   q = sequence(a, s);
-  const int64_t tile = unit / a.kv_heads;
-  const int hk = (int)(unit - tile * a.kv_heads);
-  const int rr = (int)(blockIdx.x % (R / 4)) * 4 + wave;
-  const int64_t r = tile * R + rr;
-  if (r >= (int64_t)q.m * a.group) return;
+  const int64_t back = unit / a.kv_heads;
+  const int64_t tile = s_plan[4] - 1 - back;
+  const int hk = (int)(unit - back * a.kv_heads);
   constexpr int ND = DV / 64;
-  float m = -INFINITY, l = 0.f, o[ND] = {};
-  for (int64_t k = 0; k < splits; k++) {
-    const float* po = a.work + (first + k) * partial_floats<DV>(R);
-    const float pm = po[R * DV + rr * 2], pl = po[R * DV + rr * 2 + 1];
-    float v[ND];
+  const int64_t left = (int64_t)q.m * a.group - tile * R;
+  for (int rr = wave; rr < R && rr < left; rr += 4) {
+    float m = -INFINITY, l = 0.f, o[ND] = {};
+#pragma unroll 4
+    for (int64_t k = 0; k < splits; k++) {
+      const float* po = a.work + (first + k) * partial_floats<DV>(R);
+      const float pm = po[R * DV + rr * 2], pl = po[R * DV + rr * 2 + 1];
+      float v[ND];
 #pragma unroll
-    for (int c = 0; c < ND; c++) v[c] = po[rr * DV + c * 64 + lane];
-    const float next = fmaxf(m, pm);
-    const float zero = next == -INFINITY ? 0.f : next;
-    const float keep = __builtin_amdgcn_exp2f(m - zero), add = __builtin_amdgcn_exp2f(pm - zero);
-    m = next;
-    l = l * keep + pl * add;
+      for (int c = 0; c < ND; c++) v[c] = po[rr * DV + c * 64 + lane];
+      const float next = fmaxf(m, pm);
+      const float zero = next == -INFINITY ? 0.f : next;
+      const float keep = __builtin_amdgcn_exp2f(m - zero), add = __builtin_amdgcn_exp2f(pm - zero);
+      m = next;
+      l = l * keep + pl * add;
 #pragma unroll
-    for (int c = 0; c < ND; c++) o[c] = o[c] * keep + v[c] * add;
+      for (int c = 0; c < ND; c++) o[c] = o[c] * keep + v[c] * add;
+    }
+    const int64_t r = tile * R + rr;
+    const int64_t rt = r / a.group;
+    const int h = hk * a.group + (int)(r - rt * a.group);
+    elem* op = reinterpret_cast<elem*>(a.out) + (q.q0 + rt) * a.out_stride[0] + h * a.out_stride[1];
+#pragma unroll
+    for (int c = 0; c < ND; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
+    if (a.lse && lane == 0) a.lse[(q.q0 + rt) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
-  const int64_t rt = r / a.group;
-  const int h = hk * a.group + (int)(r - rt * a.group);
-  elem* op = reinterpret_cast<elem*>(a.out) + (q.q0 + rt) * a.out_stride[0] + h * a.out_stride[1];
-#pragma unroll
-  for (int c = 0; c < ND; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
-  if (a.lse && lane == 0) a.lse[(q.q0 + rt) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- any call, one wave per (row, head)
@@ -661,54 +913,62 @@ int64_t most_tiles(const AttendArgs& a, int R) {
   return a.q_rows * a.group / R + (a.num_seqs < a.q_rows ? a.num_seqs : a.q_rows);
 }
 
-bool decodes(const AttendArgs& a, int32_t head_dim) {
-  return head_dim != 576 && a.max_q * a.group <= 2 * kRowTile;
+// The kernel for a call: rows of a row tile, 0 for the one that goes row by row.
+int tile_rows(const AttendArgs& a, int32_t head_dim) {
+  if (head_dim == 576) return 0;
+  return a.max_q * a.group <= 2 * kRowTile ? kRowTile : kTileRows;
 }
 
 // How the list of items is made for a call of tiles of R rows, and the number of items at most:
 // a split of C keys has at least `min_split` of them, and the whole call's keys over C is at
 // most `target`.
 int64_t plan(AttendArgs* a, int R, int32_t num_cus) {
-  a->min_split = 128;
-  a->target = (int64_t)num_cus * 8;
+  a->min_split = R == kRowTile ? 128 : 256;
+  a->target = (int64_t)num_cus * (R == kRowTile ? 8 : 2);
   const int64_t tiles = most_tiles(*a, R) * a->kv_heads;
   return a->max_kv <= a->min_split ? tiles : tiles + a->target;
 }
 
-template <class T, int D>
-hipError_t launch_decode(AttendArgs a, int32_t num_cus, hipStream_t stream) {
-  const int64_t items = a.items = plan(&a, kRowTile, num_cus);
-  if (items > 0x7fffffff) return hipErrorInvalidValue;
-  k_attend_decode<T, D><<<dim3((unsigned)items), 256, 0, stream>>>(a);
+template <class T, int D, int R>
+hipError_t launch_split(AttendArgs a, int32_t num_cus, hipStream_t stream) {
+  const int64_t items = a.items = plan(&a, R, num_cus);
+  const int64_t joins = most_tiles(a, R) * a.kv_heads;
+  if (items > 0x7fffffff || joins > 0x7fffffff) return hipErrorInvalidValue;
+  if (R == kRowTile)
+    k_attend_decode<T, D><<<dim3((unsigned)items), 256, 0, stream>>>(a);
+  else
+    k_attend_tiles<T, D><<<dim3((unsigned)items), 256, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.max_kv <= a.min_split) return e;
-  const int64_t joins = most_tiles(a, kRowTile) * a.kv_heads * (kRowTile / 4);
-  if (joins > 0x7fffffff) return hipErrorInvalidValue;
-  k_attend_join<T, D, kRowTile><<<dim3((unsigned)joins), 256, 0, stream>>>(a);
+  k_attend_join<T, D, R><<<dim3((unsigned)joins), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hipStream_t stream) {
   (void)hipGetLastError();
-  if (decodes(a, head_dim))
-    return head_dim == 64 ? launch_decode<T, 64>(a, num_cus, stream) : launch_decode<T, 128>(a, num_cus, stream);
-  const int64_t units = a.q_rows * a.q_heads;
-  const dim3 grid((unsigned)((units + 3) / 4));
-  if (head_dim == 64) k_attend_rows<T, 64, 64><<<grid, 256, 0, stream>>>(a);
-  else if (head_dim == 128) k_attend_rows<T, 128, 128><<<grid, 256, 0, stream>>>(a);
-  else k_attend_rows<T, 576, 512><<<grid, 256, 0, stream>>>(a);
+  const int R = tile_rows(a, head_dim);
+  if (R == kRowTile)
+    return head_dim == 64 ? launch_split<T, 64, kRowTile>(a, num_cus, stream)
+                          : launch_split<T, 128, kRowTile>(a, num_cus, stream);
+  if (R == kTileRows)
+    return head_dim == 64 ? launch_split<T, 64, kTileRows>(a, num_cus, stream)
+                          : launch_split<T, 128, kTileRows>(a, num_cus, stream);
+  const int64_t groups = (a.q_rows * a.q_heads + 3) / 4;
+  if (groups > 0x7fffffff) return hipErrorInvalidValue;
+  k_attend_rows<T, 576, 512><<<dim3((unsigned)groups), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t attend_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_cus) {
-  if (!decodes(args, head_dim) || args.q_rows <= 0 || args.num_seqs <= 0) return 0;
+  const int R = tile_rows(args, head_dim);
+  if (R == 0 || args.q_rows <= 0 || args.num_seqs <= 0) return 0;
   AttendArgs a = args;
-  const int64_t items = plan(&a, kRowTile, num_cus);
+  const int64_t items = plan(&a, R, num_cus);
   if (a.max_kv <= a.min_split) return 0;
-  return 4 * items * (head_dim == 64 ? partial_floats<64>(kRowTile) : partial_floats<128>(kRowTile));
+  return 4 * items * (head_dim == 64 ? partial_floats<64>(R) : partial_floats<128>(R));
 }
 
 hipError_t launch_attend(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t num_cus, hipStream_t stream) {
