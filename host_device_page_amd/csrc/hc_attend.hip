@@ -778,6 +778,259 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- a latent cache: one row is key and value
+// 576 dims of a key against every head of a token, 512 of them its value, so a tile of keys is read
+// into LDS once for both products.  A workgroup takes 64 rows and tiles of 64 keys (72 KiB, two of
+// them in LDS).  Its four waves cut the work without doing any twice:
+//   S^T = K Q^T    wave (i, j): rows 32 i, keys 32 j; its rows' Q stays in registers
+//   maxima of the two key halves, then the weights, go through LDS
+//   O^T += V^T P^T wave w: dims 128 w of all rows, so a value is read by one wave only
+// Decoding with few heads is bound by memory (2 * 1088 operations per row on 1152 bytes of a key), many
+// rows by LDS: 240 KiB are read from it for 2176 cycles of the matrix cores.
+constexpr int kLatRows = 64;
+constexpr int kLatKeys = 64;
+constexpr int kLatDim = 576;
+constexpr int kLatValue = 512;
+constexpr int kLatBytes = kLatDim * 2;
+
+// Byte of a 16-byte chunk of a key row.  Rows start 128 bytes apart in the banks; the swizzle of
+// 8 chunks spreads both 16 rows' same chunk and four rows' 64 bytes of dims over all banks.
+__device__ __forceinline__ int lat_place(int row, int chunk) {
+  const int f = ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+  return row * kLatBytes + (chunk ^ f) * 16;
+}
+
+template <class T>
+__global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
+  typedef typename T::v8 v8;
+  typedef typename T::elem elem;
+  constexpr int KS = kLatDim / 16;
+  constexpr int CH = kLatDim / 8;
+  constexpr int LD = kLatKeys * CH / 256;
+  constexpr int DT = 4;  // 32-dim tiles of a wave
+  __shared__ __align__(16) uint8_t s_k[2][kLatKeys * kLatBytes];
+  __shared__ __align__(16) uint8_t s_p[kLatRows * kLatKeys * 2];
+  __shared__ float s_max[2][kLatRows], s_sum[4][kLatRows];
+  __shared__ uint32_t s_nan[2];
+  __shared__ int64_t s_plan[8];
+  Item it;
+  if (!find_item(a, kLatRows, blockIdx.x, s_plan, &it)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = lane & 31, half = lane >> 5;
+  const int wi = wave >> 1, wj = wave & 1;
+  const int64_t rows_all = (int64_t)it.q.m * a.group;
+  const int64_t t0 = (int64_t)it.tile * kLatRows;
+  const int rows_tile = rows_all - t0 < kLatRows ? (int)(rows_all - t0) : kLatRows;
+  const bool two = rows_tile > 32;  // else the second 32 rows are left out
+  const bool scores = two || wi == 0;
+  const int before = it.q.kv - it.q.m;
+  // row x of the tile (a row past the end: the tile's first)
+  auto token = [&](int x) { return (int)((t0 + (x < rows_tile ? x : 0)) / a.group); };
+  auto head = [&](int x, int tok) { return (int)(t0 + (x < rows_tile ? x : 0) - (int64_t)tok * a.group); };
+  const int rr = wi * 32 + col;  // this lane's row of the scores
+  const int tok = token(rr), h = head(rr, tok);
+  const int p = before + tok;
+  const int p_first = before + (int)(t0 / a.group), p_last = before + (int)((t0 + rows_tile - 1) / a.group);
+  const Span span = span_of(a, it.q.kv, p_first, p_last);
+  const int part = ((span.n + it.splits - 1) / it.splits + kLatKeys - 1) / kLatKeys * kLatKeys;
+  const int i0 = (int64_t)it.split * part < span.n ? it.split * part : span.n;
+  const int i1 = i0 + part < span.n ? i0 + part : span.n;
+  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+  v8 q[KS];
+  {
+    const v4u* qp = reinterpret_cast<const v4u*>(a.q + 2 * ((it.q.q0 + tok) * a.q_stride[0] + h * a.q_stride[1]));
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < KS; i++) {
+      const v4u x = qp[i * 2 + half] ^ flip;
+      q[i] = __builtin_bit_cast(v8, rr < rows_tile ? x : v4u{0, 0, 0, 0});
+    }
+  }
+  const uint64_t k_row = 2 * a.k_row;
+  auto slots = [&](int base) -> uint32_t {
+    const int i = base + lane;
+    return i < i1 ? slot_of(a, it.s, (uint32_t)span.key(i)) : kNoSlot;
+  };
+  v4u kr[LD];
+  auto load = [&](uint32_t slot) {
+#pragma unroll
+    for (int x = 0; x < LD; x++) {
+      const int at = x * 256 + threadIdx.x;
+      const uint32_t sl = __shfl(slot, at / CH);
+      const v4u v = *reinterpret_cast<const v4u*>(a.k_rows + (sl == kNoSlot ? 0 : sl) * k_row + (at % CH) * 16);
+      kr[x] = sl == kNoSlot ? v4u{0, 0, 0, 0} : v;
+    }
+  };
+  auto keep_tile = [&](int buf) {
+#pragma unroll
+    for (int x = 0; x < LD; x++) {
+      const int at = x * 256 + threadIdx.x;
+      *reinterpret_cast<v4u*>(s_k[buf] + lat_place(at / CH, at % CH)) = kr[x];
+    }
+  };
+  auto p_place = [&](int row, int chunk) { return row * kLatKeys * 2 + (chunk ^ (row & 7)) * 16; };
+  f32x16 o[2][DT] = {};
+  float m[2] = {-INFINITY, -INFINITY}, l = 0.f;  // maxima of rows col and 32 + col; this lane's part of row rr's sum
+  uint32_t slot = slots(i0), slot_next = slots(i0 + kLatKeys);
+  if (i0 < i1) {
+    load(slot);
+    keep_tile(0);
+  }
+  if (threadIdx.x < 2) s_nan[threadIdx.x] = 0;
+  __syncthreads();
+  int buf = 0;
+  for (int base = i0; base < i1; base += kLatKeys) {
+    const uint64_t there = __ballot(slot != kNoSlot);
+    const bool more = base + kLatKeys < i1;
+    if (more) load(slot_next);
+    slot = slot_next;
+    slot_next = slots(base + 2 * kLatKeys);
+    float x[16];
+    if (scores) {
+      f32x16 st = {};
+#pragma unroll
+      for (int i = 0; i < KS; i++) {
+        const v8 k = *reinterpret_cast<const v8*>(s_k[buf] + lat_place(wj * 32 + col, i * 2 + half));
+        st = T::mfma32(k, q[i], st);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e++) x[e] = st[e];
+      const bool whole = there == ~0ull && (!a.causal || (span.key(base + kLatKeys - 1) <= p_first &&
+                                                          (a.window == 0 || p_last - span.key(base) < a.window)));
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+          const int k = wj * 32 + e / 4 * 8 + half * 4 + e % 4;
+          const bool sees = ((there >> k) & 1) & visible(a, p, span.key(base + k));
+          x[e] = sees ? x[e] : -INFINITY;
+        }
+      }
+      float top = x[0];
+#pragma unroll
+      for (int e = 1; e < 16; e++) top = fmaxf(top, x[e]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (half == 0) s_max[wj][rr] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      if (i == 1 && !two) break;
+      const float top = fmaxf(s_max[0][i * 32 + col], s_max[1][i * 32 + col]);
+      // the same rows and numbers in every wave, so all decide alike
+      if (__any((top - m[i]) * c > kGrow || (m[i] == -INFINITY && top != -INFINITY))) {
+        const float next = fmaxf(m[i], top);
+        const float keep = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[i] - next) * c);
+        m[i] = next;
+        if (wi == i) l *= keep;
+#pragma unroll
+        for (int d = 0; d < DT; d++) o[i][d] *= keep;
+      }
+    }
+    if (scores) {
+      const float mine = wi ? m[1] : m[0];
+      const float zero = mine == -INFINITY ? 0.f : mine * c;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -zero));
+        sum += x[e];
+      }
+      l += sum;
+#pragma unroll
+      for (int s = 0; s < 2; s++) {
+        f32x8 w;
+#pragma unroll
+        for (int e = 0; e < 8; e++) w[e] = x[s * 8 + e];
+        *reinterpret_cast<v8*>(s_p + p_place(rr, (wj * 2 + s) * 2 + half)) = __builtin_convertvector(w, v8);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      v8 w[2];
+      w[0] = *reinterpret_cast<const v8*>(s_p + p_place(col, s * 2 + half));
+      if (two) w[1] = *reinterpret_cast<const v8*>(s_p + p_place(32 + col, s * 2 + half));
+#pragma unroll
+      for (int d = 0; d < DT; d++) {
+        s16x4 v[2];
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+          const int key = s * 16 + t * 8 + half * 4 + (lane & 15) / 4;
+          const int at = wave * 128 + d * 32 + (lane & 16) + (lane & 3) * 4;
+          v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(s_k[buf] + lat_place(key, at / 8) + (at & 4) * 2));
+        }
+        const v8 vt = __builtin_bit_cast(v8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        o[0][d] = T::mfma32(vt, w[0], o[0][d]);
+        if (two) o[1][d] = T::mfma32(vt, w[1], o[1][d]);
+      }
+    }
+    buf ^= 1;
+    if (more) keep_tile(buf);
+    __syncthreads();
+  }
+  // sums of a row: two key halves times two lane halves
+  s_sum[wj * 2 + half][rr] = l;
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    bool nan = false;
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) nan |= o[i][d][e] != o[i][d][e];
+    const uint64_t b = __ballot(nan);
+    if (lane == 0 && b) atomicOr(&s_nan[i], (uint32_t)(b | b >> 32));
+  }
+  __syncthreads();
+  float* part_o = a.work + it.index * partial_floats<kLatValue>(kLatRows);
+  float* part_ml = part_o + kLatRows * kLatValue;
+  auto finish = [&](int x, int64_t row, int hh, float log2_max, float sum) {
+    if (it.splits > 1) {
+      part_ml[x * 2] = log2_max;
+      part_ml[x * 2 + 1] = sum;
+    } else if (a.lse) {
+      a.lse[row * a.q_heads + hh] = sum == 0.f ? -INFINITY : (log2_max + log2f(sum)) * kLn2;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const int x = i * 32 + col;
+    const float sum = s_sum[0][x] + s_sum[1][x] + s_sum[2][x] + s_sum[3][x];
+    if (x >= rows_tile || ((s_nan[i] >> col) & 1)) continue;
+    const int tx = token(x), hx = head(x, tx);
+    const int64_t row = it.q.q0 + tx;
+    elem* op = reinterpret_cast<elem*>(a.out) + row * a.out_stride[0] + hx * a.out_stride[1];
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const int dim = wave * 128 + d * 32 + e * 8 + half * 4;
+        const f32x4 y = {o[i][d][e * 4], o[i][d][e * 4 + 1], o[i][d][e * 4 + 2], o[i][d][e * 4 + 3]};
+        if (it.splits > 1) {
+          *reinterpret_cast<f32x4*>(part_o + x * kLatValue + dim) = y;
+        } else {
+          typedef elem e4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<e4*>(op + dim) = __builtin_convertvector(y * inv, e4);
+        }
+      }
+    if (wave == 0 && half == 0) finish(x, row, hx, m[i] == -INFINITY ? -INFINITY : m[i] * c, sum);
+  }
+  // rows that came out NaN, shared out over the waves (the tiles are done with)
+  float* s_q = reinterpret_cast<float*>(s_k[0]) + wave * kLatDim;
+  for (int x = wave; x < rows_tile; x += 4) {
+    if (!((s_nan[x >> 5] >> (x & 31)) & 1)) continue;
+    const int tx = token(x), hx = head(x, tx);
+    float oo[kLatValue / 64], mm, ll;
+    exact_row<T, kLatDim, kLatValue>(a, it.s, it.q.q0 + tx, hx, before + tx, span, i0, i1, s_q, oo, &mm, &ll);
+    elem* op = reinterpret_cast<elem*>(a.out) + (it.q.q0 + tx) * a.out_stride[0] + hx * a.out_stride[1];
+    for (int d = 0; d < kLatValue / 64; d++) {
+      if (it.splits > 1) part_o[x * kLatValue + d * 64 + lane] = oo[d];
+      else op[d * 64 + lane] = (elem)(ll == 0.f ? 0.f : oo[d] / ll);
+    }
+    if (lane == 0) finish(x, it.q.q0 + tx, hx, mm, ll);
+  }
+}
+
 // Joins the splits of a row tile, a wave a row.  Workgroups of tiles that were not split have
 // nothing to do.
 template <class T, int DV, int R>
@@ -873,49 +1126,14 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   }
 }
 
-// ---------------------------------------------------------------- any call, one wave per (row, head)
-template <class T, int DK, int DV>
-__global__ __launch_bounds__(256) void k_attend_rows(AttendArgs a) {
-  __shared__ float s_q[4][DK];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (blockIdx.x == 0)
-    for (int64_t s = threadIdx.x; s < a.num_seqs; s += blockDim.x)
-      if (!sequence(a, s).ok) flag(a.err, kErrLengths, s);
-  const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
-  const int64_t row = unit / a.q_heads;
-  const int h = (int)(unit - row * a.q_heads);
-  if (row >= a.q_rows) return;
-  int64_t s = row;
-  if (a.q_start) {  // the last sequence that starts at or before the row
-    int64_t l = 0, r = a.num_seqs;
-    while (r - l > 1) {
-      const int64_t mid = (l + r) / 2;
-      if (a.q_start[mid] <= row) l = mid; else r = mid;
-    }
-    s = l;
-  }
-  if (s >= a.num_seqs) return;
-  const Seq q = sequence(a, s);
-  if (!q.ok || row < q.q0 || row >= q.q0 + q.m) return;
-  const int p = q.kv - q.m + (int)(row - q.q0);
-  const Span span = span_of(a, q.kv, p, p);
-  typedef typename T::elem elem;
-  float o[DV / 64], m, l;
-  exact_row<T, DK, DV>(a, s, row, h, p, span, 0, span.n, s_q[wave], o, &m, &l);
-  elem* op = reinterpret_cast<elem*>(a.out) + row * a.out_stride[0] + h * a.out_stride[1];
-#pragma unroll
-  for (int c = 0; c < DV / 64; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
-  if (a.lse && lane == 0) a.lse[row * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 // Row tiles of R rows that a call can have at most: each sequence rounds up once.
 int64_t most_tiles(const AttendArgs& a, int R) {
   return a.q_rows * a.group / R + (a.num_seqs < a.q_rows ? a.num_seqs : a.q_rows);
 }
 
-// The kernel for a call: rows of a row tile, 0 for the one that goes row by row.
+// The kernel for a call, by the rows of its row tiles.
 int tile_rows(const AttendArgs& a, int32_t head_dim) {
-  if (head_dim == 576) return 0;
+  if (head_dim == kLatDim) return kLatRows;
   return a.max_q * a.group <= 2 * kRowTile ? kRowTile : kTileRows;
 }
 
@@ -924,51 +1142,48 @@ int tile_rows(const AttendArgs& a, int32_t head_dim) {
 // most `target`.
 int64_t plan(AttendArgs* a, int R, int32_t num_cus) {
   a->min_split = R == kRowTile ? 128 : 256;
-  a->target = (int64_t)num_cus * (R == kRowTile ? 8 : 2);
+  a->target = (int64_t)num_cus * (R == kRowTile ? 8 : (R == kTileRows ? 2 : 1));
   const int64_t tiles = most_tiles(*a, R) * a->kv_heads;
   return a->max_kv <= a->min_split ? tiles : tiles + a->target;
 }
 
-template <class T, int D, int R>
-hipError_t launch_split(AttendArgs a, int32_t num_cus, hipStream_t stream) {
+template <class T, int DV, int R, class Kernel>
+hipError_t launch_split(Kernel kernel, AttendArgs a, int32_t num_cus, hipStream_t stream) {
   const int64_t items = a.items = plan(&a, R, num_cus);
   const int64_t joins = most_tiles(a, R) * a.kv_heads;
   if (items > 0x7fffffff || joins > 0x7fffffff) return hipErrorInvalidValue;
-  if (R == kRowTile)
-    k_attend_decode<T, D><<<dim3((unsigned)items), 256, 0, stream>>>(a);
-  else
-    k_attend_tiles<T, D><<<dim3((unsigned)items), 256, 0, stream>>>(a);
+  kernel<<<dim3((unsigned)items), 256, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.max_kv <= a.min_split) return e;
-  k_attend_join<T, D, R><<<dim3((unsigned)joins), 256, 0, stream>>>(a);
+  k_attend_join<T, DV, R><<<dim3((unsigned)joins), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hipStream_t stream) {
   (void)hipGetLastError();
-  const int R = tile_rows(a, head_dim);
-  if (R == kRowTile)
-    return head_dim == 64 ? launch_split<T, 64, kRowTile>(a, num_cus, stream)
-                          : launch_split<T, 128, kRowTile>(a, num_cus, stream);
-  if (R == kTileRows)
-    return head_dim == 64 ? launch_split<T, 64, kTileRows>(a, num_cus, stream)
-                          : launch_split<T, 128, kTileRows>(a, num_cus, stream);
-  const int64_t groups = (a.q_rows * a.q_heads + 3) / 4;
-  if (groups > 0x7fffffff) return hipErrorInvalidValue;
-  k_attend_rows<T, 576, 512><<<dim3((unsigned)groups), 256, 0, stream>>>(a);
-  return hipGetLastError();
+  switch (tile_rows(a, head_dim)) {
+    case kRowTile:
+      return head_dim == 64 ? launch_split<T, 64, kRowTile>(k_attend_decode<T, 64>, a, num_cus, stream)
+                            : launch_split<T, 128, kRowTile>(k_attend_decode<T, 128>, a, num_cus, stream);
+    case kTileRows:
+      return head_dim == 64 ? launch_split<T, 64, kTileRows>(k_attend_tiles<T, 64>, a, num_cus, stream)
+                            : launch_split<T, 128, kTileRows>(k_attend_tiles<T, 128>, a, num_cus, stream);
+    default:
+      return launch_split<T, kLatValue, kLatRows>(k_attend_latent<T>, a, num_cus, stream);
+  }
 }
 
 }  // namespace
 
 int64_t attend_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_cus) {
   const int R = tile_rows(args, head_dim);
-  if (R == 0 || args.q_rows <= 0 || args.num_seqs <= 0) return 0;
+  if (args.q_rows <= 0 || args.num_seqs <= 0) return 0;
   AttendArgs a = args;
   const int64_t items = plan(&a, R, num_cus);
   if (a.max_kv <= a.min_split) return 0;
-  return 4 * items * (head_dim == 64 ? partial_floats<64>(R) : partial_floats<128>(R));
+  return 4 * items * (head_dim == 64 ? partial_floats<64>(R) : head_dim == 128 ? partial_floats<128>(R)
+                                                                              : partial_floats<kLatValue>(R));
 }
 
 hipError_t launch_attend(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t num_cus, hipStream_t stream) {
