@@ -98,15 +98,42 @@ __device__ __forceinline__ bool visible(const AttendArgs& a, int p, int j) {
 
 constexpr uint32_t kNoSlot = 0xffffffffu;  // layers hold fewer rows: 2^32 of the smallest are 512 GiB
 
-// Slot of key j (below 2^31) of sequence s; kNoSlot for a bad table entry, which is reported.
-__device__ __forceinline__ uint32_t slot_of(const AttendArgs& a, int64_t s, uint32_t j) {
+// Slot of key j (below 2^31) of sequence s in two steps, so that a kernel can load a table entry long
+// before it needs the slot: a wait for a load waits for all that were issued before it.
+struct Entry {
+  int64_t page;      // what the table says
+  int64_t at;        // its place in the table, -1: no key
+  uint32_t rest;     // token inside the entry
+};
+__device__ __forceinline__ Entry entry_of(const AttendArgs& a, int64_t s, uint32_t j) {
   const uint32_t e = (uint32_t)(((uint64_t)j * a.entry_magic) >> a.entry_shift);  // j / entry
-  const int64_t t = a.table[s * a.table_stride + e];
-  if (t < 0 || t >= a.entries) {
-    flag(a.err, kErrIndex, s * a.table_stride + e);
+  Entry r;
+  r.at = s * a.table_stride + e;
+  r.rest = j - e * (uint32_t)a.entry;
+  r.page = a.table[r.at];
+  return r;
+}
+// kNoSlot for no key, and for a bad table entry, which is reported.
+__device__ __forceinline__ uint32_t slot_from(const AttendArgs& a, const Entry& e) {
+  if (e.at < 0) return kNoSlot;
+  if (e.page < 0 || e.page >= a.entries) {
+    flag(a.err, kErrIndex, e.at);
     return kNoSlot;
   }
-  return (uint32_t)(t * a.entry + (j - e * (uint32_t)a.entry));
+  return (uint32_t)e.page * (uint32_t)a.entry + e.rest;
+}
+__device__ __forceinline__ uint32_t slot_of(const AttendArgs& a, int64_t s, uint32_t j) {
+  return slot_from(a, entry_of(a, s, j));
+}
+
+// 16 bytes a lane from memory into LDS, lane i to lds + 16 i (lds the same in all lanes), past the
+// registers.  Nothing waits for it but lds_arrived, of the wave that loaded.
+__device__ __forceinline__ void lds_load(const uint8_t* from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
+}
+__device__ __forceinline__ void lds_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
 }
 
 // ---------------------------------------------------------------- one row, key by key
@@ -129,6 +156,7 @@ __device__ __forceinline__ void exact_row(const AttendArgs& a, int64_t s, int64_
 #pragma unroll
   for (int c = 0; c < ND; c++) o[c] = 0.f;
   const float scale = a.scale * kLog2e;
+#pragma unroll 1
   for (int base = i0; base < i1; base += 64) {
     const int i = base + lane;
     float x = -INFINITY;
@@ -140,6 +168,7 @@ __device__ __forceinline__ void exact_row(const AttendArgs& a, int64_t s, int64_
     if (slot != kNoSlot) {
       const v4u* kp = reinterpret_cast<const v4u*>(a.k_rows + 2 * ((int64_t)slot * a.k_row + (int64_t)hk * DK));
       x = 0.f;
+#pragma unroll 1
       for (int v = 0; v < DK / 8; v++) {
         const f32x8 kv = __builtin_convertvector(__builtin_bit_cast(typename T::v8, kp[v]), f32x8);
 #pragma unroll
@@ -340,12 +369,12 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   uint8_t* sv = s_v[wave];
   // Slot of the tile's key lane % 32, kNoSlot past the end and for a key that no row sees: with one
   // token a tile (decoding) that is every hidden key, whose values then are zeros in the product.
-  auto slots = [&](int base) {
+  auto entry = [&](int base) {
     const int i = base + (lane & 31);
-    if (i >= i1) return kNoSlot;
-    const int j = span.key(i);
-    if (p_first == p_last && !visible(a, p_first, j)) return kNoSlot;
-    return slot_of(a, it.s, (uint32_t)j);
+    const int j = span.key(i < i1 ? i : i0);
+    Entry e = {0, -1, 0};
+    if (i < i1 && (p_first != p_last || visible(a, p_first, j))) e = entry_of(a, it.s, (uint32_t)j);
+    return e;
   };
   v4u kreg[2][KS], vreg[VL];
   auto load_k = [&](uint32_t slot) {
@@ -367,8 +396,8 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
     }
   };
   int base = i0 + wave * kKeys;
-  uint32_t slot = base < i1 ? slots(base) : kNoSlot;
-  uint32_t slot_next = base + 128 < i1 ? slots(base + 128) : kNoSlot;
+  Entry next_entry = entry(base + 128);
+  uint32_t slot = slot_from(a, entry(base)), slot_next = kNoSlot;
   if (base < i1) {
     load_k(slot);
     load_v(slot);
@@ -381,8 +410,9 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
       for (int i = 0; i < KS; i++) st[t] = T::mfma16(__builtin_bit_cast(v8, kreg[t][i]), q[i], st[t]);
     const uint32_t there = (uint32_t)__ballot(slot != kNoSlot);
     const bool more = base + 128 < i1;
+    slot_next = slot_from(a, next_entry);
+    next_entry = entry(base + 256);
     if (more) load_k(slot_next);
-    const uint32_t slot_after = base + 256 < i1 ? slots(base + 256) : kNoSlot;
     // V into LDS, and the next tile's on its way
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -439,7 +469,6 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
       o[d] = T::mfma16(vt, wt, o[d]);
     }
     slot = slot_next;
-    slot_next = slot_after;
   }
   // Join the four waves: sums over values into LDS (over V, which is done with), 4 waves' of a row
   // tile at a time in two halves of the dims.
@@ -546,7 +575,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
 // The products are the decoding kernel's in their 32 x 32 form: S^T = K Q^T leaves a lane with one
 // row's scores of 32 of the 64 keys, 8 q + 4 (lane / 32) + r of each 32, which are the operand of
 // O^T += V^T P^T as they stand; V comes from LDS transposed, in that order of the keys.  The next tile
-// is loaded into registers while one is computed and goes to the other half of LDS: one barrier a tile.
+// is loaded into the other half of LDS while one is computed: one barrier a tile.
 //
 // The maximum that a row's weights are relative to is replaced only when it grows by more than
 // 2^8: until then weights of up to 2^8 are summed, which loses nothing in fp32 or as operands, and the
@@ -555,13 +584,23 @@ constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
 constexpr float kGrow = 8.f;
 
+// Which chunk of a K row lies at a place of it, and back: 16 rows' same chunk in 16 places.
 template <int D>
-__device__ __forceinline__ int k_place(int row, int chunk) {  // byte of a 16-byte chunk of a K row: 16
-  return row * D * 2 + (chunk ^ (D == 128 ? row & 15 : (row >> 1) & 7)) * 16;  // rows' same chunk in 16 places
+__device__ __forceinline__ int k_chunk(int row, int chunk) {
+  return chunk ^ (D == 128 ? row & 15 : (row >> 1) & 7);
 }
 template <int D>
-__device__ __forceinline__ int v_place(int row, int chunk) {  // of a V row: four rows' 32 dims side by side
-  return row * D * 2 + (chunk ^ (D == 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2)) * 16;
+__device__ __forceinline__ int k_place(int row, int chunk) {
+  return row * D * 2 + k_chunk<D>(row, chunk) * 16;
+}
+// Of a V row: four rows' 32 dims side by side.
+template <int D>
+__device__ __forceinline__ int v_chunk(int row, int chunk) {
+  return chunk ^ (D == 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2);
+}
+template <int D>
+__device__ __forceinline__ int v_place(int row, int chunk) {
+  return row * D * 2 + v_chunk<D>(row, chunk) * 16;
 }
 
 template <class T, int D>
@@ -571,7 +610,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   constexpr int KS = D / 16;                    // product steps over the head
   constexpr int DT = D / 32;                    // 32-dim tiles of the output
   constexpr int CH = D / 8;                     // 16-byte chunks of a row
-  constexpr int LD = kTileKeys * CH / 256;      // loads of a lane, K and V each
+  constexpr int LD = kTileKeys * CH / 256;      // loads of a wave, K and V each
   constexpr int BUF = kTileKeys * D * 2;        // bytes of a K or V tile
   __shared__ __align__(16) uint8_t s_k[2][BUF], s_v[2][BUF];
   __shared__ int64_t s_plan[8];
@@ -611,45 +650,41 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   const uint8_t* kb = a.k_rows + 2 * (int64_t)it.hk * D;
   const uint8_t* vb = a.v_rows + 2 * (int64_t)it.hk * D;
   const uint64_t k_row = 2 * a.k_row, v_row = 2 * a.v_row;
-  auto slots = [&](int base) -> uint32_t {  // of key `lane` of the tile
+  auto entry = [&](int base) {  // of key `lane` of the tile
     const int i = base + lane;
-    return i < i1 ? slot_of(a, it.s, (uint32_t)span.key(i)) : kNoSlot;
+    Entry e = {0, -1, 0};
+    if (i < i1) e = entry_of(a, it.s, (uint32_t)span.key(i));
+    return e;
   };
-  v4u kr[LD], vr[LD];
-  auto load = [&](uint32_t slot) {
+  // One instruction carries 64 chunks; the swizzle is in which chunk of its row a lane fetches.
+  auto load = [&](uint32_t slot, int buf) {
 #pragma unroll
     for (int x = 0; x < LD; x++) {
-      const int at = x * 256 + threadIdx.x;
-      const uint32_t sl = __shfl(slot, at / CH);
+      const int at = (x * 4 + wave) * 64 + lane, key = at / CH, place = at % CH;
+      const uint32_t sl = __shfl(slot, key);
       const uint64_t s64 = sl == kNoSlot ? 0 : sl;
-      kr[x] = *reinterpret_cast<const v4u*>(kb + s64 * k_row + (at % CH) * 16);
-      const v4u v = *reinterpret_cast<const v4u*>(vb + s64 * v_row + (at % CH) * 16);
-      vr[x] = sl == kNoSlot ? v4u{0, 0, 0, 0} : v;
-    }
-  };
-  auto keep_tile = [&](int buf) {
-#pragma unroll
-    for (int x = 0; x < LD; x++) {
-      const int at = x * 256 + threadIdx.x;
-      *reinterpret_cast<v4u*>(s_k[buf] + k_place<D>(at / CH, at % CH)) = kr[x];
-      *reinterpret_cast<v4u*>(s_v[buf] + v_place<D>(at / CH, at % CH)) = vr[x];
+      lds_load(kb + s64 * k_row + k_chunk<D>(key, place) * 16, lds_offset(s_k[buf] + (x * 4 + wave) * 1024));
+      lds_load(vb + s64 * v_row + v_chunk<D>(key, place) * 16, lds_offset(s_v[buf] + (x * 4 + wave) * 1024));
     }
   };
   f32x16 o[DT] = {};
   float m = -INFINITY, l = 0.f;
-  uint32_t slot = slots(i0), slot_next = slots(i0 + kTileKeys);
-  if (i0 < i1) {
-    load(slot);
-    keep_tile(0);
-  }
+  Entry next_entry = entry(i0 + kTileKeys);
+  uint32_t slot = slot_from(a, entry(i0));
+  if (i0 < i1) load(slot, 0);
+  lds_arrived();
   __syncthreads();
   int buf = 0;
   for (int base = i0; base < i1; base += kTileKeys) {
     const uint64_t there = __ballot(slot != kNoSlot);
-    const bool more = base + kTileKeys < i1;
-    if (more) load(slot_next);
-    slot = slot_next;
-    slot_next = slots(base + 2 * kTileKeys);
+    slot = slot_from(a, next_entry);
+    next_entry = entry(base + 2 * kTileKeys);
+    if (base + kTileKeys < i1) load(slot, buf ^ 1);
+    if (there != ~0ull) {  // what was fetched in place of no key must not reach the product: its value is zero
+      for (int x = threadIdx.x; x < kTileKeys * CH; x += 256)
+        if (!((there >> (x / CH)) & 1)) *reinterpret_cast<v4u*>(s_v[buf] + x * 16) = v4u{0, 0, 0, 0};
+      __syncthreads();
+    }
     f32x16 st[2] = {};
 #pragma unroll
     for (int u = 0; u < 2; u++)
@@ -712,7 +747,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
       }
     }
     buf ^= 1;
-    if (more) keep_tile(buf);
+    lds_arrived();
     __syncthreads();
   }
   l += __shfl_xor(l, 32);
@@ -793,12 +828,13 @@ constexpr int kLatDim = 576;
 constexpr int kLatValue = 512;
 constexpr int kLatBytes = kLatDim * 2;
 
-// Byte of a 16-byte chunk of a key row.  Rows start 128 bytes apart in the banks; the swizzle of
-// 8 chunks spreads both 16 rows' same chunk and four rows' 64 bytes of dims over all banks.
-__device__ __forceinline__ int lat_place(int row, int chunk) {
-  const int f = ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
-  return row * kLatBytes + (chunk ^ f) * 16;
+// Which 16-byte chunk of a key row lies at a place of it, and back.  Rows start 128 bytes apart in the
+// banks; the swizzle of 8 chunks spreads both 16 rows' same chunk and four rows' 64 bytes of dims over
+// all banks.
+__device__ __forceinline__ int lat_chunk(int row, int chunk) {
+  return chunk ^ (((row >> 1) & 1) << 2 | ((row >> 2) & 3));
 }
+__device__ __forceinline__ int lat_place(int row, int chunk) { return row * kLatBytes + lat_chunk(row, chunk) * 16; }
 
 template <class T>
 __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
@@ -847,44 +883,41 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
     }
   }
   const uint64_t k_row = 2 * a.k_row;
-  auto slots = [&](int base) -> uint32_t {
+  auto entry = [&](int base) {  // of key `lane` of the tile
     const int i = base + lane;
-    return i < i1 ? slot_of(a, it.s, (uint32_t)span.key(i)) : kNoSlot;
+    Entry e = {0, -1, 0};
+    if (i < i1) e = entry_of(a, it.s, (uint32_t)span.key(i));
+    return e;
   };
-  v4u kr[LD];
-  auto load = [&](uint32_t slot) {
+  auto load = [&](uint32_t slot, int buf) {
 #pragma unroll
     for (int x = 0; x < LD; x++) {
-      const int at = x * 256 + threadIdx.x;
-      const uint32_t sl = __shfl(slot, at / CH);
-      const v4u v = *reinterpret_cast<const v4u*>(a.k_rows + (sl == kNoSlot ? 0 : sl) * k_row + (at % CH) * 16);
-      kr[x] = sl == kNoSlot ? v4u{0, 0, 0, 0} : v;
-    }
-  };
-  auto keep_tile = [&](int buf) {
-#pragma unroll
-    for (int x = 0; x < LD; x++) {
-      const int at = x * 256 + threadIdx.x;
-      *reinterpret_cast<v4u*>(s_k[buf] + lat_place(at / CH, at % CH)) = kr[x];
+      const int at = (x * 4 + wave) * 64 + lane, key = at / CH;
+      const uint32_t sl = __shfl(slot, key);
+      lds_load(a.k_rows + (sl == kNoSlot ? 0 : sl) * k_row + lat_chunk(key, at - key * CH) * 16,
+               lds_offset(s_k[buf] + (x * 4 + wave) * 1024));
     }
   };
   auto p_place = [&](int row, int chunk) { return row * kLatKeys * 2 + (chunk ^ (row & 7)) * 16; };
   f32x16 o[2][DT] = {};
   float m[2] = {-INFINITY, -INFINITY}, l = 0.f;  // maxima of rows col and 32 + col; this lane's part of row rr's sum
-  uint32_t slot = slots(i0), slot_next = slots(i0 + kLatKeys);
-  if (i0 < i1) {
-    load(slot);
-    keep_tile(0);
-  }
+  Entry next_entry = entry(i0 + kLatKeys);
+  uint32_t slot = slot_from(a, entry(i0));
+  if (i0 < i1) load(slot, 0);
+  lds_arrived();
   if (threadIdx.x < 2) s_nan[threadIdx.x] = 0;
   __syncthreads();
   int buf = 0;
   for (int base = i0; base < i1; base += kLatKeys) {
     const uint64_t there = __ballot(slot != kNoSlot);
-    const bool more = base + kLatKeys < i1;
-    if (more) load(slot_next);
-    slot = slot_next;
-    slot_next = slots(base + 2 * kLatKeys);
+    slot = slot_from(a, next_entry);
+    next_entry = entry(base + 2 * kLatKeys);
+    if (base + kLatKeys < i1) load(slot, buf ^ 1);
+    if (there != ~0ull) {  // what was fetched in place of no key must not reach the product
+      for (int x = threadIdx.x; x < kLatKeys * CH; x += 256)
+        if (!((there >> (x / CH)) & 1)) *reinterpret_cast<v4u*>(s_k[buf] + x * 16) = v4u{0, 0, 0, 0};
+      __syncthreads();
+    }
     float x[16];
     if (scores) {
       f32x16 st = {};
@@ -965,7 +998,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
       }
     }
     buf ^= 1;
-    if (more) keep_tile(buf);
+    lds_arrived();
     __syncthreads();
   }
   // sums of a row: two key halves times two lane halves
