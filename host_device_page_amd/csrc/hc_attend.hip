@@ -12,6 +12,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "hc_forward.h"
 
 namespace hc {
@@ -240,7 +242,7 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t x) {  // inclusive
 
 // Finds item `want` of the list (256 threads; s_plan: 8 int64); false when the list is shorter.
 __device__ bool find_item(const AttendArgs& a, int R, int64_t want, int64_t* s_plan, Item* it) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t work = 0;
   Seq q;
   for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
@@ -335,7 +337,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   __shared__ int64_t s_plan[8];
   Item it;
   if (!find_item(a, kRowTile, blockIdx.x, s_plan, &it)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const int rows_all = it.q.m * a.group;
   const int r0 = it.tile * kRowTile;
@@ -616,7 +618,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   __shared__ int64_t s_plan[8];
   Item it;
   if (!find_item(a, kTileRows, blockIdx.x, s_plan, &it)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int64_t rows_all = (int64_t)it.q.m * a.group;
   const int64_t t0 = (int64_t)it.tile * kTileRows;
@@ -824,10 +826,12 @@ constexpr int kLatValue = 512;
 constexpr int kLatBytes = kLatDim * 2;
 constexpr int kLatTile = kLatKeys * kLatBytes;
 
-// The swizzle of a key row's 16-byte chunks: chunk x lies at place x ^ lat_swizzle(row).  Rows start 128
-// bytes apart in the banks; this spreads both 16 rows' same chunk and the four rows by 64 bytes of
-// a transposing read over all banks.
-__device__ __forceinline__ int lat_swizzle(int row) { return ((row >> 1) & 1) << 2 | ((row >> 2) & 3); }
+// A tile lies in LDS in nine blocks of 64 dims: [dims / 64][key][128 bytes], so that one instruction
+// brings 8 keys' 128 bytes and a lane's nine of a key differ by constants.  Inside the 128 bytes 16-byte
+// chunk x lies at place x ^ lat_swizzle(key), which spreads both 16 keys' same chunk and the four
+// keys by 64 bytes of a transposing read over all banks.
+constexpr int kLatBlock = kLatKeys * 128;
+__device__ __forceinline__ int lat_swizzle(int key) { return ((key >> 1) & 1) << 2 | ((key >> 2) & 3); }
 
 // What both latent kernels share: their item's place in the sequence, and the tiles on their way.
 struct Latent {
@@ -873,23 +877,34 @@ __device__ __forceinline__ bool latent_item(const AttendArgs& a, int R, int64_t*
   return true;
 }
 
-// A tile of keys into LDS, by all four waves; slot: of key `lane`.
+// 16 bytes a lane from memory into LDS, lane i to lds + 16 i (lds the same in all lanes), past the
+// registers, from OFFSET bytes on in memory (the instruction adds its offset to both addresses).
+template <int OFFSET>
+__device__ __forceinline__ void lds_load_at(const uint8_t* from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds), "v"(from),
+               "n"(OFFSET)
+               : "memory");
+}
+template <int... B>
+__device__ __forceinline__ void latent_load_key(const uint8_t* from, uint32_t lds, std::integer_sequence<int, B...>) {
+  (lds_load_at<B * 128>(from, lds + B * (kLatBlock - 128)), ...);
+}
+// A tile of keys into LDS, 16 of them a wave; slot: of key `lane`.
 __device__ __forceinline__ void latent_load(const AttendArgs& a, uint32_t slot, const uint8_t* to) {
-  constexpr int CH = kLatDim / 8;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-  for (int x = 0; x < kLatKeys * CH / 256; x++) {
-    const int at = (x * 4 + wave) * 64 + lane, key = at / CH;
+  for (int x = 0; x < 2; x++) {
+    const int key = wave * 16 + x * 8 + lane / 8;
     const uint32_t sl = __shfl(slot, key);
-    lds_load(a.k_rows + (uint64_t)(sl == kNoSlot ? 0 : sl) * kLatBytes + ((at - key * CH) ^ lat_swizzle(key)) * 16,
-             lds_offset(to + (x * 4 + wave) * 1024));
+    latent_load_key(a.k_rows + (uint64_t)(sl == kNoSlot ? 0 : sl) * kLatBytes + ((lane & 7) ^ lat_swizzle(key)) * 16,
+                    lds_offset(to) + (wave * 16 + x * 8) * 128, std::make_integer_sequence<int, kLatBytes / 128>());
   }
 }
 
 // What was fetched in place of no key must not reach the product.
 __device__ __forceinline__ void latent_clear(uint64_t there, uint8_t* tile) {
   for (int x = threadIdx.x; x < kLatTile / 16; x += 256)
-    if (!((there >> (x / (kLatDim / 8))) & 1)) *reinterpret_cast<v4u*>(tile + x * 16) = v4u{0, 0, 0, 0};
+    if (!((there >> (x % (kLatBlock / 16) / 8)) & 1)) *reinterpret_cast<v4u*>(tile + x * 16) = v4u{0, 0, 0, 0};
   __syncthreads();
 }
 
@@ -898,7 +913,7 @@ template <class T>
 __device__ __forceinline__ void latent_again(const AttendArgs& a, const Latent& t, const uint32_t* s_nan, float* s_q,
                                              float* part_o, float* part_ml) {
   typedef typename T::elem elem;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int x = wave; x < t.rows; x += 4) {
     if (!((s_nan[x >> 5] >> (x & 31)) & 1)) continue;
     const int tok = t.token(a, x), h = t.head(a, x, tok);
@@ -949,7 +964,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
   __shared__ int64_t s_plan[8];
   Latent t;
   if (!latent_item(a, R, s_plan, &t)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
   v8 q[RB][KS];
@@ -969,12 +984,12 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
   // chunk 4 i + quad of key 16 wave + col: the swizzle changes its lowest three bits, two cases of i
   const int key = wave * 16 + col;
   int k_at[2];
-  for (int i = 0; i < 2; i++) k_at[i] = key * kLatBytes + ((i * 4 + quad) ^ lat_swizzle(key)) * 16;
+  for (int i = 0; i < 2; i++) k_at[i] = key * 128 + ((i * 4 + quad) ^ lat_swizzle(key)) * 16;
   // dims 128 wave + 16 d of keys 32 s + 16 t + 4 quad + (lane & 15) / 4: four cases of d
   const int vkey = quad * 4 + (lane & 15) / 4;
   int v_at[4];
   for (int d = 0; d < 4; d++)
-    v_at[d] = vkey * kLatBytes + wave * 256 + ((d * 2 + ((lane & 3) >> 1)) ^ lat_swizzle(vkey)) * 16 + (lane & 1) * 8;
+    v_at[d] = wave * 2 * kLatBlock + vkey * 128 + ((d * 2 + ((lane & 3) >> 1)) ^ lat_swizzle(vkey)) * 16 + (lane & 1) * 8;
   f32x4 o[RB][DT] = {};
   float m[RB], l[RB];
   for (int b = 0; b < RB; b++) m[b] = -INFINITY, l[b] = 0.f;
@@ -998,7 +1013,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
     for (int b = 0; b < RB; b++) st[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < KS; i++) {
-      const v8 k = *reinterpret_cast<const v8*>(s_k + off + k_at[i & 1] + (i >> 1) * 128);
+      const v8 k = *reinterpret_cast<const v8*>(s_k + off + k_at[i & 1] + (i >> 1) * kLatBlock);
 #pragma unroll
       for (int b = 0; b < RB; b++) st[b] = T::mfma16(k, q[b][i], st[b]);
     }
@@ -1073,7 +1088,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
 #pragma unroll
           for (int u = 0; u < 2; u++)
             v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4)(s_k + off + v_at[d & 3] + (d >> 2) * 128 + (s * 32 + u * 16) * kLatBytes));
+                (lds_s16x4)(s_k + off + v_at[d & 3] + (d >> 2) * kLatBlock + (s * 32 + u * 16) * 128));
           const v8 vt = __builtin_bit_cast(v8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
           for (int b = 0; b < RB; b++) o[b][d] = T::mfma16(vt, w[b], o[b][d]);
@@ -1145,7 +1160,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   __shared__ int64_t s_plan[8];
   Latent t;
   if (!latent_item(a, kLatRows, s_plan, &t)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int wi = wave >> 1, wj = wave & 1;
   const int rr = wi * 32 + col;  // this lane's row of the scores
@@ -1165,13 +1180,13 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   // chunk 2 i + half of key 32 j + col: the swizzle changes its lowest three bits, four cases of i
   const int key = wj * 32 + col;
   int k_at[4];
-  for (int i = 0; i < 4; i++) k_at[i] = key * kLatBytes + ((i * 2 + half) ^ lat_swizzle(key)) * 16;
+  for (int i = 0; i < 4; i++) k_at[i] = key * 128 + ((i * 2 + half) ^ lat_swizzle(key)) * 16;
   // dims 128 wave + 32 d of keys 16 s + 8 u + 4 half + (lane & 15) / 4: two cases of d, two of u
   int v_at[2][2];
   for (int d = 0; d < 2; d++)
     for (int u = 0; u < 2; u++) {
       const int k = u * 8 + half * 4 + (lane & 15) / 4;
-      v_at[d][u] = k * kLatBytes + wave * 256 + ((d * 4 + (lane & 16) / 8 + (lane & 3) / 2) ^ lat_swizzle(k)) * 16 +
+      v_at[d][u] = wave * 2 * kLatBlock + k * 128 + ((d * 4 + (lane & 16) / 8 + (lane & 3) / 2) ^ lat_swizzle(k)) * 16 +
                    (lane & 1) * 8;
     }
   auto p_place = [&](int row, int chunk) { return row * kLatKeys * 2 + (chunk ^ (row & 7)) * 16; };
@@ -1203,7 +1218,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
       if (g + 1 < KS / G) {
 #pragma unroll
         for (int i = 0; i < G; i++)
-          k[(g + 1) & 1][i] = *reinterpret_cast<const v8*>(s_k + off + k_at[i & 3] + (g + 1) * 128);
+          k[(g + 1) & 1][i] = *reinterpret_cast<const v8*>(s_k + off + k_at[i & 3] + (g + 1) * kLatBlock);
       }
 #pragma unroll
       for (int i = 0; i < G; i++) st = T::mfma32(k[g & 1][i], q[g * G + i], st);
@@ -1272,7 +1287,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
 #pragma unroll
           for (int u = 0; u < 2; u++)
             v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4)(s_k + off + v_at[d & 1][u] + (d >> 1) * 128 + s * 16 * kLatBytes));
+                (lds_s16x4)(s_k + off + v_at[d & 1][u] + (d >> 1) * kLatBlock + s * 16 * 128));
           const v8 vt = __builtin_bit_cast(v8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
           o[0][d] = T::mfma32(vt, w0, o[0][d]);
           o[1][d] = T::mfma32(vt, w1, o[1][d]);
@@ -1335,7 +1350,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   typedef typename T::elem elem;
   __shared__ int64_t s_plan[8];
   // item `splits * tile` of the list is found by walking tiles instead of items
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t work = 0;
   Seq q;
   for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
