@@ -286,12 +286,10 @@ __device__ bool find_item(const AttendArgs& a, int R, int64_t want, int64_t* s_p
   if (!found) return false;
   it->s = s_plan[0];
   it->splits = (int32_t)s_plan[1];
-  const int64_t rest = s_plan[2];
-  const int64_t unit = rest / it->splits;
+  const int64_t rest = s_plan[2], unit = rest / it->splits, back = unit / a.kv_heads;
   it->split = (int32_t)(rest - unit * it->splits);
-  const int64_t back = unit / a.kv_heads;
-  it->tile = (int32_t)(s_plan[3] - 1 - back);  // the last rows see the most keys and come first
   it->hk = (int32_t)(unit - back * a.kv_heads);
+  it->tile = (int32_t)(s_plan[3] - 1 - back);  // the last rows see the most keys and come first
   it->q = sequence(a, it->s);
   it->index = want;
   __syncthreads();
@@ -1363,7 +1361,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   work = (s_plan[0] + s_plan[1] + s_plan[2] + s_plan[3]) * a.kv_heads;
   int64_t C = (work + a.target - 1) / a.target;
   C = C < a.min_split ? a.min_split : C;
-  const int64_t want = blockIdx.x;
+  const int64_t want = blockIdx.x / a.join_parts;  // a workgroup does four rows of a tile
   int64_t tiles = 0, items = 0;
   bool found = false;
   for (int64_t s0 = 0; s0 < a.num_seqs && !found; s0 += 256) {
@@ -1402,19 +1400,20 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   if (!found) return;
   const int64_t s = s_plan[0], splits = s_plan[1], unit = s_plan[2];
   if (splits <= 1) return;
+  const int64_t back = unit / a.kv_heads;
+  const int hk = (int)(unit - back * a.kv_heads);
   const int64_t first = s_plan[3] + unit * splits;
   // a q_start that goes back (reported) can make more items than the call has room for
   if (first + splits > a.items) return;
   q = sequence(a, s);
-  const int64_t back = unit / a.kv_heads;
   const int64_t tile = s_plan[4] - 1 - back;
-  const int hk = (int)(unit - back * a.kv_heads);
   constexpr int ND = DV / 64;
   const int64_t left = (int64_t)q.m * a.group - tile * R;
-  for (int rr = wave; rr < R && rr < left; rr += 4) {
+  const int rr = (int)(blockIdx.x % a.join_parts) * 4 + wave;
+  if (rr < left) {
     float m = -INFINITY, l = 0.f, o[ND] = {};
 #pragma unroll 4
-    for (int64_t k = 0; k < splits; k++) {
+    for (int k = 0; k < (int)splits; k++) {
       const float* po = a.work + (first + k) * partial_floats<DV>(R);
       const float pm = po[R * DV + rr * 2], pl = po[R * DV + rr * 2 + 1];
       float v[ND];
@@ -1450,26 +1449,39 @@ int tile_rows(const AttendArgs& a, int32_t head_dim) {
   return rows <= 2 * kRowTile ? kRowTile : kTileRows;
 }
 
-// How the list of items is made for a call of tiles of R rows, and the number of items at most:
-// a split of C keys has at least `min_split` of them, and the whole call's keys over C is at
-// most `target`.
-int64_t plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus) {
-  const bool latent = head_dim == kLatDim;
-  a->min_split = latent || R == kRowTile ? 128 : 256;
-  a->target = (int64_t)num_cus * (latent ? 1 : (R == kRowTile ? 8 : 2));
-  const int64_t tiles = most_tiles(*a, R) * a->kv_heads;
-  return a->max_kv <= a->min_split ? tiles : tiles + a->target;
+// How the list of items is made for a call of tiles of R rows, and the number of items at most: a split of
+// C keys has at least `min_split` of them, and the whole call's keys over C is at most `target`.
+// Calls of many rows are split only when their row tiles, which the host knows, do not fill the GPU:
+// else one launch does all.
+struct Plan {
+  int64_t items, joins;  // joins: workgroups of the second launch, 0: no split can be
+};
+Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus) {
+  const bool latent = head_dim == kLatDim, few = R <= 32;
+  a->min_split = few ? 128 : 256;
+  a->target = (int64_t)num_cus * (latent ? 1 : (few ? 8 : 2));
+  Plan p = {most_tiles(*a, R) * a->kv_heads, 0};
+  const int64_t most_splits = (a->max_kv + a->min_split - 1) / a->min_split;
+  if (most_splits > 1 && (few || a->q_rows * a->group / R * a->kv_heads < a->target)) {
+    const int64_t rows = a->max_q * a->group < R ? a->max_q * a->group : R;  // of a tile at most
+    a->join_parts = (int32_t)((rows + 3) / 4);
+    p.joins = p.items * a->join_parts;
+    p.items = p.items * most_splits < p.items + a->target ? p.items * most_splits : p.items + a->target;
+  } else {
+    a->min_split = a->max_kv + 1;
+  }
+  a->items = p.items;
+  return p;
 }
 
 template <class T, int DV, int R, class Kernel>
 hipError_t launch_split(Kernel kernel, AttendArgs a, int32_t num_cus, hipStream_t stream) {
-  const int64_t items = a.items = plan(&a, R, DV == kLatValue ? kLatDim : DV, num_cus);
-  const int64_t joins = most_tiles(a, R) * a.kv_heads;
-  if (items > 0x7fffffff || joins > 0x7fffffff) return hipErrorInvalidValue;
-  kernel<<<dim3((unsigned)items), 256, 0, stream>>>(a);
+  const Plan p = plan(&a, R, DV == kLatValue ? kLatDim : DV, num_cus);
+  if (p.items > 0x7fffffff || p.joins > 0x7fffffff) return hipErrorInvalidValue;
+  kernel<<<dim3((unsigned)p.items), 256, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.max_kv <= a.min_split) return e;
-  k_attend_join<T, DV, R><<<dim3((unsigned)joins), 256, 0, stream>>>(a);
+  if (e != hipSuccess || p.joins == 0) return e;
+  k_attend_join<T, DV, R><<<dim3((unsigned)p.joins), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -1494,9 +1506,9 @@ int64_t attend_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_c
   const int R = tile_rows(args, head_dim);
   if (args.q_rows <= 0 || args.num_seqs <= 0) return 0;
   AttendArgs a = args;
-  const int64_t items = plan(&a, R, head_dim, num_cus);
-  if (a.max_kv <= a.min_split) return 0;
-  return 4 * items * (head_dim == 64 ? partial_floats<64>(R) : head_dim == 128 ? partial_floats<128>(R)
+  const Plan p = plan(&a, R, head_dim, num_cus);
+  if (p.joins == 0) return 0;
+  return 4 * p.items * (head_dim == 64 ? partial_floats<64>(R) : head_dim == 128 ? partial_floats<128>(R)
                                                                               : partial_floats<kLatValue>(R));
 }
 

@@ -55,6 +55,7 @@ struct AttendArgs {
   int64_t target, min_split, items;    // how the work is split (set by launch_attend)
   uint32_t entry_magic, entry_shift;   // j / entry == (j * magic) >> shift for j < 2^31
   int32_t q_heads, kv_heads, group, entry, causal;
+  int32_t join_parts;                  // workgroups of the joining launch to a row tile
   float scale;
 };
 // Bytes of workspace that launch_attend needs for these sizes.

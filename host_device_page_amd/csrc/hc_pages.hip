@@ -26,6 +26,8 @@ constexpr int64_t kPiece = (int64_t)kThreads * 16 * kUnroll;
 constexpr int kScanThreads = 1024;
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(1))) const v4u* gload_t;
+typedef __attribute__((address_space(1))) v4u* gstore_t;
 
 __device__ __forceinline__ void flag(int32_t* err, int bit, int64_t pos) {
   atomicOr(err, bit);
@@ -49,14 +51,15 @@ __device__ __forceinline__ void copy_piece(const Geom& g, int b, int64_t l, int6
                                            int64_t bytes) {
   const int64_t page = page_bytes(g, b, g.P);
   const uint64_t base = g.sub[b].layers[l];
-  const v4u* src = reinterpret_cast<const v4u*>(base + (uint64_t)(from * page + off));
-  v4u* dst = reinterpret_cast<v4u*>(base + (uint64_t)(to * page + off));
+  const gload_t src = reinterpret_cast<gload_t>(base + (uint64_t)(from * page + off));
+  const gstore_t dst = reinterpret_cast<gstore_t>(base + (uint64_t)(to * page + off));
   const int vecs = (int)((bytes - off < kPiece ? bytes - off : kPiece) / 16);
+  // every lane loads, past the end the last vector: loads under a condition do not leave together
   v4u v[kUnroll];
 #pragma unroll
   for (int k = 0; k < kUnroll; k++) {
     const int i = k * kThreads + threadIdx.x;
-    if (i < vecs) v[k] = src[i];
+    v[k] = src[i < vecs ? i : vecs - 1];
   }
 #pragma unroll
   for (int k = 0; k < kUnroll; k++) {
@@ -81,20 +84,19 @@ Pieces layer_pieces(const Geom& g) {
   return p;
 }
 
-// Copies unit u of a list of pairs: pair-major, then layer, then piece.  `pair` gives pair i's
-// pages and the rows of it that move (0: nothing).
+// Copies unit u of a list of n pairs: layer-major, then pair, then piece, so that what is in flight is
+// many pages of one layer and not one page of many layers, whose addresses differ by a layer's
+// power of two.  `pair` gives pair i's pages and the rows of it that move (0: nothing).
 template <class Pair>
-__device__ __forceinline__ void copy_unit(const Geom& g, const Pieces& pc, int64_t u, const Pair& pair) {
+__device__ __forceinline__ void copy_unit(const Geom& g, const Pieces& pc, int64_t n, int64_t u, const Pair& pair) {
   const int32_t per_layer = pc.end[g.nsub - 1];
-  const int64_t per_pair = (int64_t)per_layer * g.L;
-  const int64_t i = u / per_pair;
-  const int64_t rest = u - i * per_pair;
-  const int64_t l = rest / per_layer;
-  const int32_t piece = (int32_t)(rest - l * per_layer);
+  const int64_t row = u / per_layer;
+  const int32_t piece = (int32_t)(u - row * per_layer);
+  const int64_t l = row / n, i = row - l * n;
   int b = 0;
   while (piece >= pc.end[b]) b++;
   int64_t from, to, rows;
-  pair(i, &from, &to, &rows, rest == 0);
+  pair(i, &from, &to, &rows, piece == 0 && l == 0);
   if (rows <= 0) return;
   const int64_t off = (int64_t)(piece - (b ? pc.end[b - 1] : 0)) * kPiece;
   const int64_t bytes = page_bytes(g, b, rows);
@@ -102,11 +104,12 @@ __device__ __forceinline__ void copy_unit(const Geom& g, const Pieces& pc, int64
 }
 
 __global__ __launch_bounds__(kThreads) void k_copy_pages(Geom g, Pieces pc, const int64_t* __restrict__ src,
-                                                         const int64_t* __restrict__ dst, int64_t units,
+                                                         const int64_t* __restrict__ dst, int64_t n,
                                                          int32_t* __restrict__ err) {
   const int64_t pages = g.S / g.P;
+  const int64_t units = n * g.L * pc.end[g.nsub - 1];
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
-    copy_unit(g, pc, u, [&](int64_t i, int64_t* from, int64_t* to, int64_t* rows, bool first) {
+    copy_unit(g, pc, n, u, [&](int64_t i, int64_t* from, int64_t* to, int64_t* rows, bool first) {
       *from = src[i];
       *to = dst[i];
       const bool ok = *from >= 0 && *from < pages && *to >= 0 && *to < pages;
@@ -188,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void k_fork(Geom g, Pieces pc, ForkArgs a
     a.out[i * a.out_stride + j] = j < len / g.P ? a.table.entries[r * a.table.stride + j] : -1;
   }
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
-    copy_unit(g, pc, u, [&](int64_t i, int64_t* from, int64_t* to, int64_t* rows, bool first) {
+    copy_unit(g, pc, a.n, u, [&](int64_t i, int64_t* from, int64_t* to, int64_t* rows, bool first) {
       const int64_t r = a.parents[i];
       const int64_t len = length(r);
       *rows = len % g.P;
@@ -286,9 +289,10 @@ __global__ __launch_bounds__(kThreads) void k_compact(Geom g, Pieces pc, PageTab
     const int64_t p = t.entries[s * t.stride + j];
     out[s * out_stride + j] = j < n && p >= 0 && p < pages ? (int64_t)w.mark[p] : p;
   }
-  const int64_t units = w.head[1] * g.L * pc.end[g.nsub - 1];
+  const int64_t moves = w.head[1];
+  const int64_t units = moves * g.L * pc.end[g.nsub - 1];
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
-    copy_unit(g, pc, u, [&](int64_t i, int64_t* from, int64_t* to, int64_t* rows, bool) {
+    copy_unit(g, pc, moves, u, [&](int64_t i, int64_t* from, int64_t* to, int64_t* rows, bool) {
       *from = w.from[i];
       *to = w.to[i];
       *rows = g.P;
@@ -319,7 +323,7 @@ hipError_t launch_copy_pages(const Geom& g, const int64_t* src, const int64_t* d
   const Pieces pc = layer_pieces(g);
   const int64_t units = n * g.L * pc.end[g.nsub - 1];
   (void)hipGetLastError();
-  k_copy_pages<<<dim3(grid_of(units, num_cus)), kThreads, 0, stream>>>(g, pc, src, dst, units, err);
+  k_copy_pages<<<dim3(grid_of(units, num_cus)), kThreads, 0, stream>>>(g, pc, src, dst, n, err);
   return hipGetLastError();
 }
 
