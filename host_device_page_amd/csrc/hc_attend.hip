@@ -98,6 +98,20 @@ __device__ __forceinline__ bool visible(const AttendArgs& a, int p, int j) {
   return !a.causal | ((j <= p) & ((a.window == 0) | (p - j < a.window) | (j < a.sinks)));
 }
 
+// Of the 64 keys at positions base, base + 1, ... of a span those that a row at position p sees, a bit
+// each; `there`: those that are there at all.  In positions of the list: not past p, and past p - window or
+// below sinks (a window starts at or before p, so the sinks in front of it are never past p).
+__device__ __forceinline__ uint64_t first_bits(int n) {  // n of them: none below 0, all from 64 on
+  return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+__device__ __forceinline__ uint64_t sees(const AttendArgs& a, const Span& s, uint64_t there, int p, int base) {
+  if (!a.causal) return there;
+  const int at = p - s.lo + s.sk - base;  // the row's own key
+  uint64_t m = there & first_bits(at + 1);
+  if (a.window > 0) m &= first_bits(a.sinks - base) | ~first_bits(at - a.window + 1);
+  return m;
+}
+
 constexpr uint32_t kNoSlot = 0xffffffffu;  // layers hold fewer rows: 2^32 of the smallest are 512 GiB
 
 // Slot of key j (below 2^31) of sequence s in two steps, so that a kernel can load a table entry long
@@ -240,13 +254,22 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t x) {  // inclusive
   return x;
 }
 
-// Finds item `want` of the list (256 threads; s_plan: 8 int64); false when the list is shorter.
-__device__ bool find_item(const AttendArgs& a, int R, int64_t want, int64_t* s_plan, Item* it) {
+// What the joining launch has to know of an item, behind the partial results.
+struct Part {
+  int64_t splits;  // of the tile whose first split the item is, else 0
+  int64_t q0, m, tile_hk;
+};
+
+// Finds item blockIdx.x of the list (256 threads; s_plan: 8 int64); false when the list is shorter.
+// `parts`: where the items' Parts are kept, when there is a joining launch.
+__device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s_plan, Part* parts, Item* it) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t want = blockIdx.x;
   int64_t work = 0;
-  Seq q;
+  Seq q = {0, 0, 0, true};
+  PlanCount c = {0, 0};
   for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
-    const PlanCount c = plan_count(a, s, R, &q);
+    c = plan_count(a, s, R, &q);
     if (blockIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
     work += c.tiles * c.n;
   }
@@ -260,46 +283,62 @@ __device__ bool find_item(const AttendArgs& a, int R, int64_t want, int64_t* s_p
   bool found = false;
   for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 256) {
     const int64_t s = s0 + threadIdx.x;
-    PlanCount c = {0, 0};
-    if (s < a.num_seqs) c = plan_count(a, s, R, &q);
+    if (a.num_seqs > 256) {  // else they are at hand
+      c = {0, 0};
+      if (s < a.num_seqs) c = plan_count(a, s, R, &q);
+    }
     const int64_t splits = c.n <= C ? 1 : (c.n + C - 1) / C;
     const int64_t mine = c.tiles * splits * a.kv_heads;
     const int64_t incl = wave_prefix(mine);
     __syncthreads();
-    if (lane == 63) s_plan[4 + wave] = incl;
+    if (lane == 63) s_plan[wave] = incl;
     __syncthreads();
     int64_t at = before + incl - mine;
-    for (int w = 0; w < wave; w++) at += s_plan[4 + w];
-    for (int w = 0; w < 4; w++) before += s_plan[4 + w];
+    for (int w = 0; w < 4; w++) {
+      if (w < wave) at += s_plan[w];
+      before += s_plan[w];
+    }
+    found = want < before;
+    __syncthreads();
     if (want >= at && want < at + mine) {
       s_plan[0] = s;
       s_plan[1] = splits;
       s_plan[2] = want - at;
       s_plan[3] = c.tiles;
+      s_plan[4] = q.q0;
+      s_plan[5] = q.kv;
+      s_plan[6] = q.m;
     }
-    if (want < before) {
-      found = true;
-      break;
-    }
+    if (found) break;
   }
   __syncthreads();
-  if (!found) return false;
-  it->s = s_plan[0];
-  it->splits = (int32_t)s_plan[1];
-  const int64_t rest = s_plan[2], unit = rest / it->splits, back = unit / a.kv_heads;
-  it->split = (int32_t)(rest - unit * it->splits);
-  it->hk = (int32_t)(unit - back * a.kv_heads);
-  it->tile = (int32_t)(s_plan[3] - 1 - back);  // the last rows see the most keys and come first
-  it->q = sequence(a, it->s);
-  it->index = want;
+  if (found) {
+    it->s = s_plan[0];
+    it->splits = (int32_t)s_plan[1];
+    const int64_t rest = s_plan[2], unit = rest / it->splits, back = unit / a.kv_heads;
+    it->split = (int32_t)(rest - unit * it->splits);
+    it->hk = (int32_t)(unit - back * a.kv_heads);
+    it->tile = (int32_t)(s_plan[3] - 1 - back);  // the last rows see the most keys and come first
+    it->q = {s_plan[4], (int)s_plan[5], (int)s_plan[6], true};
+    it->index = want;
+  }
+  if (a.join_parts > 0 && threadIdx.x == 0) {
+    Part p = {0, 0, 0, 0};
+    if (found && it->split == 0) p = {it->splits, it->q.q0, it->q.m, (int64_t)it->tile * a.kv_heads + it->hk};
+    parts[want] = p;
+  }
   __syncthreads();
-  return true;
+  return found;
 }
 
 // Floats of a partial result: per row the sum over values, then maximum and sum of weights.
 template <int DV>
 __host__ __device__ constexpr int64_t partial_floats(int R) {
   return (int64_t)R * (DV + 2);
+}
+template <int DV, int R>
+__device__ __forceinline__ Part* parts_of(const AttendArgs& a) {
+  return reinterpret_cast<Part*>(a.work + a.items * partial_floats<DV>(R));
 }
 
 // ---------------------------------------------------------------- few rows: decoding
@@ -334,7 +373,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   __shared__ float s_m[4][kRowTile], s_l[4][kRowTile];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item(a, kRowTile, blockIdx.x, s_plan, &it)) return;
+  if (!find_item(a, kRowTile, s_plan, parts_of<D, kRowTile>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const int rows_all = it.q.m * a.group;
@@ -429,12 +468,9 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; e++) x[e] = st[e / 4][e % 4] * scale;
     if (!whole) {
+      const uint32_t see = (uint32_t)sees(a, span, there, p, base) >> (quad * 4);
 #pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const int k = (e / 4) * 16 + quad * 4 + e % 4;
-        const bool sees = ((there >> k) & 1) & visible(a, p, span.key(base + k));
-        x[e] = sees ? x[e] : -INFINITY;
-      }
+      for (int e = 0; e < 8; e++) x[e] = (see >> (e / 4 * 16 + e % 4)) & 1 ? x[e] : -INFINITY;
     }
     float top = x[0];
 #pragma unroll
@@ -604,7 +640,7 @@ __device__ __forceinline__ int v_place(int row, int chunk) {
 }
 
 template <class T, int D>
-__global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArgs a) {
   typedef typename T::v8 v8;
   typedef typename T::elem elem;
   constexpr int KS = D / 16;                    // product steps over the head
@@ -615,7 +651,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   __shared__ __align__(16) uint8_t s_k[2][BUF], s_v[2][BUF];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item(a, kTileRows, blockIdx.x, s_plan, &it)) return;
+  if (!find_item(a, kTileRows, s_plan, parts_of<D, kTileRows>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int64_t rows_all = (int64_t)it.q.m * a.group;
@@ -699,12 +735,10 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
     const bool whole = there == ~0ull && (!a.causal || (span.key(base + kTileKeys - 1) <= p_first &&
                                                         (a.window == 0 || p_last - span.key(base) < a.window)));
     if (!whole) {
+      const uint64_t see = sees(a, span, there, p, base) >> (half * 4);
+      const uint32_t part[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
 #pragma unroll
-      for (int e = 0; e < 32; e++) {
-        const int k = (e / 16) * 32 + (e % 16) / 4 * 8 + half * 4 + e % 4;
-        const bool sees = ((there >> k) & 1) & visible(a, p, span.key(base + k));
-        x[e] = sees ? x[e] : -INFINITY;
-      }
+      for (int e = 0; e < 32; e++) x[e] = (part[e / 16] >> (e % 16 / 4 * 8 + e % 4)) & 1 ? x[e] : -INFINITY;
     }
     float top = x[0];
 #pragma unroll
@@ -858,8 +892,9 @@ struct Latent {
   }
 };
 
-__device__ __forceinline__ bool latent_item(const AttendArgs& a, int R, int64_t* s_plan, Latent* t) {
-  if (!find_item(a, R, blockIdx.x, s_plan, &t->it)) return false;
+template <int R>
+__device__ __forceinline__ bool latent_item(const AttendArgs& a, int64_t* s_plan, Latent* t) {
+  if (!find_item(a, R, s_plan, parts_of<kLatValue, R>(a), &t->it)) return false;
   const Seq& q = t->it.q;
   const int64_t rows_all = (int64_t)q.m * a.group;
   t->t0 = (int64_t)t->it.tile * R;
@@ -961,7 +996,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
   __shared__ uint32_t s_nan[1];
   __shared__ int64_t s_plan[8];
   Latent t;
-  if (!latent_item(a, R, s_plan, &t)) return;
+  if (!latent_item<R>(a, s_plan, &t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
@@ -1020,12 +1055,9 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
     for (int b = 0; b < RB; b++) {
       float x[4] = {st[b][0], st[b][1], st[b][2], st[b][3]};
       if (!whole) {
+        const uint32_t see = (uint32_t)(sees(a, t.span, there, p[b], base) >> (wave * 16)) >> (quad * 4);
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const int k = wave * 16 + quad * 4 + e;
-          const bool sees = ((there >> k) & 1) & visible(a, p[b], t.span.key(base + k));
-          x[e] = sees ? x[e] : -INFINITY;
-        }
+        for (int e = 0; e < 4; e++) x[e] = (see >> e) & 1 ? x[e] : -INFINITY;
       }
       float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       y = fmaxf(y, __shfl_xor(y, 16));
@@ -1157,7 +1189,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   __shared__ uint32_t s_nan[2];
   __shared__ int64_t s_plan[8];
   Latent t;
-  if (!latent_item(a, kLatRows, s_plan, &t)) return;
+  if (!latent_item<kLatRows>(a, s_plan, &t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int wi = wave >> 1, wj = wave & 1;
@@ -1225,12 +1257,9 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
 #pragma unroll
     for (int e = 0; e < 16; e++) x[e] = st[e];
     if (!t.whole(a, base, there)) {
+      const uint32_t see = (uint32_t)(sees(a, t.span, there, p, base) >> (wj * 32)) >> (half * 4);
 #pragma unroll
-      for (int e = 0; e < 16; e++) {
-        const int k = wj * 32 + e / 4 * 8 + half * 4 + e % 4;
-        const bool sees = ((there >> k) & 1) & visible(a, p, t.span.key(base + k));
-        x[e] = sees ? x[e] : -INFINITY;
-      }
+      for (int e = 0; e < 16; e++) x[e] = (see >> (e / 4 * 8 + e % 4)) & 1 ? x[e] : -INFINITY;
     }
     float y = x[0];
 #pragma unroll
@@ -1341,100 +1370,44 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   latent_again<T>(a, t, s_nan, reinterpret_cast<float*>(s_k) + wave * kLatDim, part_o, part_ml);
 }
 
-// Joins the splits of a row tile, a wave a row.  Workgroups of tiles that were not split have
-// nothing to do.
+// Joins the splits of a row tile, a wave a row.  A workgroup looks at one item; all but the first split of
+// a tile that was split have nothing to do.
 template <class T, int DV, int R>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   typedef typename T::elem elem;
-  __shared__ int64_t s_plan[8];
-  // item `splits * tile` of the list is found by walking tiles instead of items
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t work = 0;
-  Seq q;
-  for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
-    const PlanCount c = plan_count(a, s, R, &q);
-    work += c.tiles * c.n;
-  }
-  for (int d = 1; d < 64; d <<= 1) work += __shfl_xor(work, d);
-  if (lane == 0) s_plan[wave] = work;
-  __syncthreads();
-  work = (s_plan[0] + s_plan[1] + s_plan[2] + s_plan[3]) * a.kv_heads;
-  int64_t C = (work + a.target - 1) / a.target;
-  C = C < a.min_split ? a.min_split : C;
-  const int64_t want = blockIdx.x / a.join_parts;  // a workgroup does four rows of a tile
-  int64_t tiles = 0, items = 0;
-  bool found = false;
-  for (int64_t s0 = 0; s0 < a.num_seqs && !found; s0 += 256) {
-    const int64_t s = s0 + threadIdx.x;
-    PlanCount c = {0, 0};
-    if (s < a.num_seqs) c = plan_count(a, s, R, &q);
-    const int64_t splits = c.n <= C ? 1 : (c.n + C - 1) / C;
-    const int64_t mine = c.tiles * a.kv_heads;
-    const int64_t t_incl = wave_prefix(mine), i_incl = wave_prefix(mine * splits);
-    __syncthreads();
-    if (lane == 63) {
-      s_plan[wave] = t_incl;
-      s_plan[4 + wave] = i_incl;
-    }
-    __syncthreads();
-    int64_t t_at = tiles + t_incl - mine, i_at = items + i_incl - mine * splits;
-    for (int w = 0; w < wave; w++) {
-      t_at += s_plan[w];
-      i_at += s_plan[4 + w];
-    }
-    for (int w = 0; w < 4; w++) {
-      tiles += s_plan[w];
-      items += s_plan[4 + w];
-    }
-    __syncthreads();
-    if (want >= t_at && want < t_at + mine) {
-      s_plan[0] = s;
-      s_plan[1] = splits;
-      s_plan[2] = want - t_at;
-      s_plan[3] = i_at;
-      s_plan[4] = c.tiles;
-    }
-    found = want < tiles;
-  }
-  __syncthreads();
-  if (!found) return;
-  const int64_t s = s_plan[0], splits = s_plan[1], unit = s_plan[2];
-  if (splits <= 1) return;
-  const int64_t back = unit / a.kv_heads;
-  const int hk = (int)(unit - back * a.kv_heads);
-  const int64_t first = s_plan[3] + unit * splits;
+  const int64_t first = blockIdx.x / a.join_parts;
+  const Part p = parts_of<DV, R>(a)[first];
   // a q_start that goes back (reported) can make more items than the call has room for
-  if (first + splits > a.items) return;
-  q = sequence(a, s);
-  const int64_t tile = s_plan[4] - 1 - back;
-  constexpr int ND = DV / 64;
-  const int64_t left = (int64_t)q.m * a.group - tile * R;
+  if (p.splits <= 1 || first + p.splits > a.items) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t tile = p.tile_hk / a.kv_heads;
+  const int hk = (int)(p.tile_hk - tile * a.kv_heads);
   const int rr = (int)(blockIdx.x % a.join_parts) * 4 + wave;
-  if (rr < left) {
-    float m = -INFINITY, l = 0.f, o[ND] = {};
+  const int64_t r = tile * R + rr;
+  if (rr >= R || r >= p.m * a.group) return;
+  constexpr int ND = DV / 64;
+  float m = -INFINITY, l = 0.f, o[ND] = {};
 #pragma unroll 4
-    for (int k = 0; k < (int)splits; k++) {
-      const float* po = a.work + (first + k) * partial_floats<DV>(R);
-      const float pm = po[R * DV + rr * 2], pl = po[R * DV + rr * 2 + 1];
-      float v[ND];
+  for (int k = 0; k < (int)p.splits; k++) {
+    const float* po = a.work + (first + k) * partial_floats<DV>(R);
+    const float pm = po[R * DV + rr * 2], pl = po[R * DV + rr * 2 + 1];
+    float v[ND];
 #pragma unroll
-      for (int c = 0; c < ND; c++) v[c] = po[rr * DV + c * 64 + lane];
-      const float next = fmaxf(m, pm);
-      const float zero = next == -INFINITY ? 0.f : next;
-      const float keep = __builtin_amdgcn_exp2f(m - zero), add = __builtin_amdgcn_exp2f(pm - zero);
-      m = next;
-      l = l * keep + pl * add;
+    for (int c = 0; c < ND; c++) v[c] = po[rr * DV + c * 64 + lane];
+    const float next = fmaxf(m, pm);
+    const float zero = next == -INFINITY ? 0.f : next;
+    const float keep = __builtin_amdgcn_exp2f(m - zero), add = __builtin_amdgcn_exp2f(pm - zero);
+    m = next;
+    l = l * keep + pl * add;
 #pragma unroll
-      for (int c = 0; c < ND; c++) o[c] = o[c] * keep + v[c] * add;
-    }
-    const int64_t r = tile * R + rr;
-    const int64_t rt = r / a.group;
-    const int h = hk * a.group + (int)(r - rt * a.group);
-    elem* op = reinterpret_cast<elem*>(a.out) + (q.q0 + rt) * a.out_stride[0] + h * a.out_stride[1];
-#pragma unroll
-    for (int c = 0; c < ND; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
-    if (a.lse && lane == 0) a.lse[(q.q0 + rt) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    for (int c = 0; c < ND; c++) o[c] = o[c] * keep + v[c] * add;
   }
+  const int64_t rt = r / a.group;
+  const int h = hk * a.group + (int)(r - rt * a.group);
+  elem* op = reinterpret_cast<elem*>(a.out) + (p.q0 + rt) * a.out_stride[0] + h * a.out_stride[1];
+#pragma unroll
+  for (int c = 0; c < ND; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
+  if (a.lse && lane == 0) a.lse[(p.q0 + rt) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Row tiles of R rows that a call can have at most: each sequence rounds up once.
@@ -1459,14 +1432,18 @@ struct Plan {
 Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus) {
   const bool latent = head_dim == kLatDim, few = R <= 32;
   a->min_split = few ? 128 : 256;
-  a->target = (int64_t)num_cus * (latent ? 1 : (few ? 8 : 2));
   Plan p = {most_tiles(*a, R) * a->kv_heads, 0};
+  // items that run at once: 8 or 2 workgroups a compute unit, and one of a latent cache, where the
+  // whole list, `tiles` longer than the target at most, should be one round
+  a->target = (int64_t)num_cus * (few ? 8 : 2);
+  if (latent) a->target = num_cus - p.items > num_cus / 2 ? num_cus - p.items : num_cus / 2;
+  a->join_parts = 0;
   const int64_t most_splits = (a->max_kv + a->min_split - 1) / a->min_split;
   if (most_splits > 1 && (few || a->q_rows * a->group / R * a->kv_heads < a->target)) {
     const int64_t rows = a->max_q * a->group < R ? a->max_q * a->group : R;  // of a tile at most
     a->join_parts = (int32_t)((rows + 3) / 4);
-    p.joins = p.items * a->join_parts;
     p.items = p.items * most_splits < p.items + a->target ? p.items * most_splits : p.items + a->target;
+    p.joins = p.items * a->join_parts;
   } else {
     a->min_split = a->max_kv + 1;
   }
@@ -1508,8 +1485,9 @@ int64_t attend_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_c
   AttendArgs a = args;
   const Plan p = plan(&a, R, head_dim, num_cus);
   if (p.joins == 0) return 0;
-  return 4 * p.items * (head_dim == 64 ? partial_floats<64>(R) : head_dim == 128 ? partial_floats<128>(R)
-                                                                              : partial_floats<kLatValue>(R));
+  const int64_t floats = head_dim == 64 ? partial_floats<64>(R) : head_dim == 128 ? partial_floats<128>(R)
+                                                                                 : partial_floats<kLatValue>(R);
+  return p.items * (4 * floats + (int64_t)sizeof(Part));
 }
 
 hipError_t launch_attend(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t num_cus, hipStream_t stream) {
