@@ -648,7 +648,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
   constexpr int CH = D / 8;                     // 16-byte chunks of a row
   constexpr int LD = kTileKeys * CH / 256;      // loads of a wave, K and V each
   constexpr int BUF = kTileKeys * D * 2;        // bytes of a K or V tile
-  __shared__ __align__(16) uint8_t s_k[2][BUF], s_v[2][BUF];
+  __shared__ __align__(256) uint8_t s_k[2][BUF], s_v[2][BUF];
   __shared__ int64_t s_plan[8];
   Item it;
   if (!find_item(a, kTileRows, s_plan, parts_of<D, kTileRows>(a), &it)) return;
@@ -683,24 +683,28 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
       q[i] = __builtin_bit_cast(v8, live ? x : v4u{0, 0, 0, 0});
     }
   }
-  const uint8_t* kb = a.k_rows + 2 * (int64_t)it.hk * D;
-  const uint8_t* vb = a.v_rows + 2 * (int64_t)it.hk * D;
-  const uint64_t k_row = 2 * a.k_row, v_row = 2 * a.v_row;
   auto entry = [&](int base) {  // of key `lane` of the tile
     const int i = base + lane;
     Entry e = {0, -1, 0};
     if (i < i1) e = entry_of(a, it.s, (uint32_t)span.key(i));
     return e;
   };
-  // One instruction carries 64 chunks; the swizzle is in which chunk of its row a lane fetches.
+  // One instruction carries 64 chunks; the swizzle is in which chunk of its row a lane fetches, the same
+  // one in every instruction.  Rows of K and V are equally far apart, so a key's lane works out where its
+  // rows are once and the lanes that fetch them only add their own part.
+  constexpr int RL = 64 / CH;  // rows of an instruction
+  const int from = wave * RL + lane / CH;  // a lane's first row, the next 4 RL on
+  const uint8_t* kl = a.k_rows + 2 * (int64_t)it.hk * D + k_chunk<D>(from, lane % CH) * 16;
+  const uint8_t* vl = a.v_rows + 2 * (int64_t)it.hk * D + v_chunk<D>(from, lane % CH) * 16;
   auto load = [&](uint32_t slot, int buf) {
+    const uint64_t row = slot == kNoSlot ? 0 : (uint64_t)slot * (2 * a.k_row);
+    const uint32_t lo = (uint32_t)row, hi = (uint32_t)(row >> 32);
 #pragma unroll
     for (int x = 0; x < LD; x++) {
-      const int at = (x * 4 + wave) * 64 + lane, key = at / CH, place = at % CH;
-      const uint32_t sl = __shfl(slot, key);
-      const uint64_t s64 = sl == kNoSlot ? 0 : sl;
-      lds_load(kb + s64 * k_row + k_chunk<D>(key, place) * 16, lds_offset(s_k[buf] + (x * 4 + wave) * 1024));
-      lds_load(vb + s64 * v_row + v_chunk<D>(key, place) * 16, lds_offset(s_v[buf] + (x * 4 + wave) * 1024));
+      const int key = x * 4 * RL + from;
+      const uint64_t at = (uint64_t)__shfl(hi, key) << 32 | __shfl(lo, key);
+      lds_load(kl + at, lds_offset(s_k[buf] + (x * 4 + wave) * 1024));
+      lds_load(vl + at, lds_offset(s_v[buf] + (x * 4 + wave) * 1024));
     }
   };
   f32x16 o[DT] = {};
