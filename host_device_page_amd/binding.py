@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import weakref
 
 import numpy as np
@@ -108,6 +109,12 @@ class hc_attend_desc(ctypes.Structure):
                 + [("q_stride", _I64 * 2), ("out_stride", _I64 * 2), ("workspace", _V), ("workspace_bytes", _I64)])
 
 
+# The same two structures as the methods below fill them, once per layer and token: packed bytes
+# take a fraction of the time of a ctypes structure.
+_STORE = struct.Struct("@6iq6P8qP")
+_ATTEND = struct.Struct("@9if8q6P4qPq")
+assert _STORE.size == ctypes.sizeof(hc_store_desc) and _ATTEND.size == ctypes.sizeof(hc_attend_desc)
+
 _D = ctypes.POINTER(hc_pool_desc)
 
 LOAD_LAYER_FN = ctypes.CFUNCTYPE(ctypes.c_int, _V, ctypes.c_int32, _V, _V, ctypes.c_int64, _V)
@@ -144,9 +151,9 @@ _SIGS = {
     "hc_rope_create": (ctypes.c_int, [ctypes.POINTER(hc_rope_desc), ctypes.POINTER(_V)]),
     "hc_rope_destroy": (ctypes.c_int, [_V]),
     "hc_rope_frequencies": (ctypes.c_int, [_V, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
-    "hc_store_tokens": (ctypes.c_int, [_V, ctypes.POINTER(hc_store_desc), _V]),
-    "hc_attend_workspace_bytes": (ctypes.c_int, [_V, ctypes.POINTER(hc_attend_desc), _I64P]),
-    "hc_attend": (ctypes.c_int, [_V, ctypes.POINTER(hc_attend_desc), _V]),
+    "hc_store_tokens": (ctypes.c_int, [_V, _V, _V]),
+    "hc_attend_workspace_bytes": (ctypes.c_int, [_V, _V, _I64P]),
+    "hc_attend": (ctypes.c_int, [_V, _V, _V]),
     "hc_copy_pages": (ctypes.c_int, [_V, _V, _V, _I64, _V]),
     "hc_fork_pages": (ctypes.c_int, [_V, _V, _I64, _I64, _I64, _V, _V, _I64, _V, _I64, _V, _I64, _V, _V]),
     "hc_pages_workspace_bytes": (ctypes.c_int, [_V, _I64P]),
@@ -410,9 +417,15 @@ def _in_use_on(stream, *tensors):
             t.record_stream(stream)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _torch_int64():
@@ -459,14 +472,27 @@ def _heads(x, what: str, like=None):
     """A (rows, heads, dim) CUDA tensor of bf16 or fp16 with contiguous heads, `like` another's dtype."""
     if not getattr(x, "is_cuda", False) or x.dim() != 3:
         raise TypeError(f"{what} must be a CUDA tensor of (rows, heads, dim)")
-    if str(x.dtype) not in _DTYPES or (like is not None and x.dtype != like.dtype):
+    if x.dtype not in _dtypes() or (like is not None and x.dtype != like.dtype):
         raise TypeError(f"{what} has dtype {x.dtype}" + (f", not {like.dtype}" if like is not None else ""))
     if x.shape[2] > 1 and x.stride(2) != 1:
         raise TypeError(f"{what}: the elements of a head must be contiguous")
     return x
 
 
-_DTYPES = {"torch.bfloat16": HC_BF16, "torch.float16": HC_F16}
+_dtype_codes = {}
+
+
+def _dtypes() -> dict:
+    if not _dtype_codes:
+        _dtype_codes.update({_torch().bfloat16: HC_BF16, _torch().float16: HC_F16})
+    return _dtype_codes
+
+
+def _device_list(x, what: str) -> int:
+    """_index_list(x, what, True), quickly for what passes."""
+    if getattr(x, "is_cuda", False) and x.dtype == _torch_int64() and x.is_contiguous():
+        return x.numel()
+    return _index_list(x, what, True)
 
 
 def _table(x, what: str):
@@ -482,9 +508,16 @@ def _on(stream, tensor, *used):
     """The stream a forward-pass call runs on: `stream`, whose work the tensors are then marked
     in use by, or torch's current stream of their device (as for torch's own operators)."""
     if stream is None:
-        return _V(_torch().cuda.current_stream(tensor.device).cuda_stream)
+        return _raw_stream(tensor)
     _in_use_on(stream, tensor, *used)
-    return _V(stream.cuda_stream)
+    return stream.cuda_stream
+
+
+def _raw_stream(tensor) -> int:
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's time
+    if raw is not None:
+        return raw(tensor.get_device())
+    return _torch().cuda.current_stream(tensor.device).cuda_stream
 
 
 class Pool:
@@ -626,33 +659,39 @@ class Pool:
         """Keys k (rotated) and values v of new tokens into their slots of one layer; queries q
         rotated into q_out (q itself: in place; None: a new tensor).  k, v, q: (tokens, heads,
         dim); v None for a latent cache.  Returns q_out."""
-        n = _index_list(slots, "slots", True)
-        _heads(k, "k")
-        for x, what in ((v, "v"), (q, "q"), (q_out, "q_out")):
-            if x is not None and _heads(x, what, k).shape[0] != n:
-                raise ValueError(f"{what} has {x.shape[0]} rows for {n} slots")
-        if k.shape[0] != n:
-            raise ValueError(f"k has {k.shape[0]} rows for {n} slots")
-        if v is not None and v.shape[1] != k.shape[1]:
-            raise ValueError("k and v differ in heads")
-        if q is not None and q_out is None:
-            q_out = q.new_empty(q.shape)
-        if q is None and q_out is not None:
+        n = _device_list(slots, "slots")
+        rows, kv_heads, dim = _heads(k, "k").shape
+        if rows != n:
+            raise ValueError(f"k has {rows} rows for {n} slots")
+        value_dim = v_at = v0 = v1 = q_heads = q_at = q0 = q1 = o_at = o0 = o1 = 0
+        if v is not None:
+            rows, heads, value_dim = _heads(v, "v", k).shape
+            if rows != n or heads != kv_heads:
+                raise ValueError(f"v has {rows} rows of {heads} heads for {n} slots and {kv_heads} heads")
+            v_at, (v0, v1, _) = v.data_ptr(), v.stride()
+        if q is not None:
+            rows, q_heads, q_dim = shape = _heads(q, "q", k).shape
+            if rows != n or q_dim != dim:
+                raise ValueError(f"q has {rows} rows of {q_dim} elements a head for {n} slots and {dim}")
+            if q_out is None:
+                q_out = q.new_empty(shape)
+            elif _heads(q_out, "q_out", k).shape != shape:
+                raise ValueError("q and q_out differ in shape")
+            q_at, (q0, q1, _), o_at, (o0, o1, _) = q.data_ptr(), q.stride(), q_out.data_ptr(), q_out.stride()
+        elif q_out is not None:
             raise ValueError("q_out without q")
-        if q is not None and (q.shape != q_out.shape or q.shape[2] != k.shape[2]):
-            raise ValueError("q, q_out and k must agree in heads and head_dim")
-        if rope is not None and _index_list(positions, "positions", True) != n:
-            raise ValueError("positions and slots differ in length")
-        pair = _I64 * 2
-        none = pair(0, 0)
-        d = hc_store_desc(layer, _DTYPES[str(k.dtype)], 0 if q is None else q.shape[1], k.shape[1], k.shape[2],
-                          0 if v is None else v.shape[2], n, _ptr(slots), _ptr(positions) if rope is not None else None,
-                          None if q is None else q.data_ptr(), None if q is None else q_out.data_ptr(), k.data_ptr(),
-                          None if v is None else v.data_ptr(), none if q is None else pair(*q.stride()[:2]),
-                          none if q is None else pair(*q_out.stride()[:2]), pair(*k.stride()[:2]),
-                          none if v is None else pair(*v.stride()[:2]), rope.handle if rope is not None else None)
-        s = _on(stream, k, slots, positions, q, q_out, v)
-        check(lib.hc_store_tokens(self.handle, ctypes.byref(d), s), "hc_store_tokens")
+        p_at = 0
+        if rope is not None:
+            if _device_list(positions, "positions") != n:
+                raise ValueError("positions and slots differ in length")
+            p_at = positions.data_ptr()
+        k0, k1, _ = k.stride()
+        d = _STORE.pack(layer, _dtype_codes[k.dtype], q_heads, kv_heads, dim, value_dim, n, slots.data_ptr(), p_at, q_at,
+                        o_at, k.data_ptr(), v_at, q0, q1, o0, o1, k0, k1, v0, v1,
+                        0 if rope is None else rope.handle.value)
+        rc = lib.hc_store_tokens(self.handle, d, _on(stream, k, slots, positions, q, q_out, v))
+        if rc:
+            check(rc, "hc_store_tokens")
         return q_out
 
     def attend(self, layer: int, q, table, kv_len, *, kv_heads: int, q_start=None, max_q: int | None = None,
@@ -666,46 +705,53 @@ class Pool:
         no sequence has more rows, or tokens (None: what q and the table hold).  value_dim
         below head_dim: a latent cache, whose key rows hold the values.  scale None:
         head_dim ** -0.5.  Returns (out, lse), lse None unless asked for."""
-        _heads(q, "q")
+        rows, heads, dim = _heads(q, "q").shape
         at, seqs, width, stride = _table(table, "table")
-        if _index_list(kv_len, "kv_len", True) != seqs:
+        if _device_list(kv_len, "kv_len") != seqs:
             raise ValueError("kv_len and table differ in sequences")
-        if q_start is not None and _index_list(q_start, "q_start", True) != seqs + 1:
-            raise ValueError("q_start must hold one entry more than there are sequences")
-        rows, heads, dim = q.shape
+        s_at = 0
+        if q_start is not None:
+            if _device_list(q_start, "q_start") != seqs + 1:
+                raise ValueError("q_start must hold one entry more than there are sequences")
+            s_at = q_start.data_ptr()
         if out is None:
             out = q.new_empty((rows, heads, dim if value_dim is None else value_dim))
-        elif _heads(out, "out", q).shape[:2] != (rows, heads):
-            raise ValueError("q and out differ in rows or heads")
-        elif value_dim is not None and out.shape[2] != value_dim:
-            raise ValueError("out is not value_dim wide")
+            wide = out.shape[2]
+        else:
+            o_rows, o_heads, wide = _heads(out, "out", q).shape
+            if o_rows != rows or o_heads != heads:
+                raise ValueError("q and out differ in rows or heads")
+            if value_dim is not None and wide != value_dim:
+                raise ValueError("out is not value_dim wide")
         entry = self.page_size if entry_tokens is None else entry_tokens
-        lse = q.new_empty((rows, heads), dtype=_torch().float32) if return_lse else None
-        pair = _I64 * 2
-        d = hc_attend_desc(layer, _DTYPES[str(q.dtype)], heads, kv_heads, dim, out.shape[2],
-                           1 if out.shape[2] != dim else 0, 1 if causal else 0, entry,
-                           dim ** -0.5 if scale is None else scale, window, sinks, seqs, rows,
-                           (1 if q_start is None else rows) if max_q is None else max_q,
-                           width * entry if max_kv is None else max_kv, width, stride, q.data_ptr(), out.data_ptr(),
-                           lse.data_ptr() if lse is not None else None,
-                           q_start.data_ptr() if q_start is not None else None, kv_len.data_ptr(), at,
-                           pair(*q.stride()[:2]), pair(*out.stride()[:2]))
+        lse, l_at = None, 0
+        if return_lse:
+            lse = q.new_empty((rows, heads), dtype=_torch().float32)
+            l_at = lse.data_ptr()
+        (q0, q1, _), (o0, o1, _) = q.stride(), out.stride()
+        args = (layer, _dtype_codes[q.dtype], heads, kv_heads, dim, wide, 1 if wide != dim else 0,
+                1 if causal else 0, entry, dim ** -0.5 if scale is None else scale, window, sinks, seqs, rows,
+                (1 if q_start is None else rows) if max_q is None else max_q,
+                width * entry if max_kv is None else max_kv, width, stride, q.data_ptr(), out.data_ptr(), l_at, s_at,
+                kv_len.data_ptr(), at, q0, q1, o0, o1)
         if workspace is None:
             need = _I64()
-            check(lib.hc_attend_workspace_bytes(self.handle, ctypes.byref(d), ctypes.byref(need)),
-                  "hc_attend_workspace_bytes")
+            rc = lib.hc_attend_workspace_bytes(self.handle, _ATTEND.pack(*args, 0, 0), ctypes.byref(need))
+            if rc:
+                check(rc, "hc_attend_workspace_bytes")
             if need.value:
                 workspace = q.new_empty(need.value, dtype=_torch().uint8)
-        if workspace is not None:
-            d.workspace, d.workspace_bytes = workspace.data_ptr(), _staging_bytes(workspace, "workspace")
-        s = _on(stream, q, table, kv_len, q_start, out, lse, workspace)
-        check(lib.hc_attend(self.handle, ctypes.byref(d), s), "hc_attend")
+        w_at, w_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), _staging_bytes(workspace, "workspace"))
+        rc = lib.hc_attend(self.handle, _ATTEND.pack(*args, w_at, w_bytes),
+                           _on(stream, q, table, kv_len, q_start, out, lse, workspace))
+        if rc:
+            check(rc, "hc_attend")
         return out, lse
 
     def copy_pages(self, src, dst, stream=None) -> None:
         """Pages src[i] to pages dst[i], in every layer and sub-buffer."""
-        n = _index_list(src, "src", True)
-        if _index_list(dst, "dst", True) != n:
+        n = _device_list(src, "src")
+        if _device_list(dst, "dst") != n:
             raise ValueError("src and dst differ in length")
         s = _on(stream, src, dst)
         check(lib.hc_copy_pages(self.handle, _V(_ptr(src)), _V(_ptr(dst)), n, s), "hc_copy_pages")
@@ -716,11 +762,11 @@ class Pool:
         (a one-element tensor)."""
         at, rows, width, stride = _table(table, "table")
         to, n, out_width, out_stride = _table(out, "out")
-        if _index_list(lens, "lens", True) != rows:
+        if _device_list(lens, "lens") != rows:
             raise ValueError("lens and table differ in rows")
-        if _index_list(parents, "parents", True) != n or out_width != width:
+        if _device_list(parents, "parents") != n or out_width != width:
             raise ValueError("out must have a row per parent and the table's width")
-        n_free = _index_list(free_pages, "free_pages", True)
+        n_free = _device_list(free_pages, "free_pages")
         used = table.new_empty(1)
         s = _on(stream, table, lens, parents, free_pages, out, used)
         check(lib.hc_fork_pages(self.handle, _V(at), rows, width, stride, _V(_ptr(lens)), _V(_ptr(parents)), n,
@@ -736,7 +782,7 @@ class Pool:
         """(pages, count): the pages that no table row names, ascending, in the first count[0]
         entries of `pages`."""
         at, rows, width, stride = _table(table, "table")
-        if _index_list(lens, "lens", True) != rows:
+        if _device_list(lens, "lens") != rows:
             raise ValueError("lens and table differ in rows")
         pages, count = table.new_empty(self.desc.device_slots // self.page_size), table.new_empty(1)
         work = self._pages_workspace(table)
@@ -750,7 +796,7 @@ class Pool:
         table with their new numbers.  Returns the number of live pages (a one-element tensor)."""
         at, rows, width, stride = _table(table, "table")
         to, out_rows, out_width, out_stride = _table(out, "out")
-        if _index_list(lens, "lens", True) != rows:
+        if _device_list(lens, "lens") != rows:
             raise ValueError("lens and table differ in rows")
         if (out_rows, out_width) != (rows, width):
             raise ValueError("out must have the table's shape")

@@ -260,15 +260,16 @@ struct Part {
   int64_t q0, m, tile_hk;
 };
 
-// Finds item blockIdx.x of the list (256 threads; s_plan: 8 int64); false when the list is shorter.
+// Finds item blockIdx.x of the list (W waves; s_plan: 8 int64); false when the list is shorter.
 // `parts`: where the items' Parts are kept, when there is a joining launch.
+template <int W = 4>
 __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s_plan, Part* parts, Item* it) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t want = blockIdx.x;
   int64_t work = 0;
   Seq q = {0, 0, 0, true};
   PlanCount c = {0, 0};
-  for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
+  for (int64_t s = threadIdx.x; s < a.num_seqs; s += 64 * W) {
     c = plan_count(a, s, R, &q);
     if (blockIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
     work += c.tiles * c.n;
@@ -276,14 +277,16 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
   for (int d = 1; d < 64; d <<= 1) work += __shfl_xor(work, d);
   if (lane == 0) s_plan[wave] = work;
   __syncthreads();
-  work = (s_plan[0] + s_plan[1] + s_plan[2] + s_plan[3]) * a.kv_heads;
+  work = 0;
+  for (int w = 0; w < W; w++) work += s_plan[w];
+  work *= a.kv_heads;
   int64_t C = (work + a.target - 1) / a.target;
   C = C < a.min_split ? a.min_split : C;
   int64_t before = 0;
   bool found = false;
-  for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 256) {
+  for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 64 * W) {
     const int64_t s = s0 + threadIdx.x;
-    if (a.num_seqs > 256) {  // else they are at hand
+    if (a.num_seqs > 64 * W) {  // else they are at hand
       c = {0, 0};
       if (s < a.num_seqs) c = plan_count(a, s, R, &q);
     }
@@ -294,7 +297,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
     if (lane == 63) s_plan[wave] = incl;
     __syncthreads();
     int64_t at = before + incl - mine;
-    for (int w = 0; w < 4; w++) {
+    for (int w = 0; w < W; w++) {
       if (w < wave) at += s_plan[w];
       before += s_plan[w];
     }
@@ -616,7 +619,10 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
 // The maximum that a row's weights are relative to is replaced only when it grows by more than
 // 2^8: until then weights of up to 2^8 are summed, which loses nothing in fp32 or as operands, and the
 // sums need not be scaled.
-constexpr int kTileRows = 128;
+#ifndef HC_TILE_ROWS
+#define HC_TILE_ROWS 128
+#endif
+constexpr int kTileRows = HC_TILE_ROWS;
 constexpr int kTileKeys = 64;
 constexpr float kGrow = 8.f;
 
@@ -639,24 +645,25 @@ __device__ __forceinline__ int v_place(int row, int chunk) {
   return row * D * 2 + v_chunk<D>(row, chunk) * 16;
 }
 
-template <class T, int D>
-__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArgs a) {
+template <class T, int D, int R>
+__global__ __launch_bounds__(2 * R, 2) void k_attend_tiles(AttendArgs a) {
   typedef typename T::v8 v8;
   typedef typename T::elem elem;
   constexpr int KS = D / 16;                    // product steps over the head
   constexpr int DT = D / 32;                    // 32-dim tiles of the output
   constexpr int CH = D / 8;                     // 16-byte chunks of a row
-  constexpr int LD = kTileKeys * CH / 256;      // loads of a wave, K and V each
+  constexpr int W = R / 32;                     // waves
+  constexpr int LD = kTileKeys * CH / (64 * W);      // loads of a wave, K and V each
   constexpr int BUF = kTileKeys * D * 2;        // bytes of a K or V tile
   __shared__ __align__(256) uint8_t s_k[2][BUF], s_v[2][BUF];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item(a, kTileRows, s_plan, parts_of<D, kTileRows>(a), &it)) return;
+  if (!find_item<W>(a, R, s_plan, parts_of<D, R>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int64_t rows_all = (int64_t)it.q.m * a.group;
-  const int64_t t0 = (int64_t)it.tile * kTileRows;
-  const int rows_tile = rows_all - t0 < kTileRows ? (int)(rows_all - t0) : kTileRows;
+  const int64_t t0 = (int64_t)it.tile * R;
+  const int rows_tile = rows_all - t0 < R ? (int)(rows_all - t0) : R;
   // this lane's row, and the positions of the tile's and the wave's first and last rows
   const int rr = wave * 32 + col;
   const bool live = rr < rows_tile;
@@ -693,7 +700,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
   // one in every instruction.  Rows of K and V are equally far apart, so a key's lane works out where its
   // rows are once and the lanes that fetch them only add their own part.
   constexpr int RL = 64 / CH;  // rows of an instruction
-  const int from = wave * RL + lane / CH;  // a lane's first row, the next 4 RL on
+  const int from = wave * RL + lane / CH;  // a lane's first row, the next W RL on
   const uint8_t* kl = a.k_rows + 2 * (int64_t)it.hk * D + k_chunk<D>(from, lane % CH) * 16;
   const uint8_t* vl = a.v_rows + 2 * (int64_t)it.hk * D + v_chunk<D>(from, lane % CH) * 16;
   auto load = [&](uint32_t slot, int buf) {
@@ -701,10 +708,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
     const uint32_t lo = (uint32_t)row, hi = (uint32_t)(row >> 32);
 #pragma unroll
     for (int x = 0; x < LD; x++) {
-      const int key = x * 4 * RL + from;
+      const int key = x * W * RL + from;
       const uint64_t at = (uint64_t)__shfl(hi, key) << 32 | __shfl(lo, key);
-      lds_load(kl + at, lds_offset(s_k[buf] + (x * 4 + wave) * 1024));
-      lds_load(vl + at, lds_offset(s_v[buf] + (x * 4 + wave) * 1024));
+      lds_load(kl + at, lds_offset(s_k[buf] + (x * W + wave) * 1024));
+      lds_load(vl + at, lds_offset(s_v[buf] + (x * W + wave) * 1024));
     }
   };
   f32x16 o[DT] = {};
@@ -721,10 +728,11 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
     next_entry = entry(base + 2 * kTileKeys);
     if (base + kTileKeys < i1) load(slot, buf ^ 1);
     if (there != ~0ull) {  // what was fetched in place of no key must not reach the product: its value is zero
-      for (int x = threadIdx.x; x < kTileKeys * CH; x += 256)
+      for (int x = threadIdx.x; x < kTileKeys * CH; x += 64 * W)
         if (!((there >> (x / CH)) & 1)) *reinterpret_cast<v4u*>(s_v[buf] + x * 16) = v4u{0, 0, 0, 0};
       __syncthreads();
     }
+    __builtin_amdgcn_s_setprio(1);  // waves in a product before others: two of a SIMD then fall out of step
     f32x16 st[2] = {};
 #pragma unroll
     for (int u = 0; u < 2; u++)
@@ -733,6 +741,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
         const v8 k = *reinterpret_cast<const v8*>(s_k[buf] + k_place<D>(u * 32 + col, i * 2 + half));
         st[u] = T::mfma32(k, q[i], st[u]);
       }
+    __builtin_amdgcn_s_setprio(0);
     float x[32];
 #pragma unroll
     for (int e = 0; e < 32; e++) x[e] = st[e / 16][e % 16];
@@ -764,6 +773,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
       sum += x[e];
     }
     l += sum;
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 4; s++) {
       f32x8 w;
@@ -784,6 +794,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
         o[d] = T::mfma32(vt, wt, o[d]);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     buf ^= 1;
     lds_arrived();
     __syncthreads();
@@ -799,8 +810,8 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void k_attend_tiles(AttendArg
   again = (again | again >> 32) & 0xffffffffu;
   const bool mine = live && !((again >> col) & 1);
   const float log2_max = m == -INFINITY ? -INFINITY : m * c;  // of the weights, in the joining kernel's unit
-  float* part_o = a.work + it.index * partial_floats<D>(kTileRows);
-  float* part_ml = part_o + kTileRows * D;
+  float* part_o = a.work + it.index * partial_floats<D>(R);
+  float* part_ml = part_o + R * D;
   elem* op = reinterpret_cast<elem*>(a.out) + row * a.out_stride[0] + h * a.out_stride[1];
   if (mine) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1459,7 +1470,8 @@ template <class T, int DV, int R, class Kernel>
 hipError_t launch_split(Kernel kernel, AttendArgs a, int32_t num_cus, hipStream_t stream) {
   const Plan p = plan(&a, R, DV == kLatValue ? kLatDim : DV, num_cus);
   if (p.items > 0x7fffffff || p.joins > 0x7fffffff) return hipErrorInvalidValue;
-  kernel<<<dim3((unsigned)p.items), 256, 0, stream>>>(a);
+  const int threads = DV != kLatValue && R > 32 ? 2 * R : 256;  // a wave to 32 rows of a tile
+  kernel<<<dim3((unsigned)p.items), threads, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.joins == 0) return e;
   k_attend_join<T, DV, R><<<dim3((unsigned)p.joins), 256, 0, stream>>>(a);
@@ -1477,8 +1489,8 @@ hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hi
   if (R == kRowTile)
     return head_dim == 64 ? launch_split<T, 64, kRowTile>(k_attend_decode<T, 64>, a, num_cus, stream)
                           : launch_split<T, 128, kRowTile>(k_attend_decode<T, 128>, a, num_cus, stream);
-  return head_dim == 64 ? launch_split<T, 64, kTileRows>(k_attend_tiles<T, 64>, a, num_cus, stream)
-                        : launch_split<T, 128, kTileRows>(k_attend_tiles<T, 128>, a, num_cus, stream);
+  return head_dim == 64 ? launch_split<T, 64, kTileRows>(k_attend_tiles<T, 64, kTileRows>, a, num_cus, stream)
+                        : launch_split<T, 128, kTileRows>(k_attend_tiles<T, 128, kTileRows>, a, num_cus, stream);
 }
 
 }  // namespace

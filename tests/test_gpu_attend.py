@@ -1,4 +1,5 @@
 """Attention over the device pool, against 64 bits."""
+import ctypes
 import math
 
 import pytest
@@ -283,8 +284,8 @@ def test_refusals():
     c.on["table"] = c.table.cuda()
     out, _ = c.run(return_lse=False)
     assert _ is None
-    d, _k = B.hc_attend_desc(), None
-    assert B.lib.hc_attend(c.pool.handle, d, None) == B.HC_ERR_INVALID
+    d = B.hc_attend_desc()
+    assert B.lib.hc_attend(c.pool.handle, ctypes.byref(d), None) == B.HC_ERR_INVALID
     c.close()
 
 
