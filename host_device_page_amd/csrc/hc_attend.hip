@@ -260,6 +260,25 @@ struct Part {
   int64_t q0, m, tile_hk;
 };
 
+// Keys of a split, for a call of `work` pairs of row tiles and keys.
+__device__ __forceinline__ int64_t split_keys(const AttendArgs& a, int64_t work) {
+  const int64_t C = (work * a.kv_heads + a.target - 1) / a.target;
+  return C < a.min_split ? a.min_split : C;
+}
+
+// Item `rest` of a sequence's: its row tiles from the last, whose rows see the most keys, to the first.
+__device__ __forceinline__ void set_item(const AttendArgs& a, Item* it, int64_t s, const Seq& q, int64_t tiles,
+                                         int64_t splits, int64_t rest) {
+  it->s = s;
+  it->splits = (int32_t)splits;
+  const int64_t unit = rest / it->splits, back = unit / a.kv_heads;
+  it->split = (int32_t)(rest - unit * it->splits);
+  it->hk = (int32_t)(unit - back * a.kv_heads);
+  it->tile = (int32_t)(tiles - 1 - back);
+  it->q = q;
+  it->index = blockIdx.x;
+}
+
 // Finds item blockIdx.x of the list (W waves; s_plan: 8 int64); false when the list is shorter.
 // `parts`: where the items' Parts are kept, when there is a joining launch.
 template <int W = 4>
@@ -269,68 +288,77 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
   int64_t work = 0;
   Seq q = {0, 0, 0, true};
   PlanCount c = {0, 0};
-  for (int64_t s = threadIdx.x; s < a.num_seqs; s += 64 * W) {
-    c = plan_count(a, s, R, &q);
-    if (blockIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
-    work += c.tiles * c.n;
-  }
-  for (int d = 1; d < 64; d <<= 1) work += __shfl_xor(work, d);
-  if (lane == 0) s_plan[wave] = work;
-  __syncthreads();
-  work = 0;
-  for (int w = 0; w < W; w++) work += s_plan[w];
-  work *= a.kv_heads;
-  int64_t C = (work + a.target - 1) / a.target;
-  C = C < a.min_split ? a.min_split : C;
-  int64_t before = 0;
   bool found = false;
-  for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 64 * W) {
-    const int64_t s = s0 + threadIdx.x;
-    if (a.num_seqs > 64 * W) {  // else they are at hand
-      c = {0, 0};
-      if (s < a.num_seqs) c = plan_count(a, s, R, &q);
+  if (a.num_seqs <= 4) {
+    // a few sequences: every thread goes over them by itself, without the steps of a reduction and a
+    // prefix over threads (1.5 us of a single sequence's decoding)
+    for (int64_t s = 0; s < a.num_seqs; s++) {
+      c = plan_count(a, s, R, &q);
+      if (blockIdx.x == 0 && threadIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
+      work += c.tiles * c.n;
     }
-    const int64_t splits = c.n <= C ? 1 : (c.n + C - 1) / C;
-    const int64_t mine = c.tiles * splits * a.kv_heads;
-    const int64_t incl = wave_prefix(mine);
-    __syncthreads();
-    if (lane == 63) s_plan[wave] = incl;
-    __syncthreads();
-    int64_t at = before + incl - mine;
-    for (int w = 0; w < W; w++) {
-      if (w < wave) at += s_plan[w];
-      before += s_plan[w];
+    const int64_t C = split_keys(a, work);
+    int64_t at = 0;
+    for (int64_t s = 0; s < a.num_seqs && !found; s++) {
+      if (a.num_seqs > 1) c = plan_count(a, s, R, &q);
+      const int64_t splits = c.n <= C ? 1 : (c.n + C - 1) / C, mine = c.tiles * splits * a.kv_heads;
+      found = want < at + mine;
+      if (found) set_item(a, it, s, q, c.tiles, splits, want - at);
+      at += mine;
     }
-    found = want < before;
-    __syncthreads();
-    if (want >= at && want < at + mine) {
-      s_plan[0] = s;
-      s_plan[1] = splits;
-      s_plan[2] = want - at;
-      s_plan[3] = c.tiles;
-      s_plan[4] = q.q0;
-      s_plan[5] = q.kv;
-      s_plan[6] = q.m;
+  } else {
+    for (int64_t s = threadIdx.x; s < a.num_seqs; s += 64 * W) {
+      c = plan_count(a, s, R, &q);
+      if (blockIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
+      work += c.tiles * c.n;
     }
-    if (found) break;
-  }
-  __syncthreads();
-  if (found) {
-    it->s = s_plan[0];
-    it->splits = (int32_t)s_plan[1];
-    const int64_t rest = s_plan[2], unit = rest / it->splits, back = unit / a.kv_heads;
-    it->split = (int32_t)(rest - unit * it->splits);
-    it->hk = (int32_t)(unit - back * a.kv_heads);
-    it->tile = (int32_t)(s_plan[3] - 1 - back);  // the last rows see the most keys and come first
-    it->q = {s_plan[4], (int)s_plan[5], (int)s_plan[6], true};
-    it->index = want;
+    for (int d = 1; d < 64; d <<= 1) work += __shfl_xor(work, d);
+    if (lane == 0) s_plan[wave] = work;
+    __syncthreads();
+    work = 0;
+    for (int w = 0; w < W; w++) work += s_plan[w];
+    const int64_t C = split_keys(a, work);
+    int64_t before = 0;
+    for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 64 * W) {
+      const int64_t s = s0 + threadIdx.x;
+      if (a.num_seqs > 64 * W) {  // else they are at hand
+        c = {0, 0};
+        if (s < a.num_seqs) c = plan_count(a, s, R, &q);
+      }
+      const int64_t splits = c.n <= C ? 1 : (c.n + C - 1) / C;
+      const int64_t mine = c.tiles * splits * a.kv_heads;
+      const int64_t incl = wave_prefix(mine);
+      __syncthreads();
+      if (lane == 63) s_plan[wave] = incl;
+      __syncthreads();
+      int64_t at = before + incl - mine;
+      for (int w = 0; w < W; w++) {
+        if (w < wave) at += s_plan[w];
+        before += s_plan[w];
+      }
+      found = want < before;
+      __syncthreads();
+      if (want >= at && want < at + mine) {
+        s_plan[0] = s;
+        s_plan[1] = splits;
+        s_plan[2] = want - at;
+        s_plan[3] = c.tiles;
+        s_plan[4] = q.q0;
+        s_plan[5] = q.kv;
+        s_plan[6] = q.m;
+      }
+      if (found) break;
+    }
+    __syncthreads();
+    if (found)
+      set_item(a, it, s_plan[0], {s_plan[4], (int)s_plan[5], (int)s_plan[6], true}, s_plan[3], s_plan[1], s_plan[2]);
+    __syncthreads();
   }
   if (a.join_parts > 0 && threadIdx.x == 0) {
     Part p = {0, 0, 0, 0};
     if (found && it->split == 0) p = {it->splits, it->q.q0, it->q.m, (int64_t)it->tile * a.kv_heads + it->hk};
     parts[want] = p;
   }
-  __syncthreads();
   return found;
 }
 
@@ -373,7 +401,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   constexpr int CH = D / 8;             // 16-byte chunks of a row
   constexpr int VL = kKeys * CH / 64;   // V loads of a lane
   __shared__ __align__(16) uint8_t s_v[4][kKeys * D * 2];
-  __shared__ float s_m[4][kRowTile], s_l[4][kRowTile];
+  __shared__ float s_m[4][kRowTile], s_l[4][kRowTile], s_q[4][D];
   __shared__ int64_t s_plan[8];
   Item it;
   if (!find_item(a, kRowTile, s_plan, parts_of<D, kRowTile>(a), &it)) return;
@@ -509,99 +537,82 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
     }
     slot = slot_next;
   }
-  // Join the four waves: sums over values into LDS (over V, which is done with), 4 waves' of a row
-  // tile at a time in two halves of the dims.
+  // Join the four waves through LDS (over V, which is done with): 16 threads to a row, 8 or 4 dims each.
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   if (lane < kRowTile) {
     s_m[wave][lane] = m;
     s_l[wave][lane] = l;
   }
+  __syncthreads();  // every wave is done with V: a wave's sums take more LDS than its values did
+  float* so = reinterpret_cast<float*>(&s_v[0][0]);  // [wave][row][D]
+  if (col < rows) {
+#pragma unroll
+    for (int d = 0; d < DT; d++) *reinterpret_cast<f32x4*>(so + (wave * kRowTile + col) * D + d * 16 + quad * 4) = o[d];
+  }
   __syncthreads();
-  float m_all = s_m[0][col];
-  for (int w = 1; w < 4; w++) m_all = fmaxf(m_all, s_m[w][col]);
+  constexpr int E = D / 16;
+  const int rr = threadIdx.x / 16, d0 = threadIdx.x % 16 * E;
+  const bool valid = rr < rows;  // all lanes stay: a row that came out NaN takes the whole wave
+  float m_all = s_m[0][rr];
+  for (int w = 1; w < 4; w++) m_all = fmaxf(m_all, s_m[w][rr]);
   const float zero = m_all == -INFINITY ? 0.f : m_all;
-  float l_all = 0.f;
-  for (int w = 0; w < 4; w++) l_all += s_l[w][col] * __builtin_amdgcn_exp2f(s_m[w][col] - zero);
-  const float mine = __builtin_amdgcn_exp2f(m - zero);
-  // s_v holds [wave][16 rows][D] floats in halves of D/2 dims: 4 * 16 * D/2 * 4 bytes
-  float* so = reinterpret_cast<float*>(&s_v[0][0]);
-  constexpr int H = D / 2;
-  float acc[2][kRowTile * H / 256];
+  float l_all = 0.f, acc[E] = {};
 #pragma unroll
-  for (int half = 0; half < 2; half++) {
-    if (half) __syncthreads();
+  for (int w = 0; w < 4; w++) {
+    const float f = __builtin_amdgcn_exp2f(s_m[w][rr] - zero);
+    l_all += s_l[w][rr] * f;
 #pragma unroll
-    for (int d = 0; d < DT / 2; d++)
-#pragma unroll
-      for (int e = 0; e < 4; e++)
-        so[(wave * kRowTile + col) * H + d * 16 + quad * 4 + e] = o[half * (DT / 2) + d][e] * mine;
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kRowTile * H / 256; c++) {
-      const int x = c * 256 + threadIdx.x;
-      acc[half][c] = so[x] + so[x + kRowTile * H] + so[x + 2 * kRowTile * H] + so[x + 3 * kRowTile * H];
-    }
+    for (int e = 0; e < E; e++) acc[e] += so[(w * kRowTile + rr) * D + d0 + e] * f;
   }
-  // rows that came out NaN, one bit each
-  __syncthreads();
-  uint32_t* s_nan = reinterpret_cast<uint32_t*>(&s_v[0][0]);
-  if (threadIdx.x == 0) *s_nan = 0;
-  if (wave == 0 && lane < kRowTile) {
-    s_m[0][lane] = m_all;
-    s_l[0][lane] = l_all;
-  }
-  __syncthreads();
+  bool nan = l_all != l_all;
 #pragma unroll
-  for (int half = 0; half < 2; half++)
-#pragma unroll
-    for (int c = 0; c < kRowTile * H / 256; c++)
-      if (acc[half][c] != acc[half][c]) atomicOr(s_nan, 1u << ((c * 256 + threadIdx.x) / H));
-  __syncthreads();
-  const uint32_t nan = *s_nan;
+  for (int e = 0; e < E; e++) nan |= acc[e] != acc[e];
+  const uint64_t bits = __ballot(nan && valid);  // a row's 16 threads are in one wave
+  const bool bad = (bits >> (lane & 48)) & 0xffff;
   float* part_o = a.work + it.index * partial_floats<D>(kRowTile);
   float* part_ml = part_o + kRowTile * D;
-#pragma unroll
-  for (int half = 0; half < 2; half++)
-#pragma unroll
-    for (int c = 0; c < kRowTile * H / 256; c++) {
-      const int x = c * 256 + threadIdx.x, rr = x / H, dim = half * H + x % H;
-      if (rr >= rows || ((nan >> rr) & 1)) continue;
-      if (it.splits > 1) {
-        part_o[rr * D + dim] = acc[half][c];
-      } else {
-        const int rt = (r0 + rr) / a.group, rh = it.hk * a.group + (r0 + rr - rt * a.group);
-        const float ll = s_l[0][rr];
-        reinterpret_cast<elem*>(a.out)[(it.q.q0 + rt) * a.out_stride[0] + rh * a.out_stride[1] + dim] =
-            (elem)(ll == 0.f ? 0.f : acc[half][c] / ll);
-      }
-    }
-  auto finish = [&](int rr, float mm, float ll) {
+  auto finish = [&](int y, float mm, float ll) {
     if (it.splits > 1) {
-      part_ml[rr * 2] = mm;
-      part_ml[rr * 2 + 1] = ll;
+      part_ml[y * 2] = mm;
+      part_ml[y * 2 + 1] = ll;
     } else if (a.lse) {
-      const int rt = (r0 + rr) / a.group, rh = it.hk * a.group + (r0 + rr - rt * a.group);
+      const int rt = (r0 + y) / a.group, rh = it.hk * a.group + (r0 + y - rt * a.group);
       a.lse[(it.q.q0 + rt) * a.q_heads + rh] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
     }
   };
-  if ((int)threadIdx.x < rows && !((nan >> threadIdx.x) & 1)) finish(threadIdx.x, s_m[0][threadIdx.x], s_l[0][threadIdx.x]);
-  if (nan) {
-    __syncthreads();  // s_nan is read; LDS is free
-    float* s_q = reinterpret_cast<float*>(s_v[wave]);
-    for (int rr = wave; rr < rows; rr += 4) {
-      if (!((nan >> rr) & 1)) continue;
+  if (valid && !bad) {
+    if (it.splits > 1) {
+#pragma unroll
+      for (int e = 0; e < E; e++) part_o[rr * D + d0 + e] = acc[e];
+    } else {
+      typedef elem ev __attribute__((ext_vector_type(E)));
+      typedef float fv __attribute__((ext_vector_type(E)));
       const int rt = (r0 + rr) / a.group, rh = it.hk * a.group + (r0 + rr - rt * a.group);
+      fv y;
+#pragma unroll
+      for (int e = 0; e < E; e++) y[e] = l_all == 0.f ? 0.f : acc[e] / l_all;
+      *reinterpret_cast<ev*>(reinterpret_cast<elem*>(a.out) + (it.q.q0 + rt) * a.out_stride[0] + rh * a.out_stride[1] + d0) =
+          __builtin_convertvector(y, ev);
+    }
+    if (d0 == 0) finish(rr, m_all, l_all);
+  }
+  // rows that came out NaN, by the wave that holds them
+  if (bits) {
+    for (int k = 0; k < 4; k++) {
+      const int y = wave * 4 + k;
+      if (!((bits >> (k * 16)) & 0xffff)) continue;
+      const int rt = (r0 + y) / a.group, rh = it.hk * a.group + (r0 + y - rt * a.group);
       float oo[D / 64], mm, ll;
-      exact_row<T, D, D>(a, it.s, it.q.q0 + rt, rh, it.q.kv - it.q.m + rt, span, i0, i1, s_q, oo, &mm, &ll);
+      exact_row<T, D, D>(a, it.s, it.q.q0 + rt, rh, it.q.kv - it.q.m + rt, span, i0, i1, s_q[wave], oo, &mm, &ll);
       for (int c = 0; c < D / 64; c++) {
         if (it.splits > 1)
-          part_o[rr * D + c * 64 + lane] = oo[c];
+          part_o[y * D + c * 64 + lane] = oo[c];
         else
           reinterpret_cast<elem*>(a.out)[(it.q.q0 + rt) * a.out_stride[0] + rh * a.out_stride[1] + c * 64 + lane] =
               (elem)(ll == 0.f ? 0.f : oo[c] / ll);
       }
-      if (lane == 0) finish(rr, mm, ll);
+      if (lane == 0) finish(y, mm, ll);
     }
   }
 }
