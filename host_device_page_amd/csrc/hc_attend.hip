@@ -1330,10 +1330,11 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
       }
       l += sum;
       __syncthreads();
-#pragma unroll
-      for (int s = 0; s < 4; s++) {
-        const v8 w0 = *reinterpret_cast<const v8*>(s_p + p_place(col, s * 2 + half));
-        const v8 w1 = *reinterpret_cast<const v8*>(s_p + p_place(32 + col, s * 2 + half));
+      // values and weights a step ahead as well (201 us for a chunk of 512 behind 3988, else 210)
+      v8 vf[2][DT], w[2][2];
+      auto fetch = [&](int s, int h) {
+        w[h][0] = *reinterpret_cast<const v8*>(s_p + p_place(col, s * 2 + half));
+        w[h][1] = *reinterpret_cast<const v8*>(s_p + p_place(32 + col, s * 2 + half));
 #pragma unroll
         for (int d = 0; d < DT; d++) {
           s16x4 v[2];
@@ -1341,10 +1342,19 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
           for (int u = 0; u < 2; u++)
             v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (lds_s16x4)(s_k + off + v_at[d & 1][u] + (d >> 1) * kLatBlock + s * 16 * 128));
-          const v8 vt = __builtin_bit_cast(v8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-          o[0][d] = T::mfma32(vt, w0, o[0][d]);
-          o[1][d] = T::mfma32(vt, w1, o[1][d]);
+          vf[h][d] = __builtin_bit_cast(v8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
         }
+      };
+      fetch(0, 0);
+#pragma unroll
+      for (int s = 0; s < 4; s++) {
+        if (s < 3) fetch(s + 1, (s + 1) & 1);
+#pragma unroll
+        for (int d = 0; d < DT; d++) {
+          o[0][d] = T::mfma32(vf[s & 1][d], w[s & 1][0], o[0][d]);
+          o[1][d] = T::mfma32(vf[s & 1][d], w[s & 1][1], o[1][d]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
       off = kLatTile - off;
       lds_arrived();

@@ -10,8 +10,8 @@
 // The data of a page is contiguous in every layer and sub-buffer (P rows, or one block), so a
 // pair is copied in pieces of 32 KiB, each one batch of eight 16-byte loads per lane before
 // its stores; memory bounds it.  Tables of a few thousand entries cost launches, not bandwidth,
-// so marks are cleared, set and scanned by three small launches and the entries rewritten by
-// the launch that copies.
+// so marks are cleared, set and scanned by one small launch (three for large tables) and the
+// entries rewritten by the launch that copies.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -278,6 +278,73 @@ __global__ __launch_bounds__(kScanThreads) void k_scan(Work w, int64_t pages, in
   for (int64_t k = threadIdx.x; k < movers; k += blockDim.x) w.mark[w.from[k]] = w.to[k];
 }
 
+// Clear, mark and scan in one workgroup, the marks a bit a page in LDS.
+constexpr int64_t kLiveEntries = 16384;
+constexpr int64_t kLivePages = 131072;
+
+__global__ __launch_bounds__(kScanThreads) void k_live(PageTable t, int32_t P, int64_t pages, Work w,
+                                                       int64_t* __restrict__ free_pages, int64_t* __restrict__ count,
+                                                       int32_t compact, int32_t* __restrict__ err) {
+  __shared__ uint32_t s_live[kLivePages / 32];
+  __shared__ int64_t s_wave[kScanThreads / 64];
+  const int words = (int)((pages + 31) / 32);
+  for (int i = threadIdx.x; i < words; i += kScanThreads) s_live[i] = 0;
+  __syncthreads();
+  const int entries = (int)(t.rows * t.width), width = (int)t.width;
+  for (int e = threadIdx.x; e < entries; e += kScanThreads) {
+    const int s = e / width, j = e - s * width;
+    bool bad;
+    const int64_t n = row_entries(t, s, P, &bad);
+    if (bad && j == 0) flag(err, kErrLengths, s);
+    if (j >= n) continue;
+    const int64_t p = t.entries[s * t.stride + j];
+    if (p >= 0 && p < pages)
+      atomicOr(&s_live[p >> 5], 1u << (p & 31));
+    else
+      flag(err, kErrIndex, e);
+  }
+  __syncthreads();
+  int64_t mine = 0, live, sum;
+  for (int i = threadIdx.x; i < words; i += kScanThreads) mine += __popc(s_live[i]);
+  block_prefix(mine, s_wave, &live);
+  if (threadIdx.x == 0) *count = compact ? live : pages - live;
+  // movers (live, at or above the live count) in the low half, holes (dead, below it) in the high half;
+  // for the free list every dead page is a hole
+  int64_t before = 0;
+  for (int i0 = 0; i0 < words; i0 += kScanThreads) {
+    const int i = i0 + threadIdx.x;
+    uint32_t on = 0, off = 0;
+    if (i < words) {
+      const int64_t left = pages - (int64_t)i * 32;
+      const uint32_t all = left >= 32 ? ~0u : (1u << left) - 1;
+      on = s_live[i];
+      off = ~on & all;
+      if (compact) {
+        const int64_t below = live - (int64_t)i * 32;  // pages of the word below the live count
+        const uint32_t low = below <= 0 ? 0 : below >= 32 ? ~0u : (1u << below) - 1;
+        on &= ~low;
+        off &= low;
+        for (int k = 0; k < 32 && k < left; k++) w.mark[i * 32 + k] = i * 32 + k;
+      }
+    }
+    const int64_t rank = before + block_prefix((int64_t)__popc(on) | (int64_t)__popc(off) << 32, s_wave, &sum);
+    before += sum;
+    int64_t m = rank & 0xffffffff, h = rank >> 32;
+    for (; off; off &= off - 1) {
+      const int p = i * 32 + __ffs(off) - 1;
+      if (compact) w.to[h++] = p;
+      else free_pages[h++] = p;
+    }
+    if (compact)
+      for (; on; on &= on - 1) w.from[m++] = i * 32 + __ffs(on) - 1;
+  }
+  if (!compact) return;
+  const int64_t movers = before & 0xffffffff;
+  __syncthreads();  // the lists are whole: as many movers as holes
+  if (threadIdx.x == 0) w.head[1] = movers;
+  for (int64_t k = threadIdx.x; k < movers; k += kScanThreads) w.mark[w.from[k]] = w.to[k];
+}
+
 __global__ __launch_bounds__(kThreads) void k_compact(Geom g, Pieces pc, PageTable t, Work w,
                                                       int64_t* out, int64_t out_stride) {
   const int64_t pages = g.S / g.P;
@@ -304,14 +371,22 @@ unsigned grid_of(int64_t items, int32_t num_cus) {
   return (unsigned)(items < 1 ? 1 : (items < cap ? items : cap));
 }
 
-hipError_t mark_pages(const Geom& g, const PageTable& t, const Work& w, int32_t* err, int32_t num_cus,
-                      hipStream_t stream) {
-  const int64_t pages = g.S / g.P;
+// The free list or the pairs, by one launch for tables that one workgroup gets through sooner than three
+// launches start.  A free list by one launch and by three, in us a call: 1024 pages and 432 entries
+// 11.4 and 16.1, 16384 entries 12.6 and 17.2, 32768 entries 21.1 and 17.4; 16384 pages and 16384 entries 15.7
+// and 37.8; 131072 pages and 16384 entries 75 and 256.
+hipError_t launch_live(const Geom& g, const PageTable& t, const Work& w, int64_t* free_pages, int64_t* count,
+                       int32_t compact, int32_t* err, int32_t num_cus, hipStream_t stream) {
+  const int64_t pages = g.S / g.P, entries = t.rows * t.width;
+  if (entries <= kLiveEntries && pages <= kLivePages) {
+    k_live<<<dim3(1), kScanThreads, 0, stream>>>(t, g.P, pages, w, free_pages, count, compact, err);
+    return hipGetLastError();
+  }
   k_clear<<<dim3((unsigned)((pages + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(w.mark, pages);
-  const int64_t entries = t.rows * t.width;
   if (entries > 0)
     k_mark<<<dim3(grid_of((entries + kThreads - 1) / kThreads, num_cus)), kThreads, 0, stream>>>(t, g.P, pages, w.mark,
                                                                                                err);
+  k_scan<<<dim3(1), kScanThreads, 0, stream>>>(w, pages, free_pages, count, compact);
   return hipGetLastError();
 }
 
@@ -342,20 +417,14 @@ hipError_t launch_free_pages(const Geom& g, const PageTable& t, int64_t* pages, 
                              int32_t* err, int32_t num_cus, hipStream_t stream) {
   const Work w = work_of(work, g.S / g.P);
   (void)hipGetLastError();
-  hipError_t e = mark_pages(g, t, w, err, num_cus, stream);
-  if (e != hipSuccess) return e;
-  k_scan<<<dim3(1), kScanThreads, 0, stream>>>(w, g.S / g.P, pages, count, 0);
-  return hipGetLastError();
+  return launch_live(g, t, w, pages, count, 0, err, num_cus, stream);
 }
 
 hipError_t launch_compact_pages(const Geom& g, const PageTable& t, int64_t* out, int64_t out_stride, int64_t* count,
                                 void* work, int32_t* err, int32_t num_cus, hipStream_t stream) {
   const Work w = work_of(work, g.S / g.P);
   (void)hipGetLastError();
-  hipError_t e = mark_pages(g, t, w, err, num_cus, stream);
-  if (e != hipSuccess) return e;
-  k_scan<<<dim3(1), kScanThreads, 0, stream>>>(w, g.S / g.P, nullptr, count, 1);
-  e = hipGetLastError();
+  hipError_t e = launch_live(g, t, w, nullptr, count, 1, err, num_cus, stream);
   if (e != hipSuccess) return e;
   if (t.rows * t.width == 0) return hipSuccess;  // nothing is named, nothing moves
   k_compact<<<dim3((unsigned)num_cus * 8), kThreads, 0, stream>>>(g, layer_pieces(g), t, w, out, out_stride);

@@ -211,6 +211,34 @@ def test_compact_and_free_list(kw, in_place):
     p.close()
 
 
+@pytest.mark.parametrize("pages,rows,width", [(140001, 3, 200), (3000, 400, 100), (131072, 2, 33), (33, 8, 5)])
+def test_compact_large_pools_and_tables(pages, rows, width):
+    """Pools and tables on both sides of what one workgroup scans, the last page named."""
+    p = Pages(page=1, pages=pages, rows=(16,), layers=1)
+    table = torch.randint(0, pages, (rows, width), generator=p.g)
+    table[0, 0] = pages - 1
+    lens = torch.randint(0, width + 1, (rows,), generator=p.g)
+    lens[0] = width
+    live = torch.zeros(pages, dtype=torch.bool)
+    live[torch.cat([table[s, :n] for s, n in enumerate(lens)])] = True
+    count = int(live.sum())
+    ids = torch.arange(pages)
+    source, target = ids[live & (ids >= count)], ids[~live & (ids < count)]
+    moved = ids.clone()
+    moved[source] = target
+    want = torch.where(torch.arange(width)[None] < lens[:, None], moved[table], table)
+    free, n = p.pool.free_pages(table.cuda(), lens.cuda())
+    assert n.item() == pages - count and torch.equal(free[:n.item()].cpu(), ids[~live])
+    out = torch.empty_like(table).cuda()
+    assert p.pool.compact_pages(table.cuda(), lens.cuda(), out).item() == count
+    p.pool.sync()
+    assert torch.equal(out.cpu(), want)
+    after = p.host[0].clone()
+    after[:, target] = p.host[0][:, source]
+    assert torch.equal(p.dev[0].cpu(), after)
+    p.close()
+
+
 def test_compact_full_empty_and_bad_tables():
     p = Pages(pages=8)
     table = torch.randperm(8, generator=p.g).view(2, 4)
