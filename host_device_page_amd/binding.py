@@ -513,6 +513,14 @@ def _on(stream, tensor, *used):
     return stream.cuda_stream
 
 
+def _new(stream, like, shape, dtype=None):
+    """A new tensor on `like`'s device, of the memory of the stream the call runs on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _torch().cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _raw_stream(tensor) -> int:
     raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's time
     if raw is not None:
@@ -653,7 +661,8 @@ class Pool:
         check(rc, "hc_layer_unpack")
 
     # The forward pass on the device side (hc.h: forward pass on the device pool).  `stream`:
-    # a torch stream, None for torch's current one.
+    # a torch stream, None for torch's current one; what a call returns newly made is that
+    # stream's.
     def store_tokens(self, layer: int, slots, k, v=None, *, q=None, q_out=None, rope: Rope | None = None,
                      positions=None, stream=None):
         """Keys k (rotated) and values v of new tokens into their slots of one layer; queries q
@@ -674,7 +683,7 @@ class Pool:
             if rows != n or q_dim != dim:
                 raise ValueError(f"q has {rows} rows of {q_dim} elements a head for {n} slots and {dim}")
             if q_out is None:
-                q_out = q.new_empty(shape)
+                q_out = _new(stream, q, shape)
             elif _heads(q_out, "q_out", k).shape != shape:
                 raise ValueError("q and q_out differ in shape")
             q_at, (q0, q1, _), o_at, (o0, o1, _) = q.data_ptr(), q.stride(), q_out.data_ptr(), q_out.stride()
@@ -715,7 +724,7 @@ class Pool:
                 raise ValueError("q_start must hold one entry more than there are sequences")
             s_at = q_start.data_ptr()
         if out is None:
-            out = q.new_empty((rows, heads, dim if value_dim is None else value_dim))
+            out = _new(stream, q, (rows, heads, dim if value_dim is None else value_dim))
             wide = out.shape[2]
         else:
             o_rows, o_heads, wide = _heads(out, "out", q).shape
@@ -726,7 +735,7 @@ class Pool:
         entry = self.page_size if entry_tokens is None else entry_tokens
         lse, l_at = None, 0
         if return_lse:
-            lse = q.new_empty((rows, heads), dtype=_torch().float32)
+            lse = _new(stream, q, (rows, heads), _torch().float32)
             l_at = lse.data_ptr()
         (q0, q1, _), (o0, o1, _) = q.stride(), out.stride()
         args = (layer, _dtype_codes[q.dtype], heads, kv_heads, dim, wide, 1 if wide != dim else 0,
@@ -740,7 +749,7 @@ class Pool:
             if rc:
                 check(rc, "hc_attend_workspace_bytes")
             if need.value:
-                workspace = q.new_empty(need.value, dtype=_torch().uint8)
+                workspace = _new(stream, q, (need.value,), _torch().uint8)
         w_at, w_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), _staging_bytes(workspace, "workspace"))
         rc = lib.hc_attend(self.handle, _ATTEND.pack(*args, w_at, w_bytes),
                            _on(stream, q, table, kv_len, q_start, out, lse, workspace))
@@ -767,16 +776,16 @@ class Pool:
         if _device_list(parents, "parents") != n or out_width != width:
             raise ValueError("out must have a row per parent and the table's width")
         n_free = _device_list(free_pages, "free_pages")
-        used = table.new_empty(1)
+        used = _new(stream, table, (1,))
         s = _on(stream, table, lens, parents, free_pages, out, used)
         check(lib.hc_fork_pages(self.handle, _V(at), rows, width, stride, _V(_ptr(lens)), _V(_ptr(parents)), n,
                                 _V(_ptr(free_pages)), n_free, _V(to), out_stride, _V(_ptr(used)), s), "hc_fork_pages")
         return used
 
-    def _pages_workspace(self, table):
+    def _pages_workspace(self, table, stream):
         need = _I64()
         check(lib.hc_pages_workspace_bytes(self.handle, ctypes.byref(need)), "hc_pages_workspace_bytes")
-        return table.new_empty(need.value, dtype=_torch().uint8)
+        return _new(stream, table, (need.value,), _torch().uint8)
 
     def free_pages(self, table, lens, stream=None):
         """(pages, count): the pages that no table row names, ascending, in the first count[0]
@@ -784,8 +793,8 @@ class Pool:
         at, rows, width, stride = _table(table, "table")
         if _device_list(lens, "lens") != rows:
             raise ValueError("lens and table differ in rows")
-        pages, count = table.new_empty(self.desc.device_slots // self.page_size), table.new_empty(1)
-        work = self._pages_workspace(table)
+        pages = _new(stream, table, (self.desc.device_slots // self.page_size,))
+        count, work = _new(stream, table, (1,)), self._pages_workspace(table, stream)
         s = _on(stream, table, lens, pages, count, work)
         check(lib.hc_free_pages(self.handle, _V(at), rows, width, stride, _V(_ptr(lens)), _V(_ptr(pages)),
                                 _V(_ptr(count)), _V(_ptr(work)), work.numel(), s), "hc_free_pages")
@@ -800,7 +809,7 @@ class Pool:
             raise ValueError("lens and table differ in rows")
         if (out_rows, out_width) != (rows, width):
             raise ValueError("out must have the table's shape")
-        count, work = table.new_empty(1), self._pages_workspace(table)
+        count, work = _new(stream, table, (1,)), self._pages_workspace(table, stream)
         s = _on(stream, table, lens, out, count, work)
         check(lib.hc_compact_pages(self.handle, _V(at), rows, width, stride, _V(_ptr(lens)), _V(to), out_stride,
                                    _V(_ptr(count)), _V(_ptr(work)), work.numel(), s), "hc_compact_pages")

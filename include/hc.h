@@ -501,7 +501,8 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* desc, void* stream);
  *   head_dim, value_dim  64/64 or 128/128, or 576/512 with value_in_key and kv_heads = 1.
  *              num_seqs, q_rows, max_q and max_kv are at most 2^30.
  *   q_heads    a multiple of kv_heads; q_heads / kv_heads <= 128.
- *   q, out     strides in elements of the row and of the head, as for hc_store_tokens.
+ *   q, out     strides in elements of the row and of the head, as for hc_store_tokens.  out,
+ *              lse and the workspace overlap nothing that the call reads.
  *   lse        fp32 [q_rows][q_heads], contiguous, or NULL.
  *   scale      finite.
  *   workspace  hc_attend_workspace_bytes of device memory, 16-byte aligned; may be NULL

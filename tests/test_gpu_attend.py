@@ -121,6 +121,33 @@ def test_windows_and_sinks(kw, d):
     check(kw, hq=4, hk=1 if d == 576 else 2, d=d, kv=(300, 40, 7, 129, 90), q=(70, 40, 1, 1, 2), page=16, entry=1)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(window=20, sinks=3)])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 1), (576, 4, 1)])
+def test_a_few_tokens_a_sequence(d, hq, hk, kw):
+    """Several new tokens in the decoding kernels' row tiles, splits among them."""
+    check(kw, hq=hq, hk=hk, d=d, kv=(300, 40, 1000, 2, 700), q=(2, 4, 3, 1, 4), page=16)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+@pytest.mark.parametrize("d,q", [(64, (1, 1)), (64, (30, 33)), (128, (40, 3)), (576, (1, 1)), (576, (40, 9))])
+def test_any_scale(d, q, scale):
+    check(dict(scale=scale), hq=4, hk=1 if d == 576 else 2, d=d, kv=(150, 70), q=q, page=16)
+
+
+@pytest.mark.parametrize("d,hq,hk", [(64, 2, 1), (576, 2, 1)])
+@pytest.mark.parametrize("seqs,q", [(4, 1), (5, 1), (256, 1), (257, 1), (700, 1), (300, 40)])
+def test_many_sequences(d, hq, hk, seqs, q):
+    """The list of work over one, several and very many sequences, empty ones among them."""
+    if q > 1 and d == 576:
+        q = 20
+    g = torch.Generator().manual_seed(seqs)
+    kv = torch.randint(0, 40, (seqs,), generator=g).tolist()
+    kv[seqs // 2] = 1500
+    qs = [1] * seqs if q == 1 else [q if i % 97 == 5 else i % 2 for i in range(seqs)]
+    qs = [min(a, max(b, 1)) for a, b in zip(qs, kv)]
+    check(hq=hq, hk=hk, d=d, kv=kv, q=qs, page=8)
+
+
 @pytest.mark.parametrize("d", [64, 128, 576])
 def test_without_causality(d):
     check(dict(causal=False), hq=4, hk=1 if d == 576 else 2, d=d, kv=(150, 20, 3), q=(20, 20, 9), page=16)
@@ -347,24 +374,29 @@ def test_same_result_every_time():
     c.close()
 
 
+@pytest.mark.parametrize("m", [5, 50])
+@pytest.mark.parametrize("hk,d", [(8, 128), (1, 576)])
 @pytest.mark.parametrize("entry", [1, 64])
-def test_rows_past_two_gigabytes(entry):
+def test_rows_past_two_gigabytes(entry, hk, d, m):
     """A pool whose rows lie past 2^32 bytes of a layer, and past 2^31 elements."""
-    hk, d, page = 8, 128, 64
+    page, hq = 64, 2 * hk
     S = (5 << 30) // (hk * d * 2) // page * page
-    dev = [torch.zeros((1, S, hk * d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    subs = 1 if d == 576 else 2
+    dev = [torch.zeros((1, S, hk * d), dtype=torch.bfloat16, device="cuda") for _ in range(subs)]
     pool = F.pool_of(dev, page)
     g = torch.Generator().manual_seed(3)
     n = 200
     slots = S - 1 - torch.arange(n) if entry == 1 else torch.arange(n) + S - 4 * page
-    rows = [normal(g, n, hk * d).to(torch.bfloat16) for _ in range(2)]
+    rows = [normal(g, n, hk * d).to(torch.bfloat16) for _ in range(subs)]
     for t, r in zip(dev, rows):
         t[0][slots.cuda()] = r.cuda()
     table = slots[None] if entry == 1 else torch.arange(4)[None] + S // page - 4
-    q = normal(g, 5, 16, d).to(torch.bfloat16)
-    out, lse = pool.attend(0, q.cuda(), table.cuda(), torch.tensor([n]).cuda(), kv_heads=hk,
-                           q_start=torch.tensor([0, 5]).cuda(), entry_tokens=entry, return_lse=True)
-    w, wl, tol, tol_l = F.attend(q, rows[0], rows[1], torch.arange(n)[None], [n], [0, 5], kv_heads=hk, entry=1)
+    q = normal(g, m, hq, d).to(torch.bfloat16)
+    dv = 512 if d == 576 else d
+    out, lse = pool.attend(0, q.cuda(), table.cuda(), torch.tensor([n]).cuda(), kv_heads=hk, value_dim=dv,
+                           q_start=torch.tensor([0, m]).cuda(), entry_tokens=entry, return_lse=True)
+    w, wl, tol, tol_l = F.attend(q, rows[0], None if subs == 1 else rows[1], torch.arange(n)[None], [n], [0, m],
+                                 kv_heads=hk, entry=1, value_dim=dv)
     F.close(out, w, tol, "out")
     F.close(lse, wl, tol_l, "lse")
     pool.sync()
