@@ -143,9 +143,10 @@ __device__ __forceinline__ uint32_t slot_of(const AttendArgs& a, int64_t s, uint
 }
 
 // 16 bytes a lane from memory into LDS, lane i to lds + 16 i (lds the same in all lanes), past the
-// registers.  Nothing waits for it but lds_arrived, of the wave that loaded.
+// registers.  Nothing waits for it but lds_arrived, of the wave that loaded.  (The compiler keeps nothing
+// in m0.)
 __device__ __forceinline__ void lds_load(const uint8_t* from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
 }
 __device__ __forceinline__ void lds_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
@@ -281,7 +282,9 @@ __device__ __forceinline__ void set_item(const AttendArgs& a, Item* it, int64_t 
 
 // Finds item blockIdx.x of the list (W waves; s_plan: 8 int64); false when the list is shorter.
 // `parts`: where the items' Parts are kept, when there is a joining launch.
-template <int W = 4>
+// FEW: calls of a few sequences have a way of their own, in the kernels of few rows (in those of many it
+// cost 3 % of a chunk of 2048, 575 us for 560, by the registers that the compiler then gave the loop).
+template <int W, bool FEW>
 __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s_plan, Part* parts, Item* it) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t want = blockIdx.x;
@@ -289,7 +292,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
   Seq q = {0, 0, 0, true};
   PlanCount c = {0, 0};
   bool found = false;
-  if (a.num_seqs <= 4) {
+  if (FEW && a.num_seqs <= 4) {
     // a few sequences: every thread goes over them by itself, without the steps of a reduction and a
     // prefix over threads (1.5 us of a single sequence's decoding)
     for (int64_t s = 0; s < a.num_seqs; s++) {
@@ -404,7 +407,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   __shared__ float s_m[4][kRowTile], s_l[4][kRowTile], s_q[4][D];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item(a, kRowTile, s_plan, parts_of<D, kRowTile>(a), &it)) return;
+  if (!find_item<4, true>(a, kRowTile, s_plan, parts_of<D, kRowTile>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const int rows_all = it.q.m * a.group;
@@ -669,7 +672,7 @@ __global__ __launch_bounds__(2 * R, 2) void k_attend_tiles(AttendArgs a) {
   __shared__ __align__(256) uint8_t s_k[2][BUF], s_v[2][BUF];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item<W>(a, R, s_plan, parts_of<D, R>(a), &it)) return;
+  if (!find_item<W, false>(a, R, s_plan, parts_of<D, R>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int64_t rows_all = (int64_t)it.q.m * a.group;
@@ -920,7 +923,7 @@ struct Latent {
 
 template <int R>
 __device__ __forceinline__ bool latent_item(const AttendArgs& a, int64_t* s_plan, Latent* t) {
-  if (!find_item(a, R, s_plan, parts_of<kLatValue, R>(a), &t->it)) return false;
+  if (!find_item<4, (R <= 32)>(a, R, s_plan, parts_of<kLatValue, R>(a), &t->it)) return false;
   const Seq& q = t->it.q;
   const int64_t rows_all = (int64_t)q.m * a.group;
   t->t0 = (int64_t)t->it.tile * R;
@@ -942,7 +945,7 @@ template <int OFFSET>
 __device__ __forceinline__ void lds_load_at(const uint8_t* from, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds), "v"(from),
                "n"(OFFSET)
-               : "memory", "m0");
+               : "memory");
 }
 template <int... B>
 __device__ __forceinline__ void latent_load_key(const uint8_t* from, uint32_t lds, std::integer_sequence<int, B...>) {
