@@ -469,14 +469,17 @@ class Rope:
 
 
 def _heads(x, what: str, like=None):
-    """A (rows, heads, dim) CUDA tensor of bf16 or fp16 with contiguous heads, `like` another's dtype."""
+    """(address, shape, strides) of a (rows, heads, dim) CUDA tensor of bf16 or fp16 with contiguous
+    heads, of `like`'s dtype."""
     if not getattr(x, "is_cuda", False) or x.dim() != 3:
         raise TypeError(f"{what} must be a CUDA tensor of (rows, heads, dim)")
-    if x.dtype not in _dtypes() or (like is not None and x.dtype != like.dtype):
-        raise TypeError(f"{what} has dtype {x.dtype}" + (f", not {like.dtype}" if like is not None else ""))
-    if x.shape[2] > 1 and x.stride(2) != 1:
+    dtype = x.dtype
+    if dtype not in (_dtype_codes or _dtypes()) or (like is not None and dtype != like.dtype):
+        raise TypeError(f"{what} has dtype {dtype}" + (f", not {like.dtype}" if like is not None else ""))
+    shape, strides = x.shape, x.stride()
+    if strides[2] != 1 and shape[2] > 1:
         raise TypeError(f"{what}: the elements of a head must be contiguous")
-    return x
+    return x.data_ptr(), shape, strides
 
 
 _dtype_codes = {}
@@ -490,18 +493,19 @@ def _dtypes() -> dict:
 
 def _device_list(x, what: str) -> int:
     """_index_list(x, what, True), quickly for what passes."""
-    if getattr(x, "is_cuda", False) and x.dtype == _torch_int64() and x.is_contiguous():
+    if getattr(x, "is_cuda", False) and x.dtype == (_torch_module or _torch()).int64 and x.is_contiguous():
         return x.numel()
     return _index_list(x, what, True)
 
 
 def _table(x, what: str):
     """(address, rows, width, row stride) of an int64 CUDA table with contiguous rows."""
-    if not getattr(x, "is_cuda", False) or x.dtype != _torch_int64() or x.dim() != 2:
+    if not getattr(x, "is_cuda", False) or x.dtype != (_torch_module or _torch()).int64 or x.dim() != 2:
         raise TypeError(f"{what} must be an int64 CUDA tensor of (rows, entries)")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    (rows, width), (stride, inner) = x.shape, x.stride()
+    if inner != 1 and width > 1:
         raise TypeError(f"{what}: the entries of a row must be contiguous")
-    return x.data_ptr(), x.shape[0], x.shape[1], max(x.stride(0), 0)
+    return x.data_ptr(), rows, width, stride
 
 
 def _on(stream, tensor, *used):
@@ -521,11 +525,17 @@ def _new(stream, like, shape, dtype=None):
         return like.new_empty(shape, dtype=dtype)
 
 
+_current_raw_stream = None  # device index -> the current stream's handle
+
+
 def _raw_stream(tensor) -> int:
-    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's time
-    if raw is not None:
-        return raw(tensor.get_device())
-    return _torch().cuda.current_stream(tensor.device).cuda_stream
+    global _current_raw_stream
+    if _current_raw_stream is None:
+        cuda = _torch().cuda
+        # torch's own short way takes a tenth of the public call's 2 us
+        _current_raw_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream",
+                                      lambda index: cuda.current_stream(index).cuda_stream)
+    return _current_raw_stream(tensor.get_device())
 
 
 class Pool:
@@ -669,24 +679,24 @@ class Pool:
         rotated into q_out (q itself: in place; None: a new tensor).  k, v, q: (tokens, heads,
         dim); v None for a latent cache.  Returns q_out."""
         n = _device_list(slots, "slots")
-        rows, kv_heads, dim = _heads(k, "k").shape
+        k_at, (rows, kv_heads, dim), (k0, k1, _) = _heads(k, "k")
         if rows != n:
             raise ValueError(f"k has {rows} rows for {n} slots")
         value_dim = v_at = v0 = v1 = q_heads = q_at = q0 = q1 = o_at = o0 = o1 = 0
         if v is not None:
-            rows, heads, value_dim = _heads(v, "v", k).shape
+            v_at, (rows, heads, value_dim), (v0, v1, _) = _heads(v, "v", k)
             if rows != n or heads != kv_heads:
                 raise ValueError(f"v has {rows} rows of {heads} heads for {n} slots and {kv_heads} heads")
-            v_at, (v0, v1, _) = v.data_ptr(), v.stride()
         if q is not None:
-            rows, q_heads, q_dim = shape = _heads(q, "q", k).shape
+            q_at, shape, (q0, q1, _) = _heads(q, "q", k)
+            rows, q_heads, q_dim = shape
             if rows != n or q_dim != dim:
                 raise ValueError(f"q has {rows} rows of {q_dim} elements a head for {n} slots and {dim}")
             if q_out is None:
                 q_out = _new(stream, q, shape)
-            elif _heads(q_out, "q_out", k).shape != shape:
+            o_at, o_shape, (o0, o1, _) = _heads(q_out, "q_out", k)
+            if o_shape != shape:
                 raise ValueError("q and q_out differ in shape")
-            q_at, (q0, q1, _), o_at, (o0, o1, _) = q.data_ptr(), q.stride(), q_out.data_ptr(), q_out.stride()
         elif q_out is not None:
             raise ValueError("q_out without q")
         p_at = 0
@@ -694,9 +704,8 @@ class Pool:
             if _device_list(positions, "positions") != n:
                 raise ValueError("positions and slots differ in length")
             p_at = positions.data_ptr()
-        k0, k1, _ = k.stride()
         d = _STORE.pack(layer, _dtype_codes[k.dtype], q_heads, kv_heads, dim, value_dim, n, slots.data_ptr(), p_at, q_at,
-                        o_at, k.data_ptr(), v_at, q0, q1, o0, o1, k0, k1, v0, v1,
+                        o_at, k_at, v_at, q0, q1, o0, o1, k0, k1, v0, v1,
                         0 if rope is None else rope.handle.value)
         rc = lib.hc_store_tokens(self.handle, d, _on(stream, k, slots, positions, q, q_out, v))
         if rc:
@@ -714,7 +723,7 @@ class Pool:
         no sequence has more rows, or tokens (None: what q and the table hold).  value_dim
         below head_dim: a latent cache, whose key rows hold the values.  scale None:
         head_dim ** -0.5.  Returns (out, lse), lse None unless asked for."""
-        rows, heads, dim = _heads(q, "q").shape
+        q_at, (rows, heads, dim), (q0, q1, _) = _heads(q, "q")
         at, seqs, width, stride = _table(table, "table")
         if _device_list(kv_len, "kv_len") != seqs:
             raise ValueError("kv_len and table differ in sequences")
@@ -725,23 +734,20 @@ class Pool:
             s_at = q_start.data_ptr()
         if out is None:
             out = _new(stream, q, (rows, heads, dim if value_dim is None else value_dim))
-            wide = out.shape[2]
-        else:
-            o_rows, o_heads, wide = _heads(out, "out", q).shape
-            if o_rows != rows or o_heads != heads:
-                raise ValueError("q and out differ in rows or heads")
-            if value_dim is not None and wide != value_dim:
-                raise ValueError("out is not value_dim wide")
+        o_at, (o_rows, o_heads, wide), (o0, o1, _) = _heads(out, "out", q)
+        if o_rows != rows or o_heads != heads:
+            raise ValueError("q and out differ in rows or heads")
+        if value_dim is not None and wide != value_dim:
+            raise ValueError("out is not value_dim wide")
         entry = self.page_size if entry_tokens is None else entry_tokens
         lse, l_at = None, 0
         if return_lse:
             lse = _new(stream, q, (rows, heads), _torch().float32)
             l_at = lse.data_ptr()
-        (q0, q1, _), (o0, o1, _) = q.stride(), out.stride()
         args = (layer, _dtype_codes[q.dtype], heads, kv_heads, dim, wide, 1 if wide != dim else 0,
                 1 if causal else 0, entry, dim ** -0.5 if scale is None else scale, window, sinks, seqs, rows,
                 (1 if q_start is None else rows) if max_q is None else max_q,
-                width * entry if max_kv is None else max_kv, width, stride, q.data_ptr(), out.data_ptr(), l_at, s_at,
+                width * entry if max_kv is None else max_kv, width, stride, q_at, o_at, l_at, s_at,
                 kv_len.data_ptr(), at, q0, q1, o0, o1)
         if workspace is None:
             need = _I64()

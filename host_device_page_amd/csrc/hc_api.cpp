@@ -1274,25 +1274,44 @@ int pool_forward(hc_pool* p, void* stream, PoolView* out) {
   return HC_OK;
 }
 
-int check_buffer(const void* q, int64_t bytes, int32_t device, int32_t align, bool host_ok, const char* what) {
+int BufferCheck::buffer(const void* q, int64_t bytes, int32_t align, bool host_ok, const char* what) {
   if (bytes == 0) return HC_OK;
   if (!q) return set_error(HC_ERR_INVALID, "%s is null", what);
-  if ((uintptr_t)q % (uintptr_t)align != 0)
-    return set_error(HC_ERR_UNSUPPORTED, "%s must be %d-byte aligned", what, align);
-  hipPointerAttribute_t attr;
-  if (hipPointerGetAttributes(&attr, q) != hipSuccess) {
-    (void)hipGetLastError();
-    return set_error(HC_ERR_INVALID, "%s is not memory known to HIP", what);
+  const uintptr_t at = (uintptr_t)q;
+  if (at % (uintptr_t)align != 0) return set_error(HC_ERR_UNSUPPORTED, "%s must be %d-byte aligned", what, align);
+  const Known* in = nullptr;
+  for (int32_t i = 0; i < count_ && !in; i++)
+    if (at >= known_[i].base && at < known_[i].end) in = &known_[i];
+  Known found;
+  if (!in) {
+    hipPointerAttribute_t attr;
+    if (hipPointerGetAttributes(&attr, q) != hipSuccess) {
+      (void)hipGetLastError();
+      return set_error(HC_ERR_INVALID, "%s is not memory known to HIP", what);
+    }
+    if (attr.type == hipMemoryTypeDevice) {
+      if (attr.device != device_)
+        return set_error(HC_ERR_INVALID, "%s is on device %d, the pool's device is %d", what, attr.device, device_);
+    } else if (attr.type != hipMemoryTypeHost) {
+      return set_error(HC_ERR_INVALID, "%s must be device memory%s", what, host_ok ? " (or pinned host memory)" : "");
+    } else if (attr.devicePointer != q) {
+      return set_error(HC_ERR_INVALID, "%s: pinned host memory not mapped at its host address", what);
+    }
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    if (hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)q) != hipSuccess || !base) {
+      (void)hipGetLastError();
+      return set_error(HC_ERR_INVALID, "%s: its allocation could not be found", what);
+    }
+    found = {(uintptr_t)base, (uintptr_t)base + size, attr.type == hipMemoryTypeHost};
+    if (count_ < (int32_t)(sizeof(known_) / sizeof(known_[0]))) known_[count_++] = found;
+    in = &found;
   }
-  if (attr.type == hipMemoryTypeDevice) {
-    if (attr.device != device)
-      return set_error(HC_ERR_INVALID, "%s is on device %d, the pool's device is %d", what, attr.device, device);
-  } else if (!host_ok || attr.type != hipMemoryTypeHost) {
-    return set_error(HC_ERR_INVALID, "%s must be device memory%s", what, host_ok ? " (or pinned host memory)" : "");
-  } else if (attr.devicePointer != q) {
-    return set_error(HC_ERR_INVALID, "%s: pinned host memory not mapped at its host address", what);
-  }
-  return check_extent(q, bytes, true, what);
+  if (in->host && !host_ok) return set_error(HC_ERR_INVALID, "%s must be device memory", what);
+  if ((uint64_t)bytes > (uint64_t)(in->end - at))
+    return set_error(HC_ERR_INVALID, "%s: %lld bytes are needed, its allocation ends %llu bytes after it", what,
+                     (long long)bytes, (unsigned long long)(in->end - at));
+  return HC_OK;
 }
 
 void pool_hold(hc_pool* pool) { pool->users.fetch_add(1); }

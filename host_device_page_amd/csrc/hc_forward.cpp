@@ -53,7 +53,7 @@ int64_t tensor_bytes(const int64_t* stride, int64_t n, int64_t heads, int64_t di
 }
 
 int check_tensor(const void* q, const int64_t* stride, int64_t n, int64_t heads, int64_t dim, bool writes,
-                 int32_t device, const char* what) {
+                 hc::BufferCheck& check, const char* what) {
   for (int k = 0; k < 2; k++) {
     if (stride[k] < 0 || stride[k] > kMaxStride)
       return set_error(HC_ERR_INVALID, "%s: stride %lld out of range", what, (long long)stride[k]);
@@ -71,16 +71,16 @@ int check_tensor(const void* q, const int64_t* stride, int64_t n, int64_t heads,
       need = stride[k] * (count[k] - 1) + need;
     }
   }
-  return hc::check_buffer(q, tensor_bytes(stride, n, heads, dim), device, 16, false, what);
+  return check.buffer(q, tensor_bytes(stride, n, heads, dim), 16, false, what);
 }
 
-int check_list(const int64_t* q, int64_t n, int32_t device, const char* what) {
-  return hc::check_buffer(q, n * (int64_t)sizeof(int64_t), device, 8, true, what);
+int check_list(const int64_t* q, int64_t n, hc::BufferCheck& check, const char* what) {
+  return check.buffer(q, n * (int64_t)sizeof(int64_t), 8, true, what);
 }
 
 // Written lists and counters stay in device memory.
-int check_out_list(const int64_t* q, int64_t n, int32_t device, const char* what) {
-  return hc::check_buffer(q, n * (int64_t)sizeof(int64_t), device, 8, false, what);
+int check_out_list(const int64_t* q, int64_t n, hc::BufferCheck& check, const char* what) {
+  return check.buffer(q, n * (int64_t)sizeof(int64_t), 8, false, what);
 }
 
 // [a, a + an) and [b, b + bn) share a byte.
@@ -211,15 +211,16 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
     return set_error(HC_ERR_INVALID, "the rotated elements [%d, %d) are not inside a head of %d",
                      d->rope->table.rot_offset, d->rope->table.rot_offset + d->rope->table.rot_dim, d->head_dim);
   HC_TRY(hc::pool_forward(pool, stream, &v));
+  hc::BufferCheck check(v.device);
   if (d->n == 0) return HC_OK;
-  HC_TRY(check_list(d->slots, d->n, v.device, "slots"));
-  if (d->rope) HC_TRY(check_list(d->positions, d->n, v.device, "positions"));
-  HC_TRY(check_tensor(d->k, d->k_stride, d->n, d->kv_heads, d->head_dim, false, v.device, "k"));
+  HC_TRY(check_list(d->slots, d->n, check, "slots"));
+  if (d->rope) HC_TRY(check_list(d->positions, d->n, check, "positions"));
+  HC_TRY(check_tensor(d->k, d->k_stride, d->n, d->kv_heads, d->head_dim, false, check, "k"));
   if (d->value_dim > 0)
-    HC_TRY(check_tensor(d->v, d->v_stride, d->n, d->kv_heads, d->value_dim, false, v.device, "v"));
+    HC_TRY(check_tensor(d->v, d->v_stride, d->n, d->kv_heads, d->value_dim, false, check, "v"));
   if (d->q_heads > 0) {
-    HC_TRY(check_tensor(d->q, d->q_stride, d->n, d->q_heads, d->head_dim, false, v.device, "q"));
-    HC_TRY(check_tensor(d->q_out, d->q_out_stride, d->n, d->q_heads, d->head_dim, true, v.device, "q_out"));
+    HC_TRY(check_tensor(d->q, d->q_stride, d->n, d->q_heads, d->head_dim, false, check, "q"));
+    HC_TRY(check_tensor(d->q_out, d->q_out_stride, d->n, d->q_heads, d->head_dim, true, check, "q_out"));
     if (d->q_out == d->q && (d->q_out_stride[0] != d->q_stride[0] || d->q_out_stride[1] != d->q_stride[1]) &&
         d->n * d->q_heads > 1)
       return set_error(HC_ERR_INVALID, "q_out in place of q needs q's strides");
@@ -337,22 +338,23 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
   hc::AttendArgs a;
   HC_TRY(attend_sizes(v, d, &a));
   HC_TRY(hc::pool_forward(pool, stream, &v));
+  hc::BufferCheck check(v.device);
   if (d->q_rows == 0 || d->num_seqs == 0) return HC_OK;
   if (!d->q_start && d->q_rows < d->num_seqs)
     return set_error(HC_ERR_INVALID, "without q_start every sequence has a row: q_rows is below num_seqs");
-  HC_TRY(check_tensor(d->q, d->q_stride, d->q_rows, d->q_heads, d->head_dim, false, v.device, "q"));
-  HC_TRY(check_tensor(d->out, d->out_stride, d->q_rows, d->q_heads, d->value_dim, true, v.device, "out"));
-  HC_TRY(hc::check_buffer(d->lse, d->lse ? 4 * d->q_rows * d->q_heads : 0, v.device, 4, false, "lse"));
-  if (d->q_start) HC_TRY(check_list(d->q_start, d->num_seqs + 1, v.device, "q_start"));
-  HC_TRY(check_list(d->kv_len, d->num_seqs, v.device, "kv_len"));
+  HC_TRY(check_tensor(d->q, d->q_stride, d->q_rows, d->q_heads, d->head_dim, false, check, "q"));
+  HC_TRY(check_tensor(d->out, d->out_stride, d->q_rows, d->q_heads, d->value_dim, true, check, "out"));
+  HC_TRY(check.buffer(d->lse, d->lse ? 4 * d->q_rows * d->q_heads : 0, 4, false, "lse"));
+  if (d->q_start) HC_TRY(check_list(d->q_start, d->num_seqs + 1, check, "q_start"));
+  HC_TRY(check_list(d->kv_len, d->num_seqs, check, "kv_len"));
   if (d->table_width > 0)
-    HC_TRY(check_list(d->table, (d->num_seqs - 1) * d->table_stride + d->table_width, v.device, "table"));
+    HC_TRY(check_list(d->table, (d->num_seqs - 1) * d->table_stride + d->table_width, check, "table"));
   const int64_t work = hc::attend_workspace(a, d->head_dim, v.num_cus);
   if (work > 0) {
     if (d->workspace_bytes < work)
       return set_error(HC_ERR_INVALID, "workspace_bytes %lld below the %lld that are needed",
                        (long long)d->workspace_bytes, (long long)work);
-    HC_TRY(hc::check_buffer(d->workspace, work, v.device, 16, false, "workspace"));
+    HC_TRY(check.buffer(d->workspace, work, 16, false, "workspace"));
   }
   if (overlap(d->q, tensor_bytes(d->q_stride, d->q_rows, d->q_heads, d->head_dim), d->out,
               tensor_bytes(d->out_stride, d->q_rows, d->q_heads, d->value_dim)) &&
@@ -394,17 +396,17 @@ int64_t table_entries(int64_t rows, int64_t width, int64_t stride) {
 }
 
 int check_table(const int64_t* table, const int64_t* lens, int64_t rows, int64_t width, int64_t stride,
-                int32_t device) {
-  HC_TRY(check_list(table, table_entries(rows, width, stride), device, "table"));
-  return check_list(lens, rows, device, "lens");
+                hc::BufferCheck& check) {
+  HC_TRY(check_list(table, table_entries(rows, width, stride), check, "table"));
+  return check_list(lens, rows, check, "lens");
 }
 
-int check_work(const PoolView& v, const void* work, int64_t bytes) {
+int check_work(const PoolView& v, const void* work, int64_t bytes, hc::BufferCheck& check) {
   const int64_t need = hc::pages_workspace(*v.geom);
   if (bytes < need)
     return set_error(HC_ERR_INVALID, "workspace_bytes %lld below the %lld that are needed", (long long)bytes,
                      (long long)need);
-  return hc::check_buffer(work, need, v.device, 16, false, "workspace");
+  return check.buffer(work, need, 16, false, "workspace");
 }
 
 }  // namespace
@@ -419,8 +421,9 @@ int hc_copy_pages(hc_pool* pool, const int64_t* src, const int64_t* dst, int64_t
   HC_TRY(page_pool(v));
   if (n < 0 || n >= kMaxRows) return set_error(HC_ERR_INVALID, "n must be in [0, 2^31)");
   HC_TRY(hc::pool_forward(pool, stream, &v));
-  HC_TRY(check_list(src, n, v.device, "src"));
-  HC_TRY(check_list(dst, n, v.device, "dst"));
+  hc::BufferCheck check(v.device);
+  HC_TRY(check_list(src, n, check, "src"));
+  HC_TRY(check_list(dst, n, check, "dst"));
   return launched(hc::launch_copy_pages(*v.geom, src, dst, n, v.err, v.num_cus, (hipStream_t)stream), "page copy");
 }
 
@@ -436,12 +439,13 @@ int hc_fork_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
   HC_TRY(table_sizes(n, table_width, out_stride));
   if (n_free < 0 || n_free >= kMaxRows) return set_error(HC_ERR_INVALID, "n_free must be in [0, 2^31)");
   HC_TRY(hc::pool_forward(pool, stream, &v));
-  HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, v.device));
-  HC_TRY(check_list(parents, n, v.device, "parents"));
-  HC_TRY(check_list(free_pages, n_free, v.device, "free_pages"));
+  hc::BufferCheck check(v.device);
+  HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
+  HC_TRY(check_list(parents, n, check, "parents"));
+  HC_TRY(check_list(free_pages, n_free, check, "free_pages"));
   const int64_t in = table_entries(table_rows, table_width, table_stride), out = table_entries(n, table_width, out_stride);
-  HC_TRY(check_out_list(out_table, out, v.device, "out_table"));
-  HC_TRY(check_out_list(used, 1, v.device, "used"));
+  HC_TRY(check_out_list(out_table, out, check, "out_table"));
+  HC_TRY(check_out_list(used, 1, check, "used"));
   if (overlap(table, 8 * in, out_table, 8 * out) || overlap(used, 8, out_table, 8 * out) || overlap(used, 8, table, 8 * in))
     return set_error(HC_ERR_INVALID, "out_table and used must not overlap the table");
   hc::ForkArgs a = {{table, lens, table_rows, table_width, table_stride}, parents, free_pages, n, n_free, out_table,
@@ -468,10 +472,11 @@ int hc_free_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
   HC_TRY(page_pool(v));
   HC_TRY(table_sizes(table_rows, table_width, table_stride));
   HC_TRY(hc::pool_forward(pool, stream, &v));
-  HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, v.device));
-  HC_TRY(check_out_list(free_pages, v.geom->S / v.geom->P, v.device, "free_pages"));
-  HC_TRY(check_out_list(count, 1, v.device, "count"));
-  HC_TRY(check_work(v, workspace, workspace_bytes));
+  hc::BufferCheck check(v.device);
+  HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
+  HC_TRY(check_out_list(free_pages, v.geom->S / v.geom->P, check, "free_pages"));
+  HC_TRY(check_out_list(count, 1, check, "count"));
+  HC_TRY(check_work(v, workspace, workspace_bytes, check));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};
   return launched(hc::launch_free_pages(*v.geom, t, free_pages, count, workspace, v.err, v.num_cus,
                                         (hipStream_t)stream),
@@ -489,14 +494,15 @@ int hc_compact_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, in
   HC_TRY(table_sizes(table_rows, table_width, table_stride));
   HC_TRY(table_sizes(table_rows, table_width, out_stride));
   HC_TRY(hc::pool_forward(pool, stream, &v));
-  HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, v.device));
+  hc::BufferCheck check(v.device);
+  HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
   const int64_t in = table_entries(table_rows, table_width, table_stride);
   const int64_t out = table_entries(table_rows, table_width, out_stride);
-  HC_TRY(check_out_list(out_table, out, v.device, "out_table"));
-  HC_TRY(check_out_list(count, 1, v.device, "count"));
+  HC_TRY(check_out_list(out_table, out, check, "out_table"));
+  HC_TRY(check_out_list(count, 1, check, "count"));
   if (overlap(table, 8 * in, out_table, 8 * out) && !(table == out_table && table_stride == out_stride))
     return set_error(HC_ERR_INVALID, "out_table overlaps the table without being it");
-  HC_TRY(check_work(v, workspace, workspace_bytes));
+  HC_TRY(check_work(v, workspace, workspace_bytes, check));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};
   return launched(hc::launch_compact_pages(*v.geom, t, out_table, out_stride, count, workspace, v.err, v.num_cus,
                                            (hipStream_t)stream),

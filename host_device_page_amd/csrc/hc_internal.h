@@ -99,9 +99,24 @@ struct PoolView {
 int pool_forward(hc_pool* pool, void* stream, PoolView* out);
 // The same view without touching a device (size queries).
 void pool_view(const hc_pool* pool, PoolView* out);
-// `bytes` of device memory of `device` at q, `align`-byte aligned (HC_ERR_UNSUPPORTED
-// otherwise), inside one allocation; a list may be pinned host memory too.
-int check_buffer(const void* q, int64_t bytes, int32_t device, int32_t align, bool host_ok, const char* what);
+// Checks the buffers of one call.  A buffer inside an allocation that the call's earlier buffers
+// lie in too needs no questions to the runtime, which take half a microsecond each.
+class BufferCheck {
+ public:
+  explicit BufferCheck(int32_t device) : device_(device) {}
+  // `bytes` of device memory of the device at q, `align`-byte aligned (HC_ERR_UNSUPPORTED otherwise),
+  // inside one allocation; host_ok: pinned host memory will do too.
+  int buffer(const void* q, int64_t bytes, int32_t align, bool host_ok, const char* what);
+
+ private:
+  struct Known {
+    uintptr_t base, end;
+    bool host;
+  };
+  int32_t device_;
+  int32_t count_ = 0;
+  Known known_[8];
+};
 
 // Optional timing of one kernel launch: two timing events that the launch itself
 // stamps with the kernel's start and end (hipExtLaunchKernel), so timing adds no
