@@ -387,6 +387,11 @@ __device__ __forceinline__ Part* parts_of(const AttendArgs& a) {
 //   O^T += V^T P^T (B: the same lane's 8 weights as they stand): the order of the keys inside the
 //                 product is free, so V^T is read in that order: V goes through LDS and comes
 //                 back transposed, four keys of a dim a lane
+//
+// Measured: 64 sequences up to 8192 tokens, 8 KV heads of 128, 208 us = 5.3 TB/s; 32 sequences in a window
+// of 4096 with 4 sinks, scattered slots, heads of 64, 62 us = 4.2 TB/s; one sequence of 1500 8 us and 4 us to
+// join. Eight workgroups a compute unit in the list of items: 4 213 us, 16 217 us, 32 254 us on the
+// first; three waves a SIMD instead of two (which spills) 232 us.
 constexpr int kRowTile = 16;
 constexpr int kKeys = 32;
 
@@ -629,6 +634,10 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
 // row's scores of 32 of the 64 keys, 8 q + 4 (lane / 32) + r of each 32, which are the operand of
 // O^T += V^T P^T as they stand; V comes from LDS transposed, in that order of the keys.  The next tile
 // is loaded into the other half of LDS while one is computed: one barrier a tile.
+//
+// Measured: a chunk of 2048 behind 14336 cached, 32/8 heads of 128, 545 us = 946 TFLOP/s; four prompts up to 4096
+// of fp16 heads of 64, 109 us = 589 TFLOP/s. Waves in a product go before others (s_setprio): two waves of a
+// SIMD that multiply at the same time would also compute weights at the same time, 574 us for 557.
 //
 // The maximum that a row's weights are relative to is replaced only when it grows by more than
 // 2^8: until then weights of up to 2^8 are summed, which loses nothing in fp32 or as operands, and the
@@ -880,7 +889,8 @@ __global__ __launch_bounds__(2 * R, 2) void k_attend_tiles(AttendArgs a) {
 // 576 dims of a key against every head of a token, 512 of them its value, so a tile of 64 keys (72 KiB,
 // two of them in LDS) is read into LDS once for both products, and its four waves cut the work
 // without doing any twice: scores by keys, values by dims, 128 a wave.  The maxima of the waves' keys
-// and then the weights go through LDS: three barriers a tile.
+// and then the weights go through LDS: three barriers a tile.  Measured: 32 sequences up to 6000 tokens and 16 heads
+// 33 us and 5 us to join; a chunk of 512 behind 3988 with 32 heads 190 us = 796 TFLOP/s.
 constexpr int kLatKeys = 64;
 constexpr int kLatDim = 576;
 constexpr int kLatValue = 512;
