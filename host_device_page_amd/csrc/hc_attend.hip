@@ -1473,8 +1473,10 @@ int tile_rows(const AttendArgs& a, int32_t head_dim) {
 
 // How the list of items is made for a call of tiles of R rows, and the number of items at most: a split of
 // C keys has at least `min_split` of them, and the whole call's keys over C is at most `target`.
-// Calls of many rows are split only when their row tiles, which the host knows, do not fill the GPU:
-// else one launch does all.
+// Calls of many rows are split when their row tiles, which the host knows, do not fill the GPU, or when some of
+// several sequences may be so long that their one tile each (a decoding row beside a chunk) would
+// run on alone; else one launch does all.
+constexpr int64_t kLongKeys = 16384;
 struct Plan {
   int64_t items, joins;  // joins: workgroups of the second launch, 0: no split can be
 };
@@ -1488,7 +1490,8 @@ Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus) {
   if (latent) a->target = num_cus - p.items > num_cus / 2 ? num_cus - p.items : num_cus / 2;
   a->join_parts = 0;
   const int64_t most_splits = (a->max_kv + a->min_split - 1) / a->min_split;
-  if (most_splits > 1 && (few || a->q_rows * a->group / R * a->kv_heads < a->target)) {
+  const bool fills = a->q_rows * a->group / R * a->kv_heads >= a->target;
+  if (most_splits > 1 && (few || !fills || (a->num_seqs > 1 && a->max_kv > kLongKeys))) {
     const int64_t rows = a->max_q * a->group < R ? a->max_q * a->group : R;  // of a tile at most
     a->join_parts = (int32_t)((rows + 3) / 4);
     p.items = p.items * most_splits < p.items + a->target ? p.items * most_splits : p.items + a->target;

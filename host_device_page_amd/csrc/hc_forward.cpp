@@ -446,8 +446,13 @@ int hc_fork_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
   const int64_t in = table_entries(table_rows, table_width, table_stride), out = table_entries(n, table_width, out_stride);
   HC_TRY(check_out_list(out_table, out, check, "out_table"));
   HC_TRY(check_out_list(used, 1, check, "used"));
-  if (overlap(table, 8 * in, out_table, 8 * out) || overlap(used, 8, out_table, 8 * out) || overlap(used, 8, table, 8 * in))
-    return set_error(HC_ERR_INVALID, "out_table and used must not overlap the table");
+  const struct {
+    const int64_t* list;
+    int64_t n;
+  } read[] = {{table, in}, {lens, table_rows}, {parents, n}, {free_pages, n_free}, {used, 1}};
+  for (const auto& r : read)
+    if (overlap(r.list, 8 * r.n, out_table, 8 * out) || (r.list != used && overlap(r.list, 8 * r.n, used, 8)))
+      return set_error(HC_ERR_INVALID, "out_table and used must not overlap each other or what is read");
   hc::ForkArgs a = {{table, lens, table_rows, table_width, table_stride}, parents, free_pages, n, n_free, out_table,
                     out_stride, used};
   return launched(hc::launch_fork_pages(*v.geom, a, v.err, v.num_cus, (hipStream_t)stream), "fork");
@@ -474,8 +479,13 @@ int hc_free_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
   HC_TRY(hc::pool_forward(pool, stream, &v));
   hc::BufferCheck check(v.device);
   HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
-  HC_TRY(check_out_list(free_pages, v.geom->S / v.geom->P, check, "free_pages"));
+  const int64_t in = table_entries(table_rows, table_width, table_stride), pages = v.geom->S / v.geom->P;
+  HC_TRY(check_out_list(free_pages, pages, check, "free_pages"));
   HC_TRY(check_out_list(count, 1, check, "count"));
+  if (overlap(table, 8 * in, free_pages, 8 * pages) || overlap(lens, 8 * table_rows, free_pages, 8 * pages) ||
+      overlap(count, 8, table, 8 * in) || overlap(count, 8, lens, 8 * table_rows) ||
+      overlap(count, 8, free_pages, 8 * pages))
+    return set_error(HC_ERR_INVALID, "free_pages and count must not overlap each other or what is read");
   HC_TRY(check_work(v, workspace, workspace_bytes, check));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};
   return launched(hc::launch_free_pages(*v.geom, t, free_pages, count, workspace, v.err, v.num_cus,
@@ -502,6 +512,9 @@ int hc_compact_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, in
   HC_TRY(check_out_list(count, 1, check, "count"));
   if (overlap(table, 8 * in, out_table, 8 * out) && !(table == out_table && table_stride == out_stride))
     return set_error(HC_ERR_INVALID, "out_table overlaps the table without being it");
+  if (overlap(lens, 8 * table_rows, out_table, 8 * out) || overlap(count, 8, out_table, 8 * out) ||
+      overlap(count, 8, table, 8 * in) || overlap(count, 8, lens, 8 * table_rows))
+    return set_error(HC_ERR_INVALID, "out_table and count must not overlap each other or what is read");
   HC_TRY(check_work(v, workspace, workspace_bytes, check));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};
   return launched(hc::launch_compact_pages(*v.geom, t, out_table, out_stride, count, workspace, v.err, v.num_cus,

@@ -562,7 +562,7 @@ int hc_pages_workspace_bytes(const hc_pool* pool, int64_t* out_bytes);
 
 /* Lists the pages that no table row names, ascending, in free_pages (room for
  * device_slots / P entries; those behind the list stay as they were) and their number in
- * *count. */
+ * *count.  free_pages and count overlap nothing else. */
 int hc_free_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64_t table_width, int64_t table_stride,
                   const int64_t* lens, int64_t* free_pages, int64_t* count, void* workspace, int64_t workspace_bytes,
                   void* stream);
@@ -571,7 +571,7 @@ int hc_free_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
  * where they are, and the k-th named page from *count on moves into the k-th unnamed page
  * below it.  out_table (which may be table itself) is the table with the moved pages' new
  * numbers; entries behind a row's length are copied as they are.  A page that has moved
- * keeps its old bytes. */
+ * keeps its old bytes.  out_table and count overlap nothing else. */
 int hc_compact_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64_t table_width,
                      int64_t table_stride, const int64_t* lens, int64_t* out_table, int64_t out_stride,
                      int64_t* count, void* workspace, int64_t workspace_bytes, void* stream);

@@ -148,6 +148,21 @@ def test_many_sequences(d, hq, hk, seqs, q):
     check(hq=hq, hk=hk, d=d, kv=kv, q=qs, page=8)
 
 
+def test_a_chunk_beside_long_decoding_sequences():
+    """One call of a chunk that fills the GPU and decoding rows of long sequences, which are split:
+    every decoding row and some of the chunk's against 64 bits, the lengths shorter than their bound."""
+    c = Case(hq=32, hk=8, d=64, kv=(17000, 2100, 20000, 3), q=(1, 2050, 1, 1), page=64).upload()
+    out, lse = c.run(max_q=2050, max_kv=20032)
+    torch.cuda.synchronize()
+    c.pool.sync()
+    for row, s, p in [(0, 0, 16999), (1, 1, 50), (7, 1, 56), (130, 1, 179), (2050, 1, 2099), (2051, 2, 19999), (2052, 3, 2)]:
+        w, wl, tol, tol_l = F.attend(c.q[row:row + 1], c.host[0][1], c.host[1][1], c.table[s:s + 1], [p + 1], [0, 1],
+                                     kv_heads=8, entry=64)
+        F.close(out[row:row + 1], w, tol, f"row {row}")
+        F.close(lse[row:row + 1], wl, tol_l, f"lse {row}")
+    c.close()
+
+
 @pytest.mark.parametrize("d", [64, 128, 576])
 def test_without_causality(d):
     check(dict(causal=False), hq=4, hk=1 if d == 576 else 2, d=d, kv=(150, 20, 3), q=(20, 20, 9), page=16)

@@ -276,6 +276,9 @@ def test_refusals():
 
     refuse(lambda: p.pool.fork_pages(table, lens, ints([0, 1]), ints([5]), table))              # in place
     refuse(lambda: p.pool.compact_pages(table[:, :2], lens, table[:, 1:]))                      # overlaps
+    lists = torch.zeros(64, dtype=torch.int64, device="cuda")
+    refuse(lambda: p.pool.compact_pages(table, lists[:2], lists[:6].view(2, 3)))                # the lengths
+    refuse(lambda: p.pool.fork_pages(table, lens, lists[:1], ints([5]), lists[:3].view(1, 3)))  # the parents
     with pytest.raises(ValueError):
         p.pool.fork_pages(table, lens, ints([0]), ints([5]), torch.zeros((1, 2), dtype=torch.int64, device="cuda"))
     with pytest.raises(ValueError):
