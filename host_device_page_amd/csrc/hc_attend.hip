@@ -280,11 +280,11 @@ __device__ __forceinline__ void set_item(const AttendArgs& a, Item* it, int64_t 
   it->index = blockIdx.x;
 }
 
-// Finds item blockIdx.x of the list (W waves; s_plan: 8 int64); false when the list is shorter.
+// Finds item blockIdx.x of the list (256 threads; s_plan: 8 int64); false when the list is shorter.
 // `parts`: where the items' Parts are kept, when there is a joining launch.
 // FEW: calls of a few sequences have a way of their own, in the kernels of few rows (in those of many it
 // cost 3 % of a chunk of 2048, 575 us for 560, by the registers that the compiler then gave the loop).
-template <int W, bool FEW>
+template <bool FEW>
 __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s_plan, Part* parts, Item* it) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t want = blockIdx.x;
@@ -310,7 +310,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
       at += mine;
     }
   } else {
-    for (int64_t s = threadIdx.x; s < a.num_seqs; s += 64 * W) {
+    for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
       c = plan_count(a, s, R, &q);
       if (blockIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
       work += c.tiles * c.n;
@@ -319,12 +319,12 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
     if (lane == 0) s_plan[wave] = work;
     __syncthreads();
     work = 0;
-    for (int w = 0; w < W; w++) work += s_plan[w];
+    for (int w = 0; w < 4; w++) work += s_plan[w];
     const int64_t C = split_keys(a, work);
     int64_t before = 0;
-    for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 64 * W) {
+    for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 256) {
       const int64_t s = s0 + threadIdx.x;
-      if (a.num_seqs > 64 * W) {  // else they are at hand
+      if (a.num_seqs > 256) {  // else they are at hand
         c = {0, 0};
         if (s < a.num_seqs) c = plan_count(a, s, R, &q);
       }
@@ -335,7 +335,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
       if (lane == 63) s_plan[wave] = incl;
       __syncthreads();
       int64_t at = before + incl - mine;
-      for (int w = 0; w < W; w++) {
+      for (int w = 0; w < 4; w++) {
         if (w < wave) at += s_plan[w];
         before += s_plan[w];
       }
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   __shared__ float s_m[4][kRowTile], s_l[4][kRowTile], s_q[4][D];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item<4, true>(a, kRowTile, s_plan, parts_of<D, kRowTile>(a), &it)) return;
+  if (!find_item<true>(a, kRowTile, s_plan, parts_of<D, kRowTile>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const int rows_all = it.q.m * a.group;
@@ -642,10 +642,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
 // The maximum that a row's weights are relative to is replaced only when it grows by more than
 // 2^8: until then weights of up to 2^8 are summed, which loses nothing in fp32 or as operands, and the
 // sums need not be scaled.
-#ifndef HC_TILE_ROWS
-#define HC_TILE_ROWS 128
-#endif
-constexpr int kTileRows = HC_TILE_ROWS;
+constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
 constexpr float kGrow = 8.f;
 
@@ -668,20 +665,21 @@ __device__ __forceinline__ int v_place(int row, int chunk) {
   return row * D * 2 + v_chunk<D>(row, chunk) * 16;
 }
 
-template <class T, int D, int R>
-__global__ __launch_bounds__(2 * R, 2) void k_attend_tiles(AttendArgs a) {
+template <class T, int D>
+__global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
+  constexpr int R = kTileRows;
   typedef typename T::v8 v8;
   typedef typename T::elem elem;
   constexpr int KS = D / 16;                    // product steps over the head
   constexpr int DT = D / 32;                    // 32-dim tiles of the output
   constexpr int CH = D / 8;                     // 16-byte chunks of a row
-  constexpr int W = R / 32;                     // waves
+  constexpr int W = 4;                          // waves
   constexpr int LD = kTileKeys * CH / (64 * W);      // loads of a wave, K and V each
   constexpr int BUF = kTileKeys * D * 2;        // bytes of a K or V tile
   __shared__ __align__(256) uint8_t s_k[2][BUF], s_v[2][BUF];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item<W, false>(a, R, s_plan, parts_of<D, R>(a), &it)) return;
+  if (!find_item<false>(a, R, s_plan, parts_of<D, R>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int64_t rows_all = (int64_t)it.q.m * a.group;
@@ -933,7 +931,7 @@ struct Latent {
 
 template <int R>
 __device__ __forceinline__ bool latent_item(const AttendArgs& a, int64_t* s_plan, Latent* t) {
-  if (!find_item<4, (R <= 32)>(a, R, s_plan, parts_of<kLatValue, R>(a), &t->it)) return false;
+  if (!find_item<(R <= 32)>(a, R, s_plan, parts_of<kLatValue, R>(a), &t->it)) return false;
   const Seq& q = t->it.q;
   const int64_t rows_all = (int64_t)q.m * a.group;
   t->t0 = (int64_t)t->it.tile * R;
@@ -1507,8 +1505,7 @@ template <class T, int DV, int R, class Kernel>
 hipError_t launch_split(Kernel kernel, AttendArgs a, int32_t num_cus, hipStream_t stream) {
   const Plan p = plan(&a, R, DV == kLatValue ? kLatDim : DV, num_cus);
   if (p.items > 0x7fffffff || p.joins > 0x7fffffff) return hipErrorInvalidValue;
-  const int threads = DV != kLatValue && R > 32 ? 2 * R : 256;  // a wave to 32 rows of a tile
-  kernel<<<dim3((unsigned)p.items), threads, 0, stream>>>(a);
+  kernel<<<dim3((unsigned)p.items), 256, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.joins == 0) return e;
   k_attend_join<T, DV, R><<<dim3((unsigned)p.joins), 256, 0, stream>>>(a);
@@ -1526,8 +1523,8 @@ hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hi
   if (R == kRowTile)
     return head_dim == 64 ? launch_split<T, 64, kRowTile>(k_attend_decode<T, 64>, a, num_cus, stream)
                           : launch_split<T, 128, kRowTile>(k_attend_decode<T, 128>, a, num_cus, stream);
-  return head_dim == 64 ? launch_split<T, 64, kTileRows>(k_attend_tiles<T, 64, kTileRows>, a, num_cus, stream)
-                        : launch_split<T, 128, kTileRows>(k_attend_tiles<T, 128, kTileRows>, a, num_cus, stream);
+  return head_dim == 64 ? launch_split<T, 64, kTileRows>(k_attend_tiles<T, 64>, a, num_cus, stream)
+                        : launch_split<T, 128, kTileRows>(k_attend_tiles<T, 128>, a, num_cus, stream);
 }
 
 }  // namespace
