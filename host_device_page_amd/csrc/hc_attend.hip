@@ -635,7 +635,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
 // O^T += V^T P^T as they stand; V comes from LDS transposed, in that order of the keys.  The next tile
 // is loaded into the other half of LDS while one is computed: one barrier a tile.
 //
-// Measured: a chunk of 2048 behind 14336 cached, 32/8 heads of 128, 545 us = 946 TFLOP/s; four prompts up to 4096
+// Measured: a chunk of 2048 behind 14336 cached, 32/8 heads of 128, 555 us = 929 TFLOP/s; four prompts up to 4096
 // of fp16 heads of 64, 109 us = 589 TFLOP/s. Waves in a product go before others (s_setprio): two waves of a
 // SIMD that multiply at the same time would also compute weights at the same time, 574 us for 557.
 //

@@ -17,7 +17,10 @@
  *   the per-layer exchange of a rank-sharded host tier (rank-sharded host tier
  *     page, Modifications): the owner of a layer packs the rows it loaded into a
  *     staging buffer, the other TP ranks unpack the broadcast bytes into the
- *     same slots (device memory only; the broadcast is the caller's).
+ *     same slots (device memory only; the broadcast is the caller's);
+ *   the forward pass on the device pool (no page's; what runs between two
+ *     transfers): new tokens rotated and stored in their slots, attention of new
+ *     tokens over the cached ones, and page tables forked, packed and listed.
  *
  * Host layouts:
  *   HC_LAYOUT_PAGE_FIRST      per sub-buffer [page][layer][row][elem_bytes]
