@@ -10,6 +10,7 @@
 
 #include <rocprofiler-sdk-roctx/roctx.h>
 
+#include "hc_extent.h"
 #include "hc_forward.h"
 
 using hc::PoolView;
@@ -43,13 +44,11 @@ int launched(hipError_t e, const char* what) {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;      // rows, sequences and tokens of one call
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;    // of an attention call: 32-bit positions
-constexpr int64_t kMaxStride = (int64_t)1 << 40;    // keeps every offset far inside int64
+constexpr int64_t kMaxStride = (int64_t)1 << 40;    // elements; the extents themselves are checked too
 
-// The extent of an [n][heads][dim] tensor with strides in elements, in bytes from its first
-// element: 0 when it is empty.
-int64_t tensor_bytes(const int64_t* stride, int64_t n, int64_t heads, int64_t dim) {
-  if (n <= 0 || heads <= 0) return 0;
-  return 2 * ((n - 1) * stride[0] + (heads - 1) * stride[1] + dim);
+int check_extent(const void* q, int64_t bytes, int32_t align, bool host_ok, hc::BufferCheck& check, const char* what) {
+  if (bytes == hc::kTooFar) return set_error(HC_ERR_INVALID, "%s: its strides reach past every allocation", what);
+  return check.buffer(q, bytes, align, host_ok, what);
 }
 
 int check_tensor(const void* q, const int64_t* stride, int64_t n, int64_t heads, int64_t dim, bool writes,
@@ -60,18 +59,8 @@ int check_tensor(const void* q, const int64_t* stride, int64_t n, int64_t heads,
     if (stride[k] % 8 != 0)
       return set_error(HC_ERR_UNSUPPORTED, "%s: strides must be multiples of 8 elements", what);
   }
-  if (writes) {
-    // its heads must lie apart, tokens outside heads or heads outside tokens
-    const int inner = heads > 1 && (n <= 1 || stride[1] <= stride[0]) ? 1 : 0;
-    const int64_t count[2] = {n, heads};
-    int64_t need = dim;
-    for (int k : {inner, 1 - inner}) {
-      if (count[k] <= 1) continue;
-      if (stride[k] < need) return set_error(HC_ERR_INVALID, "%s: its rows overlap", what);
-      need = stride[k] * (count[k] - 1) + need;
-    }
-  }
-  return check.buffer(q, tensor_bytes(stride, n, heads, dim), 16, false, what);
+  if (writes && !hc::rows_apart(stride, n, heads, dim)) return set_error(HC_ERR_INVALID, "%s: its rows overlap", what);
+  return check_extent(q, hc::tensor_bytes(stride, n, heads, dim), 16, false, check, what);
 }
 
 int check_list(const int64_t* q, int64_t n, hc::BufferCheck& check, const char* what) {
@@ -347,8 +336,7 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
   HC_TRY(check.buffer(d->lse, d->lse ? 4 * d->q_rows * d->q_heads : 0, 4, false, "lse"));
   if (d->q_start) HC_TRY(check_list(d->q_start, d->num_seqs + 1, check, "q_start"));
   HC_TRY(check_list(d->kv_len, d->num_seqs, check, "kv_len"));
-  if (d->table_width > 0)
-    HC_TRY(check_list(d->table, (d->num_seqs - 1) * d->table_stride + d->table_width, check, "table"));
+  HC_TRY(check_extent(d->table, hc::table_bytes(d->num_seqs, d->table_width, d->table_stride), 8, true, check, "table"));
   const int64_t work = hc::attend_workspace(a, d->head_dim, v.num_cus);
   if (work > 0) {
     if (d->workspace_bytes < work)
@@ -356,9 +344,7 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
                        (long long)d->workspace_bytes, (long long)work);
     HC_TRY(check.buffer(d->workspace, work, 16, false, "workspace"));
   }
-  if (overlap(d->q, tensor_bytes(d->q_stride, d->q_rows, d->q_heads, d->head_dim), d->out,
-              tensor_bytes(d->out_stride, d->q_rows, d->q_heads, d->value_dim)) &&
-      d->q == d->out)
+  if (d->q == d->out)
     return set_error(HC_ERR_INVALID, "out must not be q");
   a.q = (const uint8_t*)d->q;
   a.out = (uint8_t*)d->out;
@@ -391,13 +377,9 @@ int table_sizes(int64_t rows, int64_t width, int64_t stride) {
   return HC_OK;
 }
 
-int64_t table_entries(int64_t rows, int64_t width, int64_t stride) {
-  return rows > 0 && width > 0 ? (rows - 1) * stride + width : 0;
-}
-
 int check_table(const int64_t* table, const int64_t* lens, int64_t rows, int64_t width, int64_t stride,
                 hc::BufferCheck& check) {
-  HC_TRY(check_list(table, table_entries(rows, width, stride), check, "table"));
+  HC_TRY(check_extent(table, hc::table_bytes(rows, width, stride), 8, true, check, "table"));
   return check_list(lens, rows, check, "lens");
 }
 
@@ -443,15 +425,16 @@ int hc_fork_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
   HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
   HC_TRY(check_list(parents, n, check, "parents"));
   HC_TRY(check_list(free_pages, n_free, check, "free_pages"));
-  const int64_t in = table_entries(table_rows, table_width, table_stride), out = table_entries(n, table_width, out_stride);
-  HC_TRY(check_out_list(out_table, out, check, "out_table"));
+  const int64_t in = hc::table_bytes(table_rows, table_width, table_stride);
+  const int64_t out = hc::table_bytes(n, table_width, out_stride);
+  HC_TRY(check_extent(out_table, out, 8, false, check, "out_table"));
   HC_TRY(check_out_list(used, 1, check, "used"));
   const struct {
     const int64_t* list;
-    int64_t n;
-  } read[] = {{table, in}, {lens, table_rows}, {parents, n}, {free_pages, n_free}, {used, 1}};
+    int64_t bytes;
+  } read[] = {{table, in}, {lens, 8 * table_rows}, {parents, 8 * n}, {free_pages, 8 * n_free}, {used, 8}};
   for (const auto& r : read)
-    if (overlap(r.list, 8 * r.n, out_table, 8 * out) || (r.list != used && overlap(r.list, 8 * r.n, used, 8)))
+    if (overlap(r.list, r.bytes, out_table, out) || (r.list != used && overlap(r.list, r.bytes, used, 8)))
       return set_error(HC_ERR_INVALID, "out_table and used must not overlap each other or what is read");
   hc::ForkArgs a = {{table, lens, table_rows, table_width, table_stride}, parents, free_pages, n, n_free, out_table,
                     out_stride, used};
@@ -479,11 +462,11 @@ int hc_free_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
   HC_TRY(hc::pool_forward(pool, stream, &v));
   hc::BufferCheck check(v.device);
   HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
-  const int64_t in = table_entries(table_rows, table_width, table_stride), pages = v.geom->S / v.geom->P;
+  const int64_t in = hc::table_bytes(table_rows, table_width, table_stride), pages = v.geom->S / v.geom->P;
   HC_TRY(check_out_list(free_pages, pages, check, "free_pages"));
   HC_TRY(check_out_list(count, 1, check, "count"));
-  if (overlap(table, 8 * in, free_pages, 8 * pages) || overlap(lens, 8 * table_rows, free_pages, 8 * pages) ||
-      overlap(count, 8, table, 8 * in) || overlap(count, 8, lens, 8 * table_rows) ||
+  if (overlap(table, in, free_pages, 8 * pages) || overlap(lens, 8 * table_rows, free_pages, 8 * pages) ||
+      overlap(count, 8, table, in) || overlap(count, 8, lens, 8 * table_rows) ||
       overlap(count, 8, free_pages, 8 * pages))
     return set_error(HC_ERR_INVALID, "free_pages and count must not overlap each other or what is read");
   HC_TRY(check_work(v, workspace, workspace_bytes, check));
@@ -506,14 +489,14 @@ int hc_compact_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, in
   HC_TRY(hc::pool_forward(pool, stream, &v));
   hc::BufferCheck check(v.device);
   HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
-  const int64_t in = table_entries(table_rows, table_width, table_stride);
-  const int64_t out = table_entries(table_rows, table_width, out_stride);
-  HC_TRY(check_out_list(out_table, out, check, "out_table"));
+  const int64_t in = hc::table_bytes(table_rows, table_width, table_stride);
+  const int64_t out = hc::table_bytes(table_rows, table_width, out_stride);
+  HC_TRY(check_extent(out_table, out, 8, false, check, "out_table"));
   HC_TRY(check_out_list(count, 1, check, "count"));
-  if (overlap(table, 8 * in, out_table, 8 * out) && !(table == out_table && table_stride == out_stride))
+  if (overlap(table, in, out_table, out) && !(table == out_table && table_stride == out_stride))
     return set_error(HC_ERR_INVALID, "out_table overlaps the table without being it");
-  if (overlap(lens, 8 * table_rows, out_table, 8 * out) || overlap(count, 8, out_table, 8 * out) ||
-      overlap(count, 8, table, 8 * in) || overlap(count, 8, lens, 8 * table_rows))
+  if (overlap(lens, 8 * table_rows, out_table, out) || overlap(count, 8, out_table, out) ||
+      overlap(count, 8, table, in) || overlap(count, 8, lens, 8 * table_rows))
     return set_error(HC_ERR_INVALID, "out_table and count must not overlap each other or what is read");
   HC_TRY(check_work(v, workspace, workspace_bytes, check));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};

@@ -3,7 +3,7 @@
 abi_cpu: gcc, host only.  gpu_roundtrip: gcc against the HIP runtime API and the
 C oracle.  sanitize_host_{tsan,asan}: the loader and host-to-host sources built under
 a sanitizer; plan_host_asan: the write-back planner under ASan + UBSan (host code
-only).  Binaries land next to their sources
+only); forward_host_asan: the host arithmetic of the forward-pass calls, likewise.  Binaries land next to their sources
 (git-ignored)."""
 import os
 import subprocess
@@ -37,7 +37,8 @@ SANITIZERS = {
     "asan": ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer"],
 }
 HOST_SOURCES = {"sanitize_host": ["hc_loader.cpp", "hc_h2h.cpp", "hc_layout.cpp"],
-                "plan_host": ["hc_plan.cpp", "hc_layout.cpp"]}
+                "plan_host": ["hc_plan.cpp", "hc_layout.cpp"],
+                "forward_host": []}
 
 
 # ThreadSanitizer comes from ROCm's clang: its runtime intercepts pthread_cond_clockwait,

@@ -1,0 +1,76 @@
+// Host-side arithmetic of the forward-pass calls, under AddressSanitizer + UBSan.
+//
+// Extents (hc_extent.h): sizes and strides whose products pass 64 bits are told apart from small
+// tensors, small ones are counted element by element.
+#include <stdio.h>
+#include <stdlib.h>
+
+#include <set>
+#include <vector>
+
+#include "hc_extent.h"
+
+#define CHECK(cond)                                                              \
+  do {                                                                           \
+    if (!(cond)) {                                                               \
+      fprintf(stderr, "check failed at line %d: %s\n", __LINE__, #cond);         \
+      exit(1);                                                                   \
+    }                                                                            \
+  } while (0)
+
+static void extents_that_wrap() {
+  const int64_t far = (int64_t)1 << 40;
+  // (2^23 rows - 1) of stride 2^40 are 2^63 elements: in 64 bits that left 2 * dim bytes
+  for (int64_t n : {((int64_t)1 << 22) + 1, ((int64_t)1 << 23) + 1, ((int64_t)1 << 24) + 1, (int64_t)1 << 31}) {
+    const int64_t rows[2] = {far, 128}, heads[2] = {128, far};
+    CHECK(hc::tensor_bytes(rows, n, 1, 128) == hc::kTooFar);
+    CHECK(hc::tensor_bytes(heads, 1, n, 128) == hc::kTooFar);
+    CHECK(hc::rows_apart(rows, n, 8, 128));
+  }
+  const int64_t both[2] = {far, far};
+  CHECK(hc::tensor_bytes(both, 1 << 22, 1 << 22, 128) == hc::kTooFar);
+  CHECK(!hc::rows_apart(both, 1 << 24, 1 << 24, 128));  // its heads take 2^64 elements of a stride of 2^40
+  for (int64_t rows : {((int64_t)1 << 20) + 1, ((int64_t)1 << 21) + 1, ((int64_t)1 << 30), ((int64_t)1 << 31) - 1})
+    CHECK(hc::table_bytes(rows, 4, far) == hc::kTooFar);
+  // the largest that fit
+  CHECK(hc::table_bytes(2, 1, ((int64_t)1 << 60) - 2) == 8 * (((int64_t)1 << 60) - 1));
+  CHECK(hc::table_bytes(2, 1, ((int64_t)1 << 60) - 1) == hc::kTooFar);
+  const int64_t last[2] = {((int64_t)1 << 62) - 8, 8};
+  CHECK(hc::tensor_bytes(last, 2, 1, 7) == INT64_MAX - 1);
+  CHECK(hc::tensor_bytes(last, 2, 1, 8) == hc::kTooFar);
+}
+
+static void small_extents_and_overlaps() {
+  for (int64_t s0 = 0; s0 <= 40; s0 += 4)
+    for (int64_t s1 = 0; s1 <= 40; s1 += 4)
+      for (int64_t n = 0; n <= 4; n++)
+        for (int64_t heads = 0; heads <= 4; heads++)
+          for (int64_t dim : {4, 8, 12}) {
+            const int64_t stride[2] = {s0, s1};
+            std::set<int64_t> seen;
+            int64_t last = -1;
+            bool apart = true;
+            for (int64_t i = 0; i < n; i++)
+              for (int64_t h = 0; h < heads; h++)
+                for (int64_t d = 0; d < dim; d++) {
+                  const int64_t at = i * s0 + h * s1 + d;
+                  apart &= seen.insert(at).second;
+                  if (at > last) last = at;
+                }
+            CHECK(hc::tensor_bytes(stride, n, heads, dim) == 2 * (last + 1));
+            if (n > 0 && heads > 0 && hc::rows_apart(stride, n, heads, dim)) CHECK(apart);
+            // nested layouts are recognised
+            const bool rows_outside = s1 >= dim && s0 >= s1 * (heads - 1) + dim;
+            const bool heads_outside = s0 >= dim && s1 >= s0 * (n - 1) + dim;
+            if (n > 0 && heads > 0 && (rows_outside || heads_outside)) CHECK(hc::rows_apart(stride, n, heads, dim));
+            CHECK(hc::table_bytes(n, dim, s0) == (n > 0 ? 8 * ((n - 1) * s0 + dim) : 0));
+          }
+  CHECK(hc::table_bytes(5, 0, 10) == 0);
+}
+
+int main() {
+  extents_that_wrap();
+  small_extents_and_overlaps();
+  printf("forward_host ok\n");
+  return 0;
+}
