@@ -67,6 +67,7 @@ constexpr int kKinds = 8;  // gather, zc write, zc read, pads, compare, copy eng
 // a slot on a CU that the forward pass could use.  With 16, a bf16 GEMM consumer on
 // another stream overlaps 74 % of the per-layer load-back; with 256, 8 %.
 constexpr int32_t kDefaultMaxCtas = 16;
+constexpr size_t kWordsBytes = 256, kWrongAt = 64, kTakenAt = 128;  // a pool's device words
 // Staging chunks are capped at the MI355X Infinity Cache size (256 MB): the gather
 // writes a chunk and the copy engines read it back right away, so a chunk that
 // fits stays cache-resident between the two (measured: 32 x 8 MiB page images
@@ -117,10 +118,12 @@ struct hc_pool {
   int64_t staging_bytes = 0;
   int64_t chunk_pages = 0;
   uint64_t* d_tables = nullptr; // [nsub][L] layer addresses
-  int32_t* d_err = nullptr;
+  int32_t* d_err = nullptr;                 // the start of the device words below
+  hc::WrongWord* d_wrong = nullptr;
+  hc::TakenReports* d_taken = nullptr;
   unsigned long long* d_counter = nullptr;
   unsigned long long* h_counter = nullptr;  // pinned
-  int32_t* h_err = nullptr;                 // pinned
+  uint8_t* h_words = nullptr;               // pinned, a copy of the device words
   hc::Planner planner;  // write-back plan, once per burst on the CPU
   PlanBuf plan[2];
   int plan_cur = 0;
@@ -633,16 +636,21 @@ int hc_pool_create(const hc_pool_desc* desc, hc_pool** out) {
     for (int l = 0; l < L.L; l++) tables[(size_t)b * L.L + l] = (uint64_t)(uintptr_t)desc->sub[b].device_layers[l];
   if (hipMalloc((void**)&p->d_tables, tables.size() * sizeof(uint64_t)) != hipSuccess)
     return bail(set_err(HC_ERR_HIP, "hipMalloc of layer tables failed"));
-  if (hipMalloc((void**)&p->d_err, 64) != hipSuccess) return bail(set_err(HC_ERR_HIP, "hipMalloc failed"));
+  // device words: [0, 4) error bits of the transfers, [8, 16) their smallest flagged list position (none: all
+  // ones), [32, 40) counter, [kWrongAt ..) what the forward pass reported (none: all ones), [kTakenAt ..) reports
+  // that hc_pool_sync took
+  if (hipMalloc((void**)&p->d_err, kWordsBytes) != hipSuccess) return bail(set_err(HC_ERR_HIP, "hipMalloc failed"));
   p->d_counter = (unsigned long long*)((uint8_t*)p->d_err + 32);
-  if (hipHostMalloc((void**)&p->h_counter, 64, hipHostMallocDefault) != hipSuccess)
+  p->d_wrong = (hc::WrongWord*)((uint8_t*)p->d_err + kWrongAt);
+  p->d_taken = (hc::TakenReports*)((uint8_t*)p->d_err + kTakenAt);
+  if (hipHostMalloc((void**)&p->h_counter, 64 + kWordsBytes, hipHostMallocDefault) != hipSuccess)
     return bail(set_err(HC_ERR_HIP, "hipHostMalloc failed"));
-  p->h_err = (int32_t*)((uint8_t*)p->h_counter + 32);
-  // d_err: [0, 4) error bits, [8, 16) smallest flagged list position (none: all ones), [32, 40) counter
+  p->h_words = (uint8_t*)p->h_counter + 64;
   if (hipMemcpyAsync(p->d_tables, tables.data(), tables.size() * sizeof(uint64_t), hipMemcpyHostToDevice,
                      p->stream) != hipSuccess ||
-      hipMemsetAsync(p->d_err, 0, 64, p->stream) != hipSuccess ||
-      hipMemsetAsync((uint8_t*)p->d_err + 8, 0xFF, 8, p->stream) != hipSuccess)
+      hipMemsetAsync(p->d_err, 0, kWordsBytes, p->stream) != hipSuccess ||
+      hipMemsetAsync((uint8_t*)p->d_err + 8, 0xFF, 8, p->stream) != hipSuccess ||
+      hipMemsetAsync(p->d_wrong, 0xFF, sizeof(hc::WrongWord) * hc::kWrongKinds, p->stream) != hipSuccess)
     return bail(set_err(HC_ERR_HIP, "initial copies failed"));
   if (hipStreamSynchronize(p->stream) != hipSuccess) return bail(set_err(HC_ERR_HIP, "stream sync failed"));
   p->bases = std::move(tables);  // copied to the device above
@@ -705,21 +713,25 @@ int hc_pool_sync(hc_pool* p) {
   int rc = use_device(p);
   if (rc != HC_OK) return rc;
   if (stream_capturing(p)) return refuse_capture("hc_pool_sync", "it waits for the stream");
-  HIP_TRY(hipMemcpyAsync(p->h_err, p->d_err, 16, hipMemcpyDeviceToHost, p->stream));
+  HIP_TRY(hipMemcpyAsync(p->h_words, p->d_err, kTakenAt, hipMemcpyDeviceToHost, p->stream));
   HIP_TRY(hipStreamSynchronize(p->stream));
-  const int32_t e = *p->h_err;
-  if (e) {
-    uint64_t pos = 0;
-    memcpy(&pos, (const uint8_t*)p->h_err + 8, sizeof(pos));
-    HIP_TRY(hipMemsetAsync(p->d_err, 0, sizeof(int32_t), p->stream));
-    HIP_TRY(hipMemsetAsync((uint8_t*)p->d_err + 8, 0xFF, 8, p->stream));
+  hc::WrongWord words[hc::kWrongKinds], pos = hc::kNothing;
+  memcpy(words, p->h_words + kWrongAt, sizeof(words));
+  if (*(const int32_t*)p->h_words || hc::wrong_code(words, &pos)) {
+    // taken by atomics: kernels on other streams may be reporting
+    hc::TakenReports t;
+    HIP_TRY(hc::launch_take_reports(p->d_err, p->d_wrong, p->d_taken, p->stream));
+    HIP_TRY(hipMemcpyAsync(p->h_words + kTakenAt, p->d_taken, sizeof(t), hipMemcpyDeviceToHost, p->stream));
     HIP_TRY(hipStreamSynchronize(p->stream));
+    memcpy(&t, p->h_words + kTakenAt, sizeof(t));
+    pos = t.position;
+    const int32_t e = (int32_t)t.bits | hc::wrong_code(t.words, &pos);
     p->stats.device_errors++;
     return set_err(HC_ERR_DEVICE,
                    "device-side check flagged an index list (code %d:%s%s%s first flagged list position %llu)", e,
                    (e & 1) ? " index out of range;" : "",
                    (e & 2) ? " page-block rows not one whole device page;" : "",
-                   (e & 4) ? " a sequence's lengths out of bounds;" : "", (unsigned long long)pos);
+                   (e & 4) ? " a sequence's lengths out of bounds;" : "", pos);
   }
   return HC_OK;
 }
@@ -1251,7 +1263,7 @@ int graph_matches(const hc_pool* pool, const void* graph, void* const* events, i
 void pool_view(const hc_pool* p, PoolView* out) {
   out->geom = &p->geom;
   out->bases = p->bases.data();
-  out->err = p->d_err;
+  out->wrong = p->d_wrong;
   out->device = p->device;
   out->num_cus = p->num_cus;
   out->pages = p->lay.S % p->lay.P == 0;

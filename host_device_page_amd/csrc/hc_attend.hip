@@ -52,9 +52,8 @@ struct F16 {
   }
 };
 
-__device__ __forceinline__ void flag(int32_t* err, int bit, int64_t pos) {
-  atomicOr(err, bit);
-  atomicMin(reinterpret_cast<unsigned long long*>(err + 2), (unsigned long long)pos);
+__device__ __forceinline__ void flag(WrongWord* wrong, Wrong kind, int64_t pos) {
+  report_wrong<DeviceAtomic>(wrong, kind, pos);
 }
 
 // A sequence's rows and cached tokens; ok only when they are inside the call's bounds.
@@ -133,7 +132,7 @@ __device__ __forceinline__ Entry entry_of(const AttendArgs& a, int64_t s, uint32
 __device__ __forceinline__ uint32_t slot_from(const AttendArgs& a, const Entry& e) {
   if (e.at < 0) return kNoSlot;
   if (e.page < 0 || e.page >= a.entries) {
-    flag(a.err, kErrIndex, e.at);
+    flag(a.wrong, kWrongIndex, e.at);
     return kNoSlot;
   }
   return (uint32_t)e.page * (uint32_t)a.entry + e.rest;
@@ -297,7 +296,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
     // prefix over threads (1.5 us of a single sequence's decoding)
     for (int64_t s = 0; s < a.num_seqs; s++) {
       c = plan_count(a, s, R, &q);
-      if (blockIdx.x == 0 && threadIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
+      if (blockIdx.x == 0 && threadIdx.x == 0 && !q.ok) flag(a.wrong, kWrongLengths, s);
       work += c.tiles * c.n;
     }
     const int64_t C = split_keys(a, work);
@@ -312,7 +311,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
   } else {
     for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
       c = plan_count(a, s, R, &q);
-      if (blockIdx.x == 0 && !q.ok) flag(a.err, kErrLengths, s);
+      if (blockIdx.x == 0 && !q.ok) flag(a.wrong, kWrongLengths, s);
       work += c.tiles * c.n;
     }
     for (int d = 1; d < 64; d <<= 1) work += __shfl_xor(work, d);

@@ -225,7 +225,7 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
   a.q_out = (uint8_t*)d->q_out;
   a.k_rows = layer_rows(v, 0, d->layer);
   a.v_rows = d->value_dim > 0 ? layer_rows(v, 1, d->layer) : nullptr;
-  a.err = v.err;
+  a.wrong = v.wrong;
   a.n = d->n;
   a.S = v.geom->S;
   for (int k = 0; k < 2; k++) {
@@ -354,7 +354,7 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
   a.table = d->table;
   a.k_rows = layer_rows(v, 0, d->layer);
   a.v_rows = layer_rows(v, d->value_in_key ? 0 : 1, d->layer);
-  a.err = v.err;
+  a.wrong = v.wrong;
   a.work = (float*)d->workspace;
   return launched(hc::launch_attend(a, d->dtype, d->head_dim, v.num_cus, (hipStream_t)stream), "attention");
 }
@@ -406,7 +406,7 @@ int hc_copy_pages(hc_pool* pool, const int64_t* src, const int64_t* dst, int64_t
   hc::BufferCheck check(v.device);
   HC_TRY(check_list(src, n, check, "src"));
   HC_TRY(check_list(dst, n, check, "dst"));
-  return launched(hc::launch_copy_pages(*v.geom, src, dst, n, v.err, v.num_cus, (hipStream_t)stream), "page copy");
+  return launched(hc::launch_copy_pages(*v.geom, src, dst, n, v.wrong, v.num_cus, (hipStream_t)stream), "page copy");
 }
 
 int hc_fork_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64_t table_width, int64_t table_stride,
@@ -438,7 +438,7 @@ int hc_fork_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
       return set_error(HC_ERR_INVALID, "out_table and used must not overlap each other or what is read");
   hc::ForkArgs a = {{table, lens, table_rows, table_width, table_stride}, parents, free_pages, n, n_free, out_table,
                     out_stride, used};
-  return launched(hc::launch_fork_pages(*v.geom, a, v.err, v.num_cus, (hipStream_t)stream), "fork");
+  return launched(hc::launch_fork_pages(*v.geom, a, v.wrong, v.num_cus, (hipStream_t)stream), "fork");
 }
 
 int hc_pages_workspace_bytes(const hc_pool* pool, int64_t* out_bytes) {
@@ -471,7 +471,7 @@ int hc_free_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
     return set_error(HC_ERR_INVALID, "free_pages and count must not overlap each other or what is read");
   HC_TRY(check_work(v, workspace, workspace_bytes, check));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};
-  return launched(hc::launch_free_pages(*v.geom, t, free_pages, count, workspace, v.err, v.num_cus,
+  return launched(hc::launch_free_pages(*v.geom, t, free_pages, count, workspace, v.wrong, v.num_cus,
                                         (hipStream_t)stream),
                   "free list");
 }
@@ -500,7 +500,7 @@ int hc_compact_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, in
     return set_error(HC_ERR_INVALID, "out_table and count must not overlap each other or what is read");
   HC_TRY(check_work(v, workspace, workspace_bytes, check));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};
-  return launched(hc::launch_compact_pages(*v.geom, t, out_table, out_stride, count, workspace, v.err, v.num_cus,
+  return launched(hc::launch_compact_pages(*v.geom, t, out_table, out_stride, count, workspace, v.wrong, v.num_cus,
                                            (hipStream_t)stream),
                   "compaction");
 }

@@ -9,12 +9,9 @@
 
 #include "hc.h"
 #include "hc_internal.h"
+#include "hc_wrong.h"
 
 namespace hc {
-
-// Error bits of the pool's error word.
-constexpr int kErrIndex = 1;    // an index out of range
-constexpr int kErrLengths = 4;  // a sequence's lengths out of bounds
 
 // The turn per position of each rotated pair, as a fraction of 2^64: position * turns,
 // modulo 2^64, is the angle's fraction of a full turn, exact but for the rounding of
@@ -32,7 +29,7 @@ struct StoreArgs {
   const uint8_t *q, *k, *v;
   uint8_t* q_out;
   uint8_t *k_rows, *v_rows;  // the layer's sub-buffers
-  int32_t* err;
+  WrongWord* wrong;  // the pool's words of what is found wrong
   int64_t n, S;
   int64_t q_stride[2], q_out_stride[2], k_stride[2], v_stride[2];  // elements
   int32_t q_heads, kv_heads, head_dim, value_dim;
@@ -45,7 +42,7 @@ struct AttendArgs {
   float* lse;
   const int64_t *q_start, *kv_len, *table;
   const uint8_t *k_rows, *v_rows;
-  int32_t* err;
+  WrongWord* wrong;  // the pool's words of what is found wrong
   float* work;  // partial results of split sequences
   int64_t q_stride[2], out_stride[2], table_width, table_stride;
   int64_t k_row, v_row;  // elements from token to token in the layer's rows
@@ -76,13 +73,13 @@ struct ForkArgs {
   int64_t out_stride;
   int64_t* used;
 };
-hipError_t launch_copy_pages(const Geom& g, const int64_t* src, const int64_t* dst, int64_t n, int32_t* err,
+hipError_t launch_copy_pages(const Geom& g, const int64_t* src, const int64_t* dst, int64_t n, WrongWord* wrong,
                              int32_t num_cus, hipStream_t stream);
-hipError_t launch_fork_pages(const Geom& g, const ForkArgs& a, int32_t* err, int32_t num_cus, hipStream_t stream);
+hipError_t launch_fork_pages(const Geom& g, const ForkArgs& a, WrongWord* wrong, int32_t num_cus, hipStream_t stream);
 int64_t pages_workspace(const Geom& g);
 hipError_t launch_free_pages(const Geom& g, const PageTable& t, int64_t* pages, int64_t* count, void* work,
-                             int32_t* err, int32_t num_cus, hipStream_t stream);
+                             WrongWord* wrong, int32_t num_cus, hipStream_t stream);
 hipError_t launch_compact_pages(const Geom& g, const PageTable& t, int64_t* out, int64_t out_stride, int64_t* count,
-                                void* work, int32_t* err, int32_t num_cus, hipStream_t stream);
+                                void* work, WrongWord* wrong, int32_t num_cus, hipStream_t stream);
 
 }  // namespace hc

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include "hc.h"
+#include "hc_wrong.h"
 
 namespace hc {
 
@@ -85,11 +86,14 @@ void pool_release(hc_pool* pool);
 // `events` (L entries, in layer order); else HC_ERR_INVALID with a message.
 int graph_matches(const hc_pool* pool, const void* graph, void* const* events, int32_t L);
 
+// Takes what the transfers (err: bits, the smallest position 8 bytes behind) and the forward pass reported.
+hipError_t launch_take_reports(int32_t* err, WrongWord* words, TakenReports* out, hipStream_t stream);
+
 // What the forward-pass operators (hc_forward.cpp) see of a pool.
 struct PoolView {
   const Geom* geom;
   const uint64_t* bases;  // host copy of the layer addresses, [nsub][L]
-  int32_t* err;           // the pool's device error word
+  WrongWord* wrong;       // the pool's device words of what the operators find wrong
   int32_t device, num_cus;
   bool pages;             // device_slots is a multiple of page_size
 };

@@ -30,9 +30,8 @@ typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(1))) const v4u* gload_t;
 typedef __attribute__((address_space(1))) v4u* gstore_t;
 
-__device__ __forceinline__ void flag(int32_t* err, int bit, int64_t pos) {
-  atomicOr(err, bit);
-  atomicMin(reinterpret_cast<unsigned long long*>(err + 2), (unsigned long long)pos);
+__device__ __forceinline__ void flag(WrongWord* wrong, Wrong kind, int64_t pos) {
+  report_wrong<DeviceAtomic>(wrong, kind, pos);
 }
 
 // Entries of row s that count: ceil(len / P), 0 for a length out of bounds.
@@ -106,7 +105,7 @@ __device__ __forceinline__ void copy_unit(const Geom& g, const Pieces& pc, int64
 
 __global__ __launch_bounds__(kThreads) void k_copy_pages(Geom g, Pieces pc, const int64_t* __restrict__ src,
                                                          const int64_t* __restrict__ dst, int64_t n,
-                                                         int32_t* __restrict__ err) {
+                                                         WrongWord* __restrict__ wrong) {
   const int64_t pages = g.S / g.P;
   const int64_t units = n * g.L * pc.end[g.nsub - 1];
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
@@ -114,7 +113,7 @@ __global__ __launch_bounds__(kThreads) void k_copy_pages(Geom g, Pieces pc, cons
       *from = src[i];
       *to = dst[i];
       const bool ok = *from >= 0 && *from < pages && *to >= 0 && *to < pages;
-      if (!ok && first && threadIdx.x == 0) flag(err, kErrIndex, i);
+      if (!ok && first && threadIdx.x == 0) flag(wrong, kWrongIndex, i);
       *rows = ok && *from != *to ? g.P : 0;
     });
 }
@@ -141,7 +140,7 @@ __device__ __forceinline__ int64_t block_prefix(int64_t x, int64_t* s, int64_t* 
 
 // Numbers the children that need a page of their own and writes that entry of their rows.
 __global__ __launch_bounds__(kScanThreads) void k_fork_plan(int32_t P, int64_t pages, ForkArgs a,
-                                                            int32_t* __restrict__ err) {
+                                                            WrongWord* __restrict__ wrong) {
   __shared__ int64_t s_wave[kScanThreads / 64];
   int64_t taken = 0;
   for (int64_t i0 = 0; i0 < a.n; i0 += blockDim.x) {
@@ -153,9 +152,9 @@ __global__ __launch_bounds__(kScanThreads) void k_fork_plan(int32_t P, int64_t p
         bool bad;
         row_entries(a.table, r, P, &bad);
         len = bad ? 0 : a.table.lens[r];
-        if (bad) flag(err, kErrLengths, i);
+        if (bad) flag(wrong, kWrongLengths, i);
       } else {
-        flag(err, kErrIndex, i);
+        flag(wrong, kWrongIndex, i);
       }
     }
     int64_t sum;
@@ -164,7 +163,7 @@ __global__ __launch_bounds__(kScanThreads) void k_fork_plan(int32_t P, int64_t p
     if (len % P != 0) {
       int64_t page = rank < a.n_free ? a.free_pages[rank] : -1;
       if (page < 0 || page >= pages) {
-        flag(err, kErrIndex, i);
+        flag(wrong, kWrongIndex, i);
         page = -1;
       }
       a.out[i * a.out_stride + len / P] = page;
@@ -175,7 +174,7 @@ __global__ __launch_bounds__(kScanThreads) void k_fork_plan(int32_t P, int64_t p
 
 // The other entries of the children's rows, and the filled rows of the shared last pages.
 __global__ __launch_bounds__(kThreads) void k_fork(Geom g, Pieces pc, ForkArgs a, int64_t units,
-                                                   int32_t* __restrict__ err) {
+                                                   WrongWord* __restrict__ wrong) {
   const int64_t pages = g.S / g.P;
   auto length = [&](int64_t r) -> int64_t {
     bool bad;
@@ -200,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void k_fork(Geom g, Pieces pc, ForkArgs a
       *from = a.table.entries[r * a.table.stride + len / g.P];
       *to = a.out[i * a.out_stride + len / g.P];
       if (*from < 0 || *from >= pages) {
-        if (first && threadIdx.x == 0) flag(err, kErrIndex, i);
+        if (first && threadIdx.x == 0) flag(wrong, kWrongIndex, i);
         *rows = 0;
       } else if (*to < 0 || *to == *from) {
         *rows = 0;
@@ -229,19 +228,19 @@ __global__ __launch_bounds__(kThreads) void k_clear(int32_t* __restrict__ mark, 
 }
 
 __global__ __launch_bounds__(kThreads) void k_mark(PageTable t, int32_t P, int64_t pages, int32_t* __restrict__ mark,
-                                                   int32_t* __restrict__ err) {
+                                                   WrongWord* __restrict__ wrong) {
   const int64_t entries = t.rows * t.width;
   for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < entries; e += (int64_t)gridDim.x * kThreads) {
     const int64_t s = e / t.width, j = e - s * t.width;
     bool bad;
     const int64_t n = row_entries(t, s, P, &bad);
-    if (bad && j == 0) flag(err, kErrLengths, s);
+    if (bad && j == 0) flag(wrong, kWrongLengths, s);
     if (j >= n) continue;
     const int64_t p = t.entries[s * t.stride + j];
     if (p >= 0 && p < pages)
       mark[p] = 1;
     else
-      flag(err, kErrIndex, e);
+      flag(wrong, kWrongIndex, e);
   }
 }
 
@@ -285,7 +284,7 @@ constexpr int64_t kLivePages = 131072;
 
 __global__ __launch_bounds__(kScanThreads) void k_live(PageTable t, int32_t P, int64_t pages, Work w,
                                                        int64_t* __restrict__ free_pages, int64_t* __restrict__ count,
-                                                       int32_t compact, int32_t* __restrict__ err) {
+                                                       int32_t compact, WrongWord* __restrict__ wrong) {
   __shared__ uint32_t s_live[kLivePages / 32];
   __shared__ int64_t s_wave[kScanThreads / 64];
   const int words = (int)((pages + 31) / 32);
@@ -296,13 +295,13 @@ __global__ __launch_bounds__(kScanThreads) void k_live(PageTable t, int32_t P, i
     const int s = e / width, j = e - s * width;
     bool bad;
     const int64_t n = row_entries(t, s, P, &bad);
-    if (bad && j == 0) flag(err, kErrLengths, s);
+    if (bad && j == 0) flag(wrong, kWrongLengths, s);
     if (j >= n) continue;
     const int64_t p = t.entries[s * t.stride + j];
     if (p >= 0 && p < pages)
       atomicOr(&s_live[p >> 5], 1u << (p & 31));
     else
-      flag(err, kErrIndex, e);
+      flag(wrong, kWrongIndex, e);
   }
   __syncthreads();
   int64_t mine = 0, live, sum;
@@ -377,55 +376,55 @@ unsigned grid_of(int64_t items, int32_t num_cus) {
 // 11.4 and 16.1, 16384 entries 12.6 and 17.2, 32768 entries 21.1 and 17.4; 16384 pages and 16384 entries 15.7
 // and 37.8; 131072 pages and 16384 entries 75 and 256.
 hipError_t launch_live(const Geom& g, const PageTable& t, const Work& w, int64_t* free_pages, int64_t* count,
-                       int32_t compact, int32_t* err, int32_t num_cus, hipStream_t stream) {
+                       int32_t compact, WrongWord* wrong, int32_t num_cus, hipStream_t stream) {
   const int64_t pages = g.S / g.P, entries = t.rows * t.width;
   if (entries <= kLiveEntries && pages <= kLivePages) {
-    k_live<<<dim3(1), kScanThreads, 0, stream>>>(t, g.P, pages, w, free_pages, count, compact, err);
+    k_live<<<dim3(1), kScanThreads, 0, stream>>>(t, g.P, pages, w, free_pages, count, compact, wrong);
     return hipGetLastError();
   }
   k_clear<<<dim3((unsigned)((pages + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(w.mark, pages);
   if (entries > 0)
     k_mark<<<dim3(grid_of((entries + kThreads - 1) / kThreads, num_cus)), kThreads, 0, stream>>>(t, g.P, pages, w.mark,
-                                                                                               err);
+                                                                                               wrong);
   k_scan<<<dim3(1), kScanThreads, 0, stream>>>(w, pages, free_pages, count, compact);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_copy_pages(const Geom& g, const int64_t* src, const int64_t* dst, int64_t n, int32_t* err,
+hipError_t launch_copy_pages(const Geom& g, const int64_t* src, const int64_t* dst, int64_t n, WrongWord* wrong,
                              int32_t num_cus, hipStream_t stream) {
   if (n <= 0) return hipSuccess;
   const Pieces pc = layer_pieces(g);
   const int64_t units = n * g.L * pc.end[g.nsub - 1];
   (void)hipGetLastError();
-  k_copy_pages<<<dim3(grid_of(units, num_cus)), kThreads, 0, stream>>>(g, pc, src, dst, n, err);
+  k_copy_pages<<<dim3(grid_of(units, num_cus)), kThreads, 0, stream>>>(g, pc, src, dst, n, wrong);
   return hipGetLastError();
 }
 
-hipError_t launch_fork_pages(const Geom& g, const ForkArgs& a, int32_t* err, int32_t num_cus, hipStream_t stream) {
+hipError_t launch_fork_pages(const Geom& g, const ForkArgs& a, WrongWord* wrong, int32_t num_cus, hipStream_t stream) {
   const Pieces pc = layer_pieces(g);
   const int64_t units = a.n * g.L * pc.end[g.nsub - 1];
   (void)hipGetLastError();
-  k_fork_plan<<<dim3(1), kScanThreads, 0, stream>>>(g.P, g.S / g.P, a, err);
-  if (a.n > 0) k_fork<<<dim3(grid_of(units, num_cus)), kThreads, 0, stream>>>(g, pc, a, units, err);
+  k_fork_plan<<<dim3(1), kScanThreads, 0, stream>>>(g.P, g.S / g.P, a, wrong);
+  if (a.n > 0) k_fork<<<dim3(grid_of(units, num_cus)), kThreads, 0, stream>>>(g, pc, a, units, wrong);
   return hipGetLastError();
 }
 
 int64_t pages_workspace(const Geom& g) { return 16 + (g.S / g.P) * 12; }
 
 hipError_t launch_free_pages(const Geom& g, const PageTable& t, int64_t* pages, int64_t* count, void* work,
-                             int32_t* err, int32_t num_cus, hipStream_t stream) {
+                             WrongWord* wrong, int32_t num_cus, hipStream_t stream) {
   const Work w = work_of(work, g.S / g.P);
   (void)hipGetLastError();
-  return launch_live(g, t, w, pages, count, 0, err, num_cus, stream);
+  return launch_live(g, t, w, pages, count, 0, wrong, num_cus, stream);
 }
 
 hipError_t launch_compact_pages(const Geom& g, const PageTable& t, int64_t* out, int64_t out_stride, int64_t* count,
-                                void* work, int32_t* err, int32_t num_cus, hipStream_t stream) {
+                                void* work, WrongWord* wrong, int32_t num_cus, hipStream_t stream) {
   const Work w = work_of(work, g.S / g.P);
   (void)hipGetLastError();
-  hipError_t e = launch_live(g, t, w, nullptr, count, 1, err, num_cus, stream);
+  hipError_t e = launch_live(g, t, w, nullptr, count, 1, wrong, num_cus, stream);
   if (e != hipSuccess) return e;
   if (t.rows * t.width == 0) return hipSuccess;  // nothing is named, nothing moves
   k_compact<<<dim3((unsigned)num_cus * 8), kThreads, 0, stream>>>(g, layer_pieces(g), t, w, out, out_stride);

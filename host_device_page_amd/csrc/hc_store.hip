@@ -51,10 +51,7 @@ __global__ __launch_bounds__(kThreads) void k_store_tokens(StoreArgs a, int32_t 
   if ((int)threadIdx.x < count) {
     const int64_t slot = a.slots[t0 + threadIdx.x];
     const bool ok = slot >= 0 && slot < a.S;
-    if (!ok && slot != -1 && split == 0) {
-      atomicOr(a.err, kErrIndex);
-      atomicMin(reinterpret_cast<unsigned long long*>(a.err + 2), (unsigned long long)(t0 + threadIdx.x));
-    }
+    if (!ok && slot != -1 && split == 0) report_wrong<DeviceAtomic>(a.wrong, kWrongIndex, t0 + threadIdx.x);
     s_slot[threadIdx.x] = ok ? slot : -1;
   }
   for (int i = threadIdx.x; i < count * pairs; i += kThreads) {

@@ -2,13 +2,18 @@
 //
 // Extents (hc_extent.h): sizes and strides whose products pass 64 bits are told apart from small
 // tensors, small ones are counted element by element.
+//
+// Reports (hc_wrong.h): two reports made between any two steps of a hc_pool_sync that takes others;
+// each is in what this sync or the next one takes, with its position.
 #include <stdio.h>
 #include <stdlib.h>
 
+#include <functional>
 #include <set>
 #include <vector>
 
 #include "hc_extent.h"
+#include "hc_wrong.h"
 
 #define CHECK(cond)                                                              \
   do {                                                                           \
@@ -68,7 +73,82 @@ static void small_extents_and_overlaps() {
   CHECK(hc::table_bytes(5, 0, 10) == 0);
 }
 
+// Atomics that let something else happen before each of them.
+struct Stepped {
+  static std::function<void()> between;
+  static void minimum(hc::WrongWord* word, hc::WrongWord x) {
+    if (x < *word) *word = x;
+  }
+  static hc::WrongWord exchange(hc::WrongWord* word, hc::WrongWord x) {
+    between();
+    const hc::WrongWord old = *word;
+    *word = x;
+    return old;
+  }
+};
+std::function<void()> Stepped::between;
+
+// The reports of one hc_pool_sync: a look at the words, and if there is something, all of it taken.
+static std::vector<hc::WrongWord> sync_takes(hc::WrongWord* words) {
+  std::vector<hc::WrongWord> taken(hc::kWrongKinds, hc::kNothing);
+  Stepped::between();
+  std::vector<hc::WrongWord> seen(words, words + hc::kWrongKinds);
+  hc::WrongWord first = hc::kNothing;
+  if (hc::wrong_code(seen.data(), &first)) hc::take_wrong<Stepped>(words, taken.data());
+  Stepped::between();
+  return taken;
+}
+
+static void reports_beside_a_sync() {
+  struct Report {
+    hc::Wrong kind;
+    int64_t position;
+    int step;  // made before this step
+  };
+  for (int before = 0; before < 2; before++)  // something to take at the start
+    for (int i = 0; i < 4; i++)
+      for (int j = 0; j < 4; j++)
+        for (int kinds = 0; kinds < 4; kinds++)
+          for (int order = 0; order < 2; order++) {
+            hc::WrongWord words[hc::kWrongKinds] = {hc::kNothing, hc::kNothing};
+            if (before) hc::report_wrong<Stepped>(words, hc::kWrongIndex, 50);
+            Report r[2] = {{(kinds & 1) ? hc::kWrongLengths : hc::kWrongIndex, order ? 7 : 90, i},
+                           {(kinds & 2) ? hc::kWrongLengths : hc::kWrongIndex, order ? 90 : 7, j}};
+            int step = 0;
+            bool made[2] = {false, false};
+            Stepped::between = [&] {
+              for (int k = 0; k < 2; k++)
+                if (r[k].step == step) {
+                  hc::report_wrong<Stepped>(words, r[k].kind, r[k].position);
+                  made[k] = true;
+                }
+              step++;
+            };
+            std::vector<std::vector<hc::WrongWord>> takes = {sync_takes(words)};
+            while (step < 4) Stepped::between();
+            Stepped::between = [] {};
+            takes.push_back(sync_takes(words));
+            takes.push_back(sync_takes(words));
+            for (int k = 0; k < 2; k++) {
+              CHECK(made[k]);
+              bool found = false;
+              for (auto& t : takes) found |= t[r[k].kind] <= (hc::WrongWord)r[k].position;
+              CHECK(found);
+            }
+            if (before) CHECK(takes[0][hc::kWrongIndex] <= 50);
+            CHECK(takes[2][0] == hc::kNothing && takes[2][1] == hc::kNothing);  // and nothing twice
+          }
+  hc::WrongWord words[hc::kWrongKinds] = {hc::kNothing, hc::kNothing}, first = hc::kNothing;
+  CHECK(hc::wrong_code(words, &first) == 0 && first == hc::kNothing);
+  words[hc::kWrongLengths] = 9;
+  CHECK(hc::wrong_code(words, &first) == 4 && first == 9);
+  words[hc::kWrongIndex] = 3;
+  first = 12;  // what the transfers reported
+  CHECK(hc::wrong_code(words, &first) == 5 && first == 3);
+}
+
 int main() {
+  reports_beside_a_sync();
   extents_that_wrap();
   small_extents_and_overlaps();
   printf("forward_host ok\n");
