@@ -188,7 +188,15 @@ __global__ __launch_bounds__(kThreads) void k_fork(Geom g, Pieces pc, ForkArgs a
     const int64_t r = a.parents[i];
     const int64_t len = length(r);
     if (j == len / g.P && len % g.P != 0) continue;  // its own page, numbered already
-    a.out[i * a.out_stride + j] = j < len / g.P ? a.table.entries[r * a.table.stride + j] : -1;
+    int64_t page = -1;
+    if (j < len / g.P) {
+      page = a.table.entries[r * a.table.stride + j];
+      if (page < 0 || page >= pages) {
+        flag(wrong, kWrongIndex, i);
+        page = -1;
+      }
+    }
+    a.out[i * a.out_stride + j] = page;
   }
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
     copy_unit(g, pc, a.n, u, [&](int64_t i, int64_t* from, int64_t* to, int64_t* rows, bool first) {

@@ -555,7 +555,9 @@ int hc_copy_pages(hc_pool* pool, const int64_t* src, const int64_t* dst, int64_t
  * parent's page are copied to it (a page block as a whole).  out_table[i][0 .. table_width)
  * is the child's row, -1 behind its pages; *used is the number of free pages the children need.
  * A child that finds no free page left, or whose parent is out of range, is reported, its
- * entry (its whole row) -1.  out_table and used must not overlap what is read. */
+ * entry (its whole row) -1.  A full page of the parent that is outside the pool is -1 in the
+ * child's row; where it is the partly filled one, the child's own page stays as it was.  Both
+ * are reported.  out_table and used must not overlap what is read. */
 int hc_fork_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64_t table_width, int64_t table_stride,
                   const int64_t* lens, const int64_t* parents, int64_t n, const int64_t* free_pages, int64_t n_free,
                   int64_t* out_table, int64_t out_stride, int64_t* used, void* stream);
