@@ -230,6 +230,17 @@ __host__ __device__ inline Work work_of(void* w, int64_t pages) {
   return k;
 }
 
+// The lengths of a table without entries, none of which a pass over the entries sees.
+__device__ __forceinline__ void check_lengths(const PageTable& t, int32_t P, WrongWord* wrong, int64_t first,
+                                              int64_t step) {
+  if (t.width > 0) return;
+  for (int64_t s = first; s < t.rows; s += step) {
+    bool bad;
+    row_entries(t, s, P, &bad);
+    if (bad) flag(wrong, kWrongLengths, s);
+  }
+}
+
 __global__ __launch_bounds__(kThreads) void k_clear(int32_t* __restrict__ mark, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i < n) mark[i] = 0;
@@ -237,6 +248,7 @@ __global__ __launch_bounds__(kThreads) void k_clear(int32_t* __restrict__ mark, 
 
 __global__ __launch_bounds__(kThreads) void k_mark(PageTable t, int32_t P, int64_t pages, int32_t* __restrict__ mark,
                                                    WrongWord* __restrict__ wrong) {
+  check_lengths(t, P, wrong, (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads);
   const int64_t entries = t.rows * t.width;
   for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < entries; e += (int64_t)gridDim.x * kThreads) {
     const int64_t s = e / t.width, j = e - s * t.width;
@@ -298,6 +310,7 @@ __global__ __launch_bounds__(kScanThreads) void k_live(PageTable t, int32_t P, i
   const int words = (int)((pages + 31) / 32);
   for (int i = threadIdx.x; i < words; i += kScanThreads) s_live[i] = 0;
   __syncthreads();
+  check_lengths(t, P, wrong, threadIdx.x, kScanThreads);
   const int entries = (int)(t.rows * t.width), width = (int)t.width;
   for (int e = threadIdx.x; e < entries; e += kScanThreads) {
     const int s = e / width, j = e - s * width;
@@ -391,9 +404,9 @@ hipError_t launch_live(const Geom& g, const PageTable& t, const Work& w, int64_t
     return hipGetLastError();
   }
   k_clear<<<dim3((unsigned)((pages + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(w.mark, pages);
-  if (entries > 0)
-    k_mark<<<dim3(grid_of((entries + kThreads - 1) / kThreads, num_cus)), kThreads, 0, stream>>>(t, g.P, pages, w.mark,
-                                                                                               wrong);
+  if (t.rows > 0)
+    k_mark<<<dim3(grid_of(((t.width > 0 ? entries : t.rows) + kThreads - 1) / kThreads, num_cus)), kThreads, 0, stream>>>(
+        t, g.P, pages, w.mark, wrong);
   k_scan<<<dim3(1), kScanThreads, 0, stream>>>(w, pages, free_pages, count, compact);
   return hipGetLastError();
 }

@@ -55,3 +55,22 @@ def test_entries_behind_a_length_are_not_read(pool):
     pool.fork_pages(table, ints([PAGE, 0]), ints([0, 1]), ints([15]), out)
     pool.sync()
     assert out.tolist() == [[3, -1], [-1, -1]]
+
+
+@pytest.mark.parametrize("pages", [20, 131073])
+def test_lengths_of_a_table_without_entries(pages):
+    """Rows of no entries: a length above 0 is out of bounds like any other, on both sides of what one
+    workgroup scans."""
+    dev = [torch.zeros((1, pages, 16), dtype=torch.uint8, device="cuda")]
+    pool = F.pool_of(dev, 1)
+    empty = torch.empty((300, 0), dtype=torch.int64, device="cuda")
+    lens = torch.zeros(300, dtype=torch.int64)
+    free, n = pool.free_pages(empty, lens.cuda())
+    assert n.item() == pages and torch.equal(free.cpu(), torch.arange(pages))
+    assert pool.compact_pages(empty, lens.cuda(), empty).item() == 0
+    pool.sync()
+    lens[280:] = 1
+    for call in (lambda: pool.free_pages(empty, lens.cuda())[1], lambda: pool.compact_pages(empty, lens.cuda(), empty)):
+        assert call().item() in (0, pages)
+        reported(pool, "lengths out of bounds; first flagged list position 280")
+    pool.close()
