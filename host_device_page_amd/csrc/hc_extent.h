@@ -31,10 +31,57 @@ inline bool rows_apart(const int64_t* stride, int64_t n, int64_t heads, int64_t 
   return true;
 }
 
+// [a, a + an) and [b, b + bn) share a byte.
+inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
 // Bytes of a table of int64 entries from its first one: 0 when it has none.
 inline int64_t table_bytes(int64_t rows, int64_t width, int64_t stride) {
   if (rows <= 0 || width <= 0) return 0;
   return extent(8 * ((__int128)(rows - 1) * stride + width));
+}
+
+// A tensor of `elem`-byte elements, strides (of the token and of the head) in elements.
+struct Tensor {
+  const void* at;
+  int64_t stride[2];
+  int64_t n, heads, dim;
+  int32_t elem = 2;
+  int64_t bytes() const { return elem == 2 ? tensor_bytes(stride, n, heads, dim) : table_bytes(n, dim, stride[0]); }
+};
+// A table as one: a row of entries per "token".
+inline Tensor table_tensor(const void* at, int64_t rows, int64_t width, int64_t stride) {
+  return {at, {stride, 0}, rows, 1, width, 8};
+}
+
+// Two tensors of the same element size, whose extents fit, share an element.  Views of one buffer lie
+// between each other's tokens and heads, so where both step alike the heads are compared one by one; tensors
+// of unlike head strides are compared token by token, of unlike token strides as a whole, and may be
+// taken to share what they only enclose.
+inline bool share(const Tensor& a, const Tensor& b) {
+  if (!overlap(a.at, a.bytes(), b.at, b.bytes())) return false;
+  if (a.n > 1 && b.n > 1 && a.stride[0] != b.stride[0]) return true;
+  const int64_t token = a.elem * (a.n > 1 ? a.stride[0] : b.n > 1 ? b.stride[0] : 0);
+  const bool alike = a.heads <= 1 || b.heads <= 1 || a.stride[1] == b.stride[1];
+  const int64_t head = alike ? a.elem * (a.heads > 1 ? a.stride[1] : b.heads > 1 ? b.stride[1] : 0) : 0;
+  // bytes compared: a head's, or all from a token's first head to its last
+  const int64_t an = a.elem * (alike ? a.dim : (a.heads - 1) * a.stride[1] + a.dim);
+  const int64_t bn = b.elem * (alike ? b.dim : (b.heads - 1) * b.stride[1] + b.dim);
+  const int64_t off = (int64_t)((uintptr_t)b.at - (uintptr_t)a.at);
+  for (int64_t h = alike ? -(a.heads - 1) : 0; h <= (alike ? b.heads - 1 : 0); h++) {
+    // token i of a meets token j of b where (i - j) * token is in (low, high)
+    const int64_t low = off + h * head - an, high = off + h * head + bn;
+    int64_t k = 0;
+    if (token > 0) {
+      k = low >= 0 ? low / token + 1 : -((-low - 1) / token);  // the least with k * token > low
+      if (k < 1 - b.n) k = 1 - b.n;
+      if (k > a.n - 1) continue;
+    }
+    if (k * token > low && k * token < high) return true;
+  }
+  return false;
 }
 
 }  // namespace hc

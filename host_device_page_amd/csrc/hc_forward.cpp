@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <new>
 
 #include <rocprofiler-sdk-roctx/roctx.h>
@@ -72,11 +73,12 @@ int check_out_list(const int64_t* q, int64_t n, hc::BufferCheck& check, const ch
   return check.buffer(q, n * (int64_t)sizeof(int64_t), 8, false, what);
 }
 
-// [a, a + an) and [b, b + bn) share a byte.
-bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
-}
+struct Span {
+  const void* at;
+  int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) { return hc::overlap(a.at, a.bytes, b.at, b.bytes); }
+Span span_of(const hc::Tensor& t) { return {t.at, t.bytes()}; }
 
 // Sub-buffer b holds token rows of exactly `elems` 2-byte elements.
 int check_rows(const PoolView& v, int b, int64_t elems, const char* what) {
@@ -96,6 +98,10 @@ int check_layer(const PoolView& v, int32_t layer, int32_t dtype) {
 
 uint8_t* layer_rows(const PoolView& v, int b, int32_t layer) {
   return (uint8_t*)(uintptr_t)v.bases[(size_t)b * v.geom->L + layer];
+}
+
+Span layer_span(const PoolView& v, int b, int32_t layer) {
+  return {layer_rows(v, b, layer), v.geom->S * v.geom->sub[b].elem};
 }
 
 }  // namespace
@@ -214,6 +220,19 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
         d->n * d->q_heads > 1)
       return set_error(HC_ERR_INVALID, "q_out in place of q needs q's strides");
   }
+  const hc::Tensor q = {d->q, {d->q_stride[0], d->q_stride[1]}, d->n, d->q_heads, d->head_dim};
+  const hc::Tensor q_out = {d->q_out, {d->q_out_stride[0], d->q_out_stride[1]}, d->n, d->q_heads, d->head_dim};
+  const hc::Tensor k = {d->k, {d->k_stride[0], d->k_stride[1]}, d->n, d->kv_heads, d->head_dim};
+  const hc::Tensor v_in = {d->v, {d->v_stride[0], d->v_stride[1]}, d->n, d->value_dim > 0 ? d->kv_heads : 0,
+                           d->value_dim};
+  const Span slots = {d->slots, 8 * d->n}, positions = {d->positions, d->rope ? 8 * d->n : 0};
+  if ((q_out.at != q.at && share(q_out, q)) || share(q_out, k) || share(q_out, v_in) ||
+      overlap(span_of(q_out), slots) || overlap(span_of(q_out), positions))
+    return set_error(HC_ERR_INVALID, "q_out overlaps what is read");
+  for (int b = 0; b < (d->value_dim > 0 ? 2 : 1); b++)
+    for (const Span& x : {span_of(q), span_of(q_out), span_of(k), span_of(v_in), slots, positions})
+      if (overlap(x, layer_span(v, b, d->layer)))
+        return set_error(HC_ERR_INVALID, "the call's buffers must not overlap the layer's rows");
   hc::StoreArgs a;
   memset(&a, 0, sizeof(a));
   if (d->rope) a.rope = d->rope->table;
@@ -344,8 +363,24 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
                        (long long)d->workspace_bytes, (long long)work);
     HC_TRY(check.buffer(d->workspace, work, 16, false, "workspace"));
   }
-  if (d->q == d->out)
-    return set_error(HC_ERR_INVALID, "out must not be q");
+  const hc::Tensor q = {d->q, {d->q_stride[0], d->q_stride[1]}, d->q_rows, d->q_heads, d->head_dim};
+  const hc::Tensor out = {d->out, {d->out_stride[0], d->out_stride[1]}, d->q_rows, d->q_heads, d->value_dim};
+  if (share(q, out)) return set_error(HC_ERR_INVALID, "out must not overlap q");
+  const Span writes[] = {span_of(out), {d->lse, d->lse ? 4 * d->q_rows * d->q_heads : 0}, {d->workspace, work}};
+  const Span reads[] = {span_of(q),
+                        {d->q_start, d->q_start ? 8 * (d->num_seqs + 1) : 0},
+                        {d->kv_len, 8 * d->num_seqs},
+                        {d->table, hc::table_bytes(d->num_seqs, d->table_width, d->table_stride)},
+                        layer_span(v, 0, d->layer),
+                        layer_span(v, d->value_in_key ? 0 : 1, d->layer)};
+  for (int w = 0; w < 3; w++) {
+    for (int r = w == 0 ? 1 : 0; r < 6; r++)  // out and q are compared above
+      if (overlap(writes[w], reads[r]))
+        return set_error(HC_ERR_INVALID, "out, lse and the workspace must not overlap what is read");
+    for (int o = 0; o < w; o++)
+      if (overlap(writes[w], writes[o]))
+        return set_error(HC_ERR_INVALID, "out, lse and the workspace must not overlap each other");
+  }
   a.q = (const uint8_t*)d->q;
   a.out = (uint8_t*)d->out;
   a.lse = d->lse;
@@ -383,12 +418,17 @@ int check_table(const int64_t* table, const int64_t* lens, int64_t rows, int64_t
   return check_list(lens, rows, check, "lens");
 }
 
-int check_work(const PoolView& v, const void* work, int64_t bytes, hc::BufferCheck& check) {
+// The workspace, apart from the call's other buffers.
+int check_work(const PoolView& v, const void* work, int64_t bytes, hc::BufferCheck& check,
+               std::initializer_list<Span> others) {
   const int64_t need = hc::pages_workspace(*v.geom);
   if (bytes < need)
     return set_error(HC_ERR_INVALID, "workspace_bytes %lld below the %lld that are needed", (long long)bytes,
                      (long long)need);
-  return check.buffer(work, need, 16, false, "workspace");
+  HC_TRY(check.buffer(work, need, 16, false, "workspace"));
+  for (const Span& o : others)
+    if (overlap({work, need}, o)) return set_error(HC_ERR_INVALID, "the workspace overlaps another buffer");
+  return HC_OK;
 }
 
 }  // namespace
@@ -425,17 +465,14 @@ int hc_fork_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
   HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
   HC_TRY(check_list(parents, n, check, "parents"));
   HC_TRY(check_list(free_pages, n_free, check, "free_pages"));
-  const int64_t in = hc::table_bytes(table_rows, table_width, table_stride);
-  const int64_t out = hc::table_bytes(n, table_width, out_stride);
-  HC_TRY(check_extent(out_table, out, 8, false, check, "out_table"));
+  const hc::Tensor in = hc::table_tensor(table, table_rows, table_width, table_stride);
+  const hc::Tensor out = hc::table_tensor(out_table, n, table_width, out_stride);
+  HC_TRY(check_extent(out_table, out.bytes(), 8, false, check, "out_table"));
   HC_TRY(check_out_list(used, 1, check, "used"));
-  const struct {
-    const int64_t* list;
-    int64_t bytes;
-  } read[] = {{table, in}, {lens, 8 * table_rows}, {parents, 8 * n}, {free_pages, 8 * n_free}, {used, 8}};
-  for (const auto& r : read)
-    if (overlap(r.list, r.bytes, out_table, out) || (r.list != used && overlap(r.list, r.bytes, used, 8)))
-      return set_error(HC_ERR_INVALID, "out_table and used must not overlap each other or what is read");
+  bool shared = share(in, out) || overlap(span_of(in), {used, 8});
+  for (const Span& r : {Span{lens, 8 * table_rows}, Span{parents, 8 * n}, Span{free_pages, 8 * n_free}, Span{used, 8}})
+    shared |= overlap(r, span_of(out)) || (r.at != used && overlap(r, {used, 8}));
+  if (shared) return set_error(HC_ERR_INVALID, "out_table and used must not overlap each other or what is read");
   hc::ForkArgs a = {{table, lens, table_rows, table_width, table_stride}, parents, free_pages, n, n_free, out_table,
                     out_stride, used};
   return launched(hc::launch_fork_pages(*v.geom, a, v.wrong, v.num_cus, (hipStream_t)stream), "fork");
@@ -462,14 +499,14 @@ int hc_free_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, int64
   HC_TRY(hc::pool_forward(pool, stream, &v));
   hc::BufferCheck check(v.device);
   HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
-  const int64_t in = hc::table_bytes(table_rows, table_width, table_stride), pages = v.geom->S / v.geom->P;
-  HC_TRY(check_out_list(free_pages, pages, check, "free_pages"));
+  const Span in = {table, hc::table_bytes(table_rows, table_width, table_stride)}, lengths = {lens, 8 * table_rows};
+  const Span list = {free_pages, 8 * (v.geom->S / v.geom->P)}, number = {count, 8};
+  HC_TRY(check.buffer(free_pages, list.bytes, 8, false, "free_pages"));
   HC_TRY(check_out_list(count, 1, check, "count"));
-  if (overlap(table, in, free_pages, 8 * pages) || overlap(lens, 8 * table_rows, free_pages, 8 * pages) ||
-      overlap(count, 8, table, in) || overlap(count, 8, lens, 8 * table_rows) ||
-      overlap(count, 8, free_pages, 8 * pages))
+  if (overlap(in, list) || overlap(lengths, list) || overlap(number, in) || overlap(number, lengths) ||
+      overlap(number, list))
     return set_error(HC_ERR_INVALID, "free_pages and count must not overlap each other or what is read");
-  HC_TRY(check_work(v, workspace, workspace_bytes, check));
+  HC_TRY(check_work(v, workspace, workspace_bytes, check, {in, lengths, list, number}));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};
   return launched(hc::launch_free_pages(*v.geom, t, free_pages, count, workspace, v.wrong, v.num_cus,
                                         (hipStream_t)stream),
@@ -489,16 +526,17 @@ int hc_compact_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, in
   HC_TRY(hc::pool_forward(pool, stream, &v));
   hc::BufferCheck check(v.device);
   HC_TRY(check_table(table, lens, table_rows, table_width, table_stride, check));
-  const int64_t in = hc::table_bytes(table_rows, table_width, table_stride);
-  const int64_t out = hc::table_bytes(table_rows, table_width, out_stride);
-  HC_TRY(check_extent(out_table, out, 8, false, check, "out_table"));
+  const hc::Tensor in = hc::table_tensor(table, table_rows, table_width, table_stride);
+  const hc::Tensor out = hc::table_tensor(out_table, table_rows, table_width, out_stride);
+  const Span lengths = {lens, 8 * table_rows}, number = {count, 8};
+  HC_TRY(check_extent(out_table, out.bytes(), 8, false, check, "out_table"));
   HC_TRY(check_out_list(count, 1, check, "count"));
-  if (overlap(table, in, out_table, out) && !(table == out_table && table_stride == out_stride))
+  if (share(in, out) && !(table == out_table && table_stride == out_stride))
     return set_error(HC_ERR_INVALID, "out_table overlaps the table without being it");
-  if (overlap(lens, 8 * table_rows, out_table, out) || overlap(count, 8, out_table, out) ||
-      overlap(count, 8, table, in) || overlap(count, 8, lens, 8 * table_rows))
+  if (overlap(lengths, span_of(out)) || overlap(number, span_of(out)) || overlap(number, span_of(in)) ||
+      overlap(number, lengths))
     return set_error(HC_ERR_INVALID, "out_table and count must not overlap each other or what is read");
-  HC_TRY(check_work(v, workspace, workspace_bytes, check));
+  HC_TRY(check_work(v, workspace, workspace_bytes, check, {span_of(in), lengths, span_of(out), number}));
   const hc::PageTable t = {table, lens, table_rows, table_width, table_stride};
   return launched(hc::launch_compact_pages(*v.geom, t, out_table, out_stride, count, workspace, v.wrong, v.num_cus,
                                            (hipStream_t)stream),

@@ -398,6 +398,11 @@ int hc_layer_unpack(hc_pool* pool, int32_t layer, const void* src, int64_t src_b
  * or writes; a workspace is written by the call that gets it, so calls that can run
  * at once (two captured graphs among them) need their own.
  *
+ * What a call writes overlaps nothing that it reads or writes besides (but for what is said at
+ * hc_store_tokens and hc_compact_pages), and calls where it does are refused.  Views of one buffer
+ * that lie between each other's rows are fine when their token strides are equal and their head
+ * strides are equal or their tokens apart; tables when their row strides are equal.
+ *
  * Elements are bf16 or fp16.  Sub-buffer 0 of the pool holds keys, a row of
  * kv_heads * head_dim elements per token, sub-buffer 1 values, kv_heads * value_dim
  * elements; both are token rows.  A latent cache (MLA) has one row per token that is
@@ -453,7 +458,7 @@ int hc_rope_frequencies(const hc_rope* rope, double* out_frequencies, double* ou
  *   positions  n int64, any value.
  *   q, q_out   queries of q_heads heads, or both NULL (q_heads 0).  q_out may be q itself
  *              with the same strides (in place); otherwise inputs and outputs must not
- *              overlap, nor k and v the pool's rows.
+ *              overlap, nor any of them the layer's rows.
  *   strides    in elements, of the token and of the head, >= 0 and multiples of 8; the
  *              elements of a head are contiguous and every base address is 16-byte
  *              aligned.  A stride of 0 (one token or head for all) is fine for inputs; the

@@ -3,6 +3,9 @@
 // Extents (hc_extent.h): sizes and strides whose products pass 64 bits are told apart from small
 // tensors, small ones are counted element by element.
 //
+// Overlap of two strided tensors, against every element of both: never missed, and told apart exactly
+// where both step alike.
+//
 // Reports (hc_wrong.h): two reports made between any two steps of a hc_pool_sync that takes others;
 // each is in what this sync or the next one takes, with its position.
 #include <stdio.h>
@@ -71,6 +74,47 @@ static void small_extents_and_overlaps() {
             CHECK(hc::table_bytes(n, dim, s0) == (n > 0 ? 8 * ((n - 1) * s0 + dim) : 0));
           }
   CHECK(hc::table_bytes(5, 0, 10) == 0);
+}
+
+static void tensors_that_share() {
+  uint64_t seed = 1;
+  auto below = [&](int n) {
+    seed = seed * 6364136223846793005ull + 1442695040888963407ull;
+    return (int64_t)((seed >> 33) % n);
+  };
+  static int16_t memory[4096];
+  int alike = 0, apart = 0, enclosed = 0;
+  for (int round = 0; round < 300000; round++) {
+    hc::Tensor t[2];
+    std::set<int64_t> at[2];
+    const int64_t token = below(30), head = below(12);
+    for (int i = 0; i < 2; i++) {
+      const bool own = below(3) == 0;
+      const int64_t base = below(120);
+      t[i] = {memory + base, {own ? below(30) : token, own ? below(12) : head}, below(5), below(4), 1 + below(5)};
+      for (int64_t n = 0; n < t[i].n; n++)
+        for (int64_t h = 0; h < t[i].heads; h++)
+          for (int64_t d = 0; d < t[i].dim; d++) at[i].insert(base + n * t[i].stride[0] + h * t[i].stride[1] + d);
+    }
+    bool want = false;
+    for (int64_t x : at[0]) want |= at[1].count(x) > 0;
+    const bool got = hc::share(t[0], t[1]);
+    CHECK(got == hc::share(t[1], t[0]));
+    CHECK(got || !want);
+    const bool tokens = t[0].n <= 1 || t[1].n <= 1 || t[0].stride[0] == t[1].stride[0];
+    const bool heads = t[0].heads <= 1 || t[1].heads <= 1 || t[0].stride[1] == t[1].stride[1];
+    if (tokens && heads) CHECK(got == want);
+    alike += tokens && heads && want;
+    apart += tokens && heads && !want && !at[0].empty() && !at[1].empty() &&
+             hc::overlap(t[0].at, t[0].bytes(), t[1].at, t[1].bytes());
+    enclosed += got && !want;
+  }
+  CHECK(alike > 10000 && apart > 1000 && enclosed > 100);  // all of it was met
+  // tables side by side in one buffer of rows of 8 entries
+  static int64_t rows[64];
+  CHECK(!hc::share(hc::table_tensor(rows, 8, 4, 8), hc::table_tensor(rows + 4, 8, 4, 8)));
+  CHECK(hc::share(hc::table_tensor(rows, 8, 5, 8), hc::table_tensor(rows + 4, 7, 4, 8)));
+  CHECK(hc::share(hc::table_tensor(rows, 8, 4, 8), hc::table_tensor(rows, 8, 4, 8)));
 }
 
 // Atomics that let something else happen before each of them.
@@ -151,6 +195,7 @@ int main() {
   reports_beside_a_sync();
   extents_that_wrap();
   small_extents_and_overlaps();
+  tensors_that_share();
   printf("forward_host ok\n");
   return 0;
 }

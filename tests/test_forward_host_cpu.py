@@ -9,8 +9,8 @@ import build as cbuild  # noqa: E402
 
 
 def test_host_arithmetic_under_sanitizers():
-    """Extents of tensors and tables from sizes and strides, those that pass 64 bits among them, and
-    reports made between the steps of a sync that takes others."""
+    """Extents of tensors and tables from sizes and strides, those that pass 64 bits among them, overlaps
+    of strided tensors, and reports made between the steps of a sync that takes others."""
     exe = cbuild.build_sanitized("asan", "forward_host")
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1", UBSAN_OPTIONS="halt_on_error=1 print_stacktrace=1")
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120, env=env)
