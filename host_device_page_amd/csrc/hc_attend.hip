@@ -142,10 +142,9 @@ __device__ __forceinline__ uint32_t slot_of(const AttendArgs& a, int64_t s, uint
 }
 
 // 16 bytes a lane from memory into LDS, lane i to lds + 16 i (lds the same in all lanes), past the
-// registers.  Nothing waits for it but lds_arrived, of the wave that loaded.  (The compiler keeps nothing
-// in m0.)
+// registers.  Nothing waits for it but lds_arrived, of the wave that loaded.
 __device__ __forceinline__ void lds_load(const uint8_t* from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
 }
 __device__ __forceinline__ void lds_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
@@ -952,7 +951,7 @@ template <int OFFSET>
 __device__ __forceinline__ void lds_load_at(const uint8_t* from, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds), "v"(from),
                "n"(OFFSET)
-               : "memory");
+               : "memory", "m0");
 }
 template <int... B>
 __device__ __forceinline__ void latent_load_key(const uint8_t* from, uint32_t lds, std::integer_sequence<int, B...>) {
