@@ -111,6 +111,12 @@ __device__ __forceinline__ uint64_t sees(const AttendArgs& a, const Span& s, uin
   return m;
 }
 
+// |scale| in base 2, above 0: hidden scores are -infinity and have to stay that.  For a scale of 0 it is fp32's
+// least number, which brings the largest scores down to 2^-21, so that all weights are alike.
+__device__ __forceinline__ float weight_scale(const AttendArgs& a) {
+  return a.scale == 0.f ? 0x1p-149f : fabsf(a.scale) * kLog2e;
+}
+
 constexpr uint32_t kNoSlot = 0xffffffffu;  // layers hold fewer rows: 2^32 of the smallest are 512 GiB
 
 // Slot of key j (below 2^31) of sequence s in two steps, so that a kernel can load a table entry long
@@ -696,9 +702,8 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   const int part = ((span.n + it.splits - 1) / it.splits + kTileKeys - 1) / kTileKeys * kTileKeys;
   const int i0 = (int64_t)it.split * part < span.n ? it.split * part : span.n;
   const int i1 = i0 + part < span.n ? i0 + part : span.n;
-  // weights are exp2(c * score - c * maximum) with c > 0; a negative scale turns the queries' sign, and
-  // for 0 every finite score times c is 0
-  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+  // weights are exp2(c * score - c * maximum); a negative scale turns the queries' sign
+  const float c = weight_scale(a);
   v8 q[KS];
   {
     const v4u* qp = reinterpret_cast<const v4u*>(a.q + 2 * (row * a.q_stride[0] + h * a.q_stride[1]));
@@ -1034,7 +1039,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
   if (!latent_item<R>(a, s_plan, &t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+  const float c = weight_scale(a);
   v8 q[RB][KS];
   int p[RB];
 #pragma unroll
@@ -1230,7 +1235,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   const int wi = wave >> 1, wj = wave & 1;
   const int rr = wi * 32 + col;  // this lane's row of the scores
   const int tok = t.token(a, rr), p = t.before + tok;
-  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+  const float c = weight_scale(a);
   v8 q[KS];
   {
     const v4u* qp = reinterpret_cast<const v4u*>(
