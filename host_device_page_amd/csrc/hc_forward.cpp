@@ -54,7 +54,9 @@ int check_extent(const void* q, int64_t bytes, int32_t align, bool host_ok, hc::
 
 int check_tensor(const void* q, const int64_t* stride, int64_t n, int64_t heads, int64_t dim, bool writes,
                  hc::BufferCheck& check, const char* what) {
+  const int64_t count[2] = {n, heads};
   for (int k = 0; k < 2; k++) {
+    if (count[k] <= 1) continue;  // no step is taken
     if (stride[k] < 0 || stride[k] > kMaxStride)
       return set_error(HC_ERR_INVALID, "%s: stride %lld out of range", what, (long long)stride[k]);
     if (stride[k] % 8 != 0)
@@ -216,8 +218,8 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
   if (d->q_heads > 0) {
     HC_TRY(check_tensor(d->q, d->q_stride, d->n, d->q_heads, d->head_dim, false, check, "q"));
     HC_TRY(check_tensor(d->q_out, d->q_out_stride, d->n, d->q_heads, d->head_dim, true, check, "q_out"));
-    if (d->q_out == d->q && (d->q_out_stride[0] != d->q_stride[0] || d->q_out_stride[1] != d->q_stride[1]) &&
-        d->n * d->q_heads > 1)
+    if (d->q_out == d->q && ((d->n > 1 && d->q_out_stride[0] != d->q_stride[0]) ||
+                             (d->q_heads > 1 && d->q_out_stride[1] != d->q_stride[1])))
       return set_error(HC_ERR_INVALID, "q_out in place of q needs q's strides");
   }
   const hc::Tensor q = {d->q, {d->q_stride[0], d->q_stride[1]}, d->n, d->q_heads, d->head_dim};
@@ -531,7 +533,7 @@ int hc_compact_pages(hc_pool* pool, const int64_t* table, int64_t table_rows, in
   const Span lengths = {lens, 8 * table_rows}, number = {count, 8};
   HC_TRY(check_extent(out_table, out.bytes(), 8, false, check, "out_table"));
   HC_TRY(check_out_list(count, 1, check, "count"));
-  if (share(in, out) && !(table == out_table && table_stride == out_stride))
+  if (share(in, out) && !(table == out_table && (table_stride == out_stride || table_rows == 1)))
     return set_error(HC_ERR_INVALID, "out_table overlaps the table without being it");
   if (overlap(lengths, span_of(out)) || overlap(number, span_of(out)) || overlap(number, span_of(in)) ||
       overlap(number, lengths))

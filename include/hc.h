@@ -462,7 +462,8 @@ int hc_rope_frequencies(const hc_rope* rope, double* out_frequencies, double* ou
  *   strides    in elements, of the token and of the head, >= 0 and multiples of 8; the
  *              elements of a head are contiguous and every base address is 16-byte
  *              aligned.  A stride of 0 (one token or head for all) is fine for inputs; the
- *              heads of q_out must not overlap.
+ *              heads of q_out must not overlap.  Of a single token or head the stride is
+ *              not looked at.
  *   head_dim, value_dim  multiples of 8; value_dim 0: no value rows (a latent cache).
  * kv_heads * head_dim and kv_heads * value_dim must be exactly the pool's rows. */
 typedef struct hc_store_desc {
