@@ -149,6 +149,9 @@ __device__ __forceinline__ uint32_t slot_of(const AttendArgs& a, int64_t s, uint
 
 // 16 bytes a lane from memory into LDS, lane i to lds + 16 i (lds the same in all lanes), past the
 // registers.  Nothing waits for it but lds_arrived, of the wave that loaded.
+// (m0 is reserved, which the compiler remarks on: it keeps no values of its own there, but what it puts there for an
+// instruction has to be put there again behind this.)
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_load(const uint8_t* from, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
 }
