@@ -238,7 +238,7 @@ struct Item {
   int64_t s;
   Seq q;
   int32_t hk, tile, split, splits;
-  int64_t index;  // place in the list: where its partial result lies
+  int64_t index;  // place in the list: where its partial result lies, if its tile is split
 };
 
 struct PlanCount {
@@ -262,7 +262,7 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t x) {  // inclusive
   return x;
 }
 
-// What the joining launch has to know of an item, behind the partial results.
+// What the joining launch has to know of an item that has a place for a partial result, behind all of those.
 struct Part {
   int64_t splits;  // of the tile whose first split the item is, else 0
   int64_t q0, m, tile_hk;
@@ -289,9 +289,12 @@ __device__ __forceinline__ void set_item(const AttendArgs& a, Item* it, int64_t 
 
 // Finds item blockIdx.x of the list (256 threads; s_plan: 8 int64); false when the list is shorter.
 // `parts`: where the items' Parts are kept, when there is a joining launch.
+// SPLIT_FIRST: calls with fewer places of partial results than items, in which the items of split tiles come first in
+// the list, so that a partial result's place stays its item's.  (Kernels of their own: the other calls' loops get
+// registers as if there were none, which otherwise cost 1.5 % of a chunk of 2048.)
 // FEW: calls of a few sequences have a way of their own, in the kernels of few rows (in those of many it
 // cost 3 % of a chunk of 2048, 575 us for 560, by the registers that the compiler then gave the loop).
-template <bool FEW>
+template <bool FEW, bool SPLIT_FIRST>
 __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s_plan, Part* parts, Item* it) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t want = blockIdx.x;
@@ -299,7 +302,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
   Seq q = {0, 0, 0, true};
   PlanCount c = {0, 0};
   bool found = false;
-  if (FEW && a.num_seqs <= 4) {
+  if (FEW && !SPLIT_FIRST && a.num_seqs <= 4) {
     // a few sequences: every thread goes over them by itself, without the steps of a reduction and a
     // prefix over threads (1.5 us of a single sequence's decoding)
     for (int64_t s = 0; s < a.num_seqs; s++) {
@@ -329,6 +332,22 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
     for (int w = 0; w < 4; w++) work += s_plan[w];
     const int64_t C = split_keys(a, work);
     int64_t before = 0;
+    bool split_ones = false;
+    if (SPLIT_FIRST) {
+      int64_t first = 0;
+      for (int64_t s = threadIdx.x; s < a.num_seqs; s += 256) {
+        if (a.num_seqs > 256) c = plan_count(a, s, R, &q);
+        if (c.n > C) first += c.tiles * ((c.n + C - 1) / C) * a.kv_heads;
+      }
+      for (int d = 1; d < 64; d <<= 1) first += __shfl_xor(first, d);
+      __syncthreads();
+      if (lane == 0) s_plan[wave] = first;
+      __syncthreads();
+      first = 0;
+      for (int w = 0; w < 4; w++) first += s_plan[w];
+      split_ones = want < first;
+      before = split_ones ? 0 : first;
+    }
     for (int64_t s0 = 0; s0 < a.num_seqs; s0 += 256) {
       const int64_t s = s0 + threadIdx.x;
       if (a.num_seqs > 256) {  // else they are at hand
@@ -336,7 +355,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
         if (s < a.num_seqs) c = plan_count(a, s, R, &q);
       }
       const int64_t splits = c.n <= C ? 1 : (c.n + C - 1) / C;
-      const int64_t mine = c.tiles * splits * a.kv_heads;
+      const int64_t mine = SPLIT_FIRST && (splits > 1) != split_ones ? 0 : c.tiles * splits * a.kv_heads;
       const int64_t incl = wave_prefix(mine);
       __syncthreads();
       if (lane == 63) s_plan[wave] = incl;
@@ -364,7 +383,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int R, int64_t* s
       set_item(a, it, s_plan[0], {s_plan[4], (int)s_plan[5], (int)s_plan[6], true}, s_plan[3], s_plan[1], s_plan[2]);
     __syncthreads();
   }
-  if (a.join_parts > 0 && threadIdx.x == 0) {
+  if ((SPLIT_FIRST ? want < a.slots : a.join_parts > 0) && threadIdx.x == 0) {
     Part p = {0, 0, 0, 0};
     if (found && it->split == 0) p = {it->splits, it->q.q0, it->q.m, (int64_t)it->tile * a.kv_heads + it->hk};
     parts[want] = p;
@@ -379,7 +398,7 @@ __host__ __device__ constexpr int64_t partial_floats(int R) {
 }
 template <int DV, int R>
 __device__ __forceinline__ Part* parts_of(const AttendArgs& a) {
-  return reinterpret_cast<Part*>(a.work + a.items * partial_floats<DV>(R));
+  return reinterpret_cast<Part*>(a.work + a.slots * partial_floats<DV>(R));
 }
 
 // ---------------------------------------------------------------- few rows: decoding
@@ -407,7 +426,7 @@ __device__ __forceinline__ int v_swizzle(int row) {  // 16-byte chunks of a V ro
   return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3);  // the transposing reads then spread over all banks
 }
 
-template <class T, int D>
+template <class T, int D, bool SPLIT_FIRST>
 __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   typedef typename T::v8 v8;
   typedef typename T::elem elem;
@@ -419,7 +438,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
   __shared__ float s_m[4][kRowTile], s_l[4][kRowTile], s_q[4][D];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item<true>(a, kRowTile, s_plan, parts_of<D, kRowTile>(a), &it)) return;
+  if (!find_item<true, SPLIT_FIRST>(a, kRowTile, s_plan, parts_of<D, kRowTile>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const int rows_all = it.q.m * a.group;
@@ -672,7 +691,7 @@ __device__ __forceinline__ int v_place(int row, int chunk) {
   return row * D * 2 + v_chunk<D>(row, chunk) * 16;
 }
 
-template <class T, int D>
+template <class T, int D, bool SPLIT_FIRST>
 __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   constexpr int R = kTileRows;
   typedef typename T::v8 v8;
@@ -686,7 +705,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   __shared__ __align__(256) uint8_t s_k[2][BUF], s_v[2][BUF];
   __shared__ int64_t s_plan[8];
   Item it;
-  if (!find_item<false>(a, R, s_plan, parts_of<D, R>(a), &it)) return;
+  if (!find_item<false, SPLIT_FIRST>(a, R, s_plan, parts_of<D, R>(a), &it)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int64_t rows_all = (int64_t)it.q.m * a.group;
@@ -935,9 +954,9 @@ struct Latent {
   }
 };
 
-template <int R>
+template <int R, bool SPLIT_FIRST>
 __device__ __forceinline__ bool latent_item(const AttendArgs& a, int64_t* s_plan, Latent* t) {
-  if (!find_item<(R <= 32)>(a, R, s_plan, parts_of<kLatValue, R>(a), &t->it)) return false;
+  if (!find_item<(R <= 32), SPLIT_FIRST>(a, R, s_plan, parts_of<kLatValue, R>(a), &t->it)) return false;
   const Seq& q = t->it.q;
   const int64_t rows_all = (int64_t)q.m * a.group;
   t->t0 = (int64_t)t->it.tile * R;
@@ -1027,7 +1046,7 @@ __device__ __forceinline__ void latent_store(const AttendArgs& a, const Latent& 
 
 // Up to 16 or 32 rows (RB of 16): decoding.  Bound by memory: 2 * 1088 operations a row on the 1152 bytes of a
 // key.  Scores in 16 x 16 products, wave w taking keys 16 w of the tile against all rows.
-template <class T, int RB>
+template <class T, int RB, bool SPLIT_FIRST>
 __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
   typedef typename T::v8 v8;
   constexpr int R = 16 * RB;
@@ -1039,7 +1058,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
   __shared__ uint32_t s_nan[1];
   __shared__ int64_t s_plan[8];
   Latent t;
-  if (!latent_item<R>(a, s_plan, &t)) return;
+  if (!latent_item<R, SPLIT_FIRST>(a, s_plan, &t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const float c = weight_scale(a);
@@ -1221,7 +1240,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
 // registers, and keys 32 j.
 constexpr int kLatRows = 64;
 
-template <class T>
+template <class T, bool SPLIT_FIRST>
 __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   typedef typename T::v8 v8;
   constexpr int KS = kLatDim / 16;
@@ -1232,7 +1251,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   __shared__ uint32_t s_nan[2];
   __shared__ int64_t s_plan[8];
   Latent t;
-  if (!latent_item<kLatRows>(a, s_plan, &t)) return;
+  if (!latent_item<kLatRows, SPLIT_FIRST>(a, s_plan, &t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int wi = wave >> 1, wj = wave & 1;
@@ -1423,15 +1442,15 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   latent_again<T>(a, t, s_nan, reinterpret_cast<float*>(s_k) + wave * kLatDim, part_o, part_ml);
 }
 
-// Joins the splits of a row tile, a wave a row.  A workgroup looks at one item; all but the first split of
-// a tile that was split have nothing to do.
+// Joins the splits of a row tile, a wave a row.  A workgroup looks at the item of one place; all but the first
+// split of a tile that was split have nothing to do.
 template <class T, int DV, int R>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   typedef typename T::elem elem;
   const int64_t first = blockIdx.x / a.join_parts;
   const Part p = parts_of<DV, R>(a)[first];
   // a q_start that goes back (reported) can make more items than the call has room for
-  if (p.splits <= 1 || first + p.splits > a.items) return;
+  if (p.splits <= 1 || first + p.splits > a.slots) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t tile = p.tile_hk / a.kv_heads;
   const int hk = (int)(p.tile_hk - tile * a.kv_heads);
@@ -1480,42 +1499,65 @@ int tile_rows(const AttendArgs& a, int32_t head_dim) {
 // Calls of many rows are split when their row tiles, which the host knows, do not fill the GPU, or when some of
 // several sequences may be so long that their one tile each (a decoding row beside a chunk) would
 // run on alone; else one launch does all.
+//
+// Only split tiles have partial results.  A split tile of n > C keys has at most (n + C - 1) / C < 2 n / C
+// splits, so that they are less than twice the target, however many row tiles the call has.  A call of more
+// items than that has just those places, and takes the split tiles first; of another the list is left in the order
+// of the sequences, which is found sooner (38.4 us for 37.5 of a latent decoding batch).
 constexpr int64_t kLongKeys = 16384;
 struct Plan {
   int64_t items, joins;  // joins: workgroups of the second launch, 0: no split can be
+  bool few_places;       // fewer places of partial results than items
 };
 Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus) {
   const bool latent = head_dim == kLatDim, few = R <= 32;
   a->min_split = few ? 128 : 256;
-  Plan p = {most_tiles(*a, R) * a->kv_heads, 0};
+  Plan p = {most_tiles(*a, R) * a->kv_heads, 0, false};
   // items that run at once: 8 or 2 workgroups a compute unit, and one of a latent cache, where the
   // whole list, `tiles` longer than the target at most, should be one round
   a->target = (int64_t)num_cus * (few ? 8 : 2);
   if (latent) a->target = num_cus - p.items > num_cus / 2 ? num_cus - p.items : num_cus / 2;
   a->join_parts = 0;
+  a->slots = 0;
   const int64_t most_splits = (a->max_kv + a->min_split - 1) / a->min_split;
   const bool fills = a->q_rows * a->group / R * a->kv_heads >= a->target;
   if (most_splits > 1 && (few || !fills || (a->num_seqs > 1 && a->max_kv > kLongKeys))) {
     const int64_t rows = a->max_q * a->group < R ? a->max_q * a->group : R;  // of a tile at most
     a->join_parts = (int32_t)((rows + 3) / 4);
-    p.items = p.items * most_splits < p.items + a->target ? p.items * most_splits : p.items + a->target;
-    p.joins = p.items * a->join_parts;
+    p.items += most_splits - 1 <= a->target / p.items ? p.items * (most_splits - 1) : a->target;
+    p.few_places = p.items > 2 * a->target;
+    a->slots = p.few_places ? 2 * a->target : p.items;
+    p.joins = a->slots * a->join_parts;
   } else {
     a->min_split = a->max_kv + 1;
   }
-  a->items = p.items;
   return p;
 }
 
-template <class T, int DV, int R, class Kernel>
-hipError_t launch_split(Kernel kernel, AttendArgs a, int32_t num_cus, hipStream_t stream) {
+// kernels: of calls whose items all have a place for a partial result, or that are not split, and of others.
+template <class T, int DV, int R>
+hipError_t launch_split(void (*const (&kernels)[2])(AttendArgs), AttendArgs a, int32_t num_cus, hipStream_t stream) {
   const Plan p = plan(&a, R, DV == kLatValue ? kLatDim : DV, num_cus);
   if (p.items > 0x7fffffff || p.joins > 0x7fffffff) return hipErrorInvalidValue;
-  kernel<<<dim3((unsigned)p.items), 256, 0, stream>>>(a);
+  kernels[p.few_places]<<<dim3((unsigned)p.items), 256, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.joins == 0) return e;
   k_attend_join<T, DV, R><<<dim3((unsigned)p.joins), 256, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <class T, int RB>
+hipError_t launch_latent_few(const AttendArgs& a, int32_t num_cus, hipStream_t stream) {
+  return launch_split<T, kLatValue, 16 * RB>({k_attend_latent_few<T, RB, false>, k_attend_latent_few<T, RB, true>}, a,
+                                             num_cus, stream);
+}
+template <class T, int D>
+hipError_t launch_decode(const AttendArgs& a, int32_t num_cus, hipStream_t stream) {
+  return launch_split<T, D, kRowTile>({k_attend_decode<T, D, false>, k_attend_decode<T, D, true>}, a, num_cus, stream);
+}
+template <class T, int D>
+hipError_t launch_tiles(const AttendArgs& a, int32_t num_cus, hipStream_t stream) {
+  return launch_split<T, D, kTileRows>({k_attend_tiles<T, D, false>, k_attend_tiles<T, D, true>}, a, num_cus, stream);
 }
 
 template <class T>
@@ -1523,14 +1565,13 @@ hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hi
   (void)hipGetLastError();
   const int R = tile_rows(a, head_dim);
   if (head_dim == kLatDim)
-    return R == 16   ? launch_split<T, kLatValue, 16>(k_attend_latent_few<T, 1>, a, num_cus, stream)
-           : R == 32 ? launch_split<T, kLatValue, 32>(k_attend_latent_few<T, 2>, a, num_cus, stream)
-                     : launch_split<T, kLatValue, kLatRows>(k_attend_latent<T>, a, num_cus, stream);
+    return R == 16   ? launch_latent_few<T, 1>(a, num_cus, stream)
+           : R == 32 ? launch_latent_few<T, 2>(a, num_cus, stream)
+                     : launch_split<T, kLatValue, kLatRows>({k_attend_latent<T, false>, k_attend_latent<T, true>}, a,
+                                                            num_cus, stream);
   if (R == kRowTile)
-    return head_dim == 64 ? launch_split<T, 64, kRowTile>(k_attend_decode<T, 64>, a, num_cus, stream)
-                          : launch_split<T, 128, kRowTile>(k_attend_decode<T, 128>, a, num_cus, stream);
-  return head_dim == 64 ? launch_split<T, 64, kTileRows>(k_attend_tiles<T, 64>, a, num_cus, stream)
-                        : launch_split<T, 128, kTileRows>(k_attend_tiles<T, 128>, a, num_cus, stream);
+    return head_dim == 64 ? launch_decode<T, 64>(a, num_cus, stream) : launch_decode<T, 128>(a, num_cus, stream);
+  return head_dim == 64 ? launch_tiles<T, 64>(a, num_cus, stream) : launch_tiles<T, 128>(a, num_cus, stream);
 }
 
 }  // namespace
@@ -1543,7 +1584,7 @@ int64_t attend_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_c
   if (p.joins == 0) return 0;
   const int64_t floats = head_dim == 64 ? partial_floats<64>(R) : head_dim == 128 ? partial_floats<128>(R)
                                                                                  : partial_floats<kLatValue>(R);
-  return p.items * (4 * floats + (int64_t)sizeof(Part));
+  return a.slots * (4 * floats + (int64_t)sizeof(Part));
 }
 
 hipError_t launch_attend(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t num_cus, hipStream_t stream) {

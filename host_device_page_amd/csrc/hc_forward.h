@@ -49,7 +49,7 @@ struct AttendArgs {
   int64_t num_seqs, q_rows, max_q, max_kv;
   int32_t window, sinks;
   int64_t entries;                     // table entries of the pool: S / entry
-  int64_t target, min_split, items;    // how the work is split (set by launch_attend)
+  int64_t target, min_split, slots;    // how the work is split (set by launch_attend); places of partial results
   uint32_t entry_magic, entry_shift;   // j / entry == (j * magic) >> shift for j < 2^31
   int32_t q_heads, kv_heads, group, entry, causal;
   int32_t join_parts;                  // workgroups of the joining launch to a row tile
