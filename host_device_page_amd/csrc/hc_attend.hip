@@ -1487,7 +1487,12 @@ int64_t most_tiles(const AttendArgs& a, int R) {
   return a.q_rows * a.group / R + (a.num_seqs < a.q_rows ? a.num_seqs : a.q_rows);
 }
 
-// The kernel for a call: the rows of its row tiles.
+// The kernel for a call: the rows of its row tiles.  64 sequences up to 8192 tokens, 32/8 heads of 128, with several
+// new tokens each, in tiles of 16 and of 128 rows: 17 to 32 rows of a KV head 298 and 273 us, 48 rows 370 and
+// 278, 64 rows 482 and 285 (16 rows fit one tile, 230); 16/4 heads of 64: 32 rows 88 and 70, 48 rows 102 and 71.
+// So from 17 rows on tiles of 128 are ahead, and the border of 32 is a tenth to a fifth too slow for what is
+// between.  32 sequences up to 6000 tokens of a latent cache, in tiles of 32 and of 64 rows: 20 rows 43.0 and 45.1 us, 32
+// rows 46.0 and 45.3, 40 rows 62.9 and 48.0, 64 rows 70.0 and 52.1.
 int tile_rows(const AttendArgs& a, int32_t head_dim) {
   const int64_t rows = a.max_q * a.group;
   if (head_dim == kLatDim) return rows <= 16 ? 16 : rows <= 32 ? 32 : kLatRows;
@@ -1496,14 +1501,28 @@ int tile_rows(const AttendArgs& a, int32_t head_dim) {
 
 // How the list of items is made for a call of tiles of R rows, and the number of items at most: a split of
 // C keys has at least `min_split` of them, and the whole call's keys over C is at most `target`.
-// Calls of many rows are split when their row tiles, which the host knows, do not fill the GPU, or when some of
-// several sequences may be so long that their one tile each (a decoding row beside a chunk) would
-// run on alone; else one launch does all.
+//
+// min_split: few rows, with 64, 128 and 256 keys at least: one sequence of 4000 21.4, 15.8 and 15.2 us, 16 of 600 27.9,
+// 21.3 and 18.7, one of 1500 of a latent cache 18.8, 18.3 and 21.1.  Many rows, with 128, 256 and 512: a chunk of 64 behind
+// 1436 22.8, 22.3 and 26.6, of 256 behind 1744 35.1, 34.9 and 33.5, of 32 of a latent cache behind 1468 35.5, 36.1 and 43.6.
+//
+// Calls of many rows are split when their row tiles, which the host knows, are fewer than the target, or when some of
+// several sequences may be so long that their one tile each (a decoding row beside a chunk) would run on alone; else one
+// launch does all.  The second rule, applied and not: a chunk of 4096 beside one row of 32768 keys 250 and 876 us, beside
+// four of 65536 387 and 1668, a latent chunk of 512 beside one of 32768 71 and 1258; beside one of 16384 it would gain
+// too (255 and 517).  Calls whose sequences keep the GPU busy anyway pay for it: a chunk of 4096 beside 63
+// rows of 8192 686 and 670, of 32768 1772 and 1756, four fp16 prompts up to 4096 139 and 127; hence not for
+// shorter ones.
+//
+// A latent cache's target leaves places to the tiles themselves.  With the whole GPU as its target: 32 sequences
+// up to 6000 of 16 heads 52.4 us for 38.4, 16 sequences up to 16384 of 128 heads 129 for 90; but half the GPU, which
+// it comes down to, is too little where tiles are many: a chunk of 255 tokens of 32 heads 118 for 194, and from 128 tiles
+// on, where a call counts as filling that half and is not split, 64 sequences up to 16384 of 128 heads 358 for 705.
 //
 // Only split tiles have partial results.  A split tile of n > C keys has at most (n + C - 1) / C < 2 n / C
 // splits, so that they are less than twice the target, however many row tiles the call has.  A call of more
 // items than that has just those places, and takes the split tiles first; of another the list is left in the order
-// of the sequences, which is found sooner (38.4 us for 37.5 of a latent decoding batch).
+// of the sequences, which is found sooner (a sequence of 1500 12.0 us for 12.8, 64 up to 8192 207.3 for 208.1).
 constexpr int64_t kLongKeys = 16384;
 struct Plan {
   int64_t items, joins;  // joins: workgroups of the second launch, 0: no split can be

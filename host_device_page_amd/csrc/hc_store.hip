@@ -118,7 +118,9 @@ __global__ __launch_bounds__(kThreads) void k_store_tokens(StoreArgs a, int32_t 
 
 hipError_t launch_store(const StoreArgs& a, int32_t dtype, int32_t num_cus, hipStream_t stream) {
   if (a.n <= 0) return hipSuccess;
-  // Few tokens: one a workgroup, and its heads over up to 8 workgroups.
+  // Few tokens: one a workgroup, and its heads over up to 8 workgroups.  Of 32 + 8 + 8 heads of 128, in a graph: one
+  // token with its heads over 1, 8 and 16 workgroups 4.25, 3.23 and 3.18 us, 32 tokens 4.50, 3.32 and 3.52; four
+  // tokens a workgroup for one 4.00 for 3.32 us at 32 tokens, 12.9 for 12.5 at 2048, 35.2 for 35.8 at 8192.
   const int64_t fill = (int64_t)num_cus * 4;
   const int32_t tokens = a.n >= fill * kTokens ? kTokens : 1;
   const int64_t groups = (a.n + tokens - 1) / tokens;

@@ -25,3 +25,32 @@ def test_scales_next_to_zero(d, hk, hq, q, scale):
     keys[:, :] = 2.0 ** size * (torch.randint(0, 5, (len(keys), 1), generator=g) - 2) / 2
     c.upload().check(scale=scale)
     c.close()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d,hk,hq,q", HEADS)
+def test_small_weights_of_many_keys(d, hk, hq, q, dtype):
+    """One key of a large score and no value, the others of weights next to 2^-16, below fp16's normal range: what
+    they add up to is the output."""
+    c = Case(dtype=dtype, hq=hq, hk=hk, d=d, kv=(1500, 700), q=q, page=16)
+    c.q.zero_()
+    c.q[..., d - 1] = 1.0
+    keys, values = c.host[0][c.layer], c.host[-1][c.layer]
+    keys.zero_()
+    if d == 576:
+        keys.view(len(keys), hk, d)[..., :512] = 1.0
+    else:
+        values[:] = 1.0
+    first = [F.slots_of(c.table[s], 1, c.entry) for s in range(2)]
+    for where in first:
+        keys[where] = 0.0
+        keys.view(len(keys), hk, d)[where, :, d - 1] = 11.0625
+        if d != 576:
+            values[where] = 0.0
+    c.upload()
+    out, lse = c.run(scale=1.0)
+    torch.cuda.synchronize()
+    want = c.want(scale=1.0)
+    assert want[0].gt(0.009).all()
+    c.compare(out, lse, want)
+    c.close()
