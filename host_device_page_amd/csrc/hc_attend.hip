@@ -661,8 +661,9 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
 // O^T += V^T P^T as they stand; V comes from LDS transposed, in that order of the keys.  The next tile
 // is loaded into the other half of LDS while one is computed: one barrier a tile.
 //
-// Measured: a chunk of 2048 behind 14336 cached, 32/8 heads of 128, 555 us = 929 TFLOP/s; four prompts up to 4096
-// of fp16 heads of 64, 109 us = 589 TFLOP/s. Waves in a product go before others (s_setprio): two waves of a
+// Measured: a chunk of 2048 behind 14336 cached, 32/8 heads of 128, 548 to 578 us over machines = 890 to 940 TFLOP/s;
+// four prompts of unequal lengths up to 4096 of fp16 16/4 heads of 64, 114 to 121 us = 530 to 560 TFLOP/s, of
+// equal lengths 646, one of 16384 757: short prompts behind long ones leave places empty at the end. Waves in a product go before others (s_setprio): two waves of a
 // SIMD that multiply at the same time would also compute weights at the same time, 574 us for 557.
 //
 // The maximum that a row's weights are relative to is replaced only when it grows by more than
@@ -913,7 +914,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
 // two of them in LDS) is read into LDS once for both products, and its four waves cut the work
 // without doing any twice: scores by keys, values by dims, 128 a wave.  The maxima of the waves' keys
 // and then the weights go through LDS: three barriers a tile.  Measured: 32 sequences up to 6000 tokens and 16 heads
-// 33 us and 5 us to join; a chunk of 512 behind 3988 with 32 heads 190 us = 796 TFLOP/s.
+// 32 us and 5 us to join; a chunk of 512 behind 3988 with 32 heads 190 to 193 us = 784 to 796 TFLOP/s.
 constexpr int kLatKeys = 64;
 constexpr int kLatDim = 576;
 constexpr int kLatValue = 512;

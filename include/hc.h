@@ -517,7 +517,8 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* desc, void* stream);
  *   workspace  hc_attend_workspace_bytes of device memory, 16-byte aligned; may be NULL
  *              when that is 0.
  * Scores, softmax statistics and sums are fp32; a probability is rounded to the element
- * type once, as the operand of the product with the values, and the output once. */
+ * type once, as the operand of the product with the values (fp16 probabilities are off by up
+ * to 2^-25 of the row's largest too, below fp16's normal range), and the output once. */
 typedef struct hc_attend_desc {
   int32_t layer, dtype;
   int32_t q_heads, kv_heads, head_dim, value_dim;
