@@ -164,7 +164,9 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // Softmax sums of one query row over positions [i0, i1) of its span, by one wave: lanes take keys
 // for the scores and dims for the sum, and nothing of a key that the row does not see is touched.
 // The tiled kernels multiply hidden keys' values by a weight of 0, which is NaN where the value is
-// not finite; they do the rows that came out NaN again with this.  s_q: DK floats of this wave's.
+// not finite; they do the rows that came out NaN again with this, unless the sum of weights is NaN too: then a score
+// that the row sees is, and so is the row.  (One row costs as much as a hundred in tiles: 2048 rows behind 14336, all of
+// NaN queries, took 160 ms, now 0.6.)  s_q: DK floats of this wave's.
 template <class T, int DK, int DV>
 __device__ __forceinline__ void exact_row(const AttendArgs& a, int64_t s, int64_t row, int h, int p, Span span,
                                        int i0, int i1, float* s_q, float* o, float* m_out, float* l_out) {
@@ -599,10 +601,10 @@ __global__ __launch_bounds__(256, 2) void k_attend_decode(AttendArgs a) {
 #pragma unroll
     for (int e = 0; e < E; e++) acc[e] += so[(w * kRowTile + rr) * D + d0 + e] * f;
   }
-  bool nan = l_all != l_all;
+  bool nan = false;
 #pragma unroll
   for (int e = 0; e < E; e++) nan |= acc[e] != acc[e];
-  const uint64_t bits = __ballot(nan && valid);  // a row's 16 threads are in one wave
+  const uint64_t bits = __ballot(nan && valid && l_all == l_all);  // a row's 16 threads are in one wave
   const bool bad = (bits >> (lane & 48)) & 0xffff;
   float* part_o = a.work + it.index * partial_floats<D>(kRowTile);
   float* part_ml = part_o + kRowTile * D;
@@ -852,8 +854,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   for (int d = 0; d < DT; d++)
 #pragma unroll
     for (int e = 0; e < 16; e++) nan |= o[d][e] != o[d][e];
-  nan |= l != l;
-  uint64_t again = __ballot(nan && live);
+  uint64_t again = __ballot(nan && live && l == l);
   again = (again | again >> 32) & 0xffffffffu;
   const bool mine = live && !((again >> col) & 1);
   const float log2_max = m == -INFINITY ? -INFINITY : m * c;  // of the weights, in the joining kernel's unit
@@ -1004,14 +1005,17 @@ __device__ __forceinline__ void latent_clear(uint64_t there, uint8_t* tile) {
   __syncthreads();
 }
 
-// Rows that came out NaN, shared out over the waves; s_q: kLatDim floats of this wave's.
+// Rows that came out NaN, but for those whose sum of weights is NaN, shared out over the waves; s_sum: four parts of
+// R rows' sums, s_q: kLatDim floats of this wave's.
 template <class T>
-__device__ __forceinline__ void latent_again(const AttendArgs& a, const Latent& t, const uint32_t* s_nan, float* s_q,
-                                             float* part_o, float* part_ml) {
+__device__ __forceinline__ void latent_again(const AttendArgs& a, const Latent& t, const uint32_t* s_nan,
+                                             const float* s_sum, int R, float* s_q, float* part_o, float* part_ml) {
   typedef typename T::elem elem;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int x = wave; x < t.rows; x += 4) {
     if (!((s_nan[x >> 5] >> (x & 31)) & 1)) continue;
+    const float sum = s_sum[x] + s_sum[R + x] + s_sum[2 * R + x] + s_sum[3 * R + x];
+    if (sum != sum) continue;
     const int tok = t.token(a, x), h = t.head(a, x, tok);
     const int64_t row = t.it.q.q0 + tok;
     float o[kLatValue / 64], m, l;
@@ -1216,8 +1220,8 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
 #pragma unroll
   for (int b = 0; b < RB; b++) {
     const int x = b * 16 + col;
-    if (x >= t.rows || ((s_nan[0] >> x) & 1)) continue;
     const float sum = s_sum[0][x] + s_sum[1][x] + s_sum[2][x] + s_sum[3][x];
+    if (x >= t.rows || (((s_nan[0] >> x) & 1) && sum == sum)) continue;
     const int tok = t.token(a, x), h = t.head(a, x, tok);
     const int64_t row = t.it.q.q0 + tok;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -1233,7 +1237,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
       }
     }
   }
-  latent_again<T>(a, t, s_nan, reinterpret_cast<float*>(s_k) + wave * kLatDim, part_o, part_ml);
+  latent_again<T>(a, t, s_nan, &s_sum[0][0], R, reinterpret_cast<float*>(s_k) + wave * kLatDim, part_o, part_ml);
 }
 
 // 64 rows: chunks, and many heads.  Bound by the matrix cores and LDS: 240 KiB are read from it for 2176
@@ -1419,8 +1423,8 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
 #pragma unroll
   for (int i = 0; i < 2; i++) {
     const int x = i * 32 + col;
-    if (x >= t.rows || ((s_nan[i] >> col) & 1)) continue;
     const float sum = s_sum[0][x] + s_sum[1][x] + s_sum[2][x] + s_sum[3][x];
+    if (x >= t.rows || (((s_nan[i] >> col) & 1) && sum == sum)) continue;
     const int tx = t.token(a, x), hx = t.head(a, x, tx);
     const int64_t row = t.it.q.q0 + tx;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -1440,7 +1444,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
       }
     }
   }
-  latent_again<T>(a, t, s_nan, reinterpret_cast<float*>(s_k) + wave * kLatDim, part_o, part_ml);
+  latent_again<T>(a, t, s_nan, &s_sum[0][0], kLatRows, reinterpret_cast<float*>(s_k) + wave * kLatDim, part_o, part_ml);
 }
 
 // Joins the splits of a row tile, a wave a row.  A workgroup looks at the item of one place; all but the first

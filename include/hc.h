@@ -492,7 +492,9 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* desc, void* stream);
  * p - j < window or j < sinks.  What stands in rows that a query does not see never
  * reaches its output, infinities and NaN included.  A row that sees nothing (kv_len 0,
  * or more new tokens than cached ones), or whose every visible score is -infinity, is
- * zeros, its lse -infinity.
+ * zeros, its lse -infinity; one that sees a score that is NaN is NaN.  (Rows over values that are not
+ * finite, their own or hidden ones next to them, are computed one by one, which takes some
+ * hundred times as long as other rows.)
  *   q_start    num_seqs + 1 int64, not decreasing, or NULL: one query row per sequence.
  *              Rows of q behind the last sequence (a padded batch) leave out and lse as
  *              they were.
