@@ -53,6 +53,7 @@ HC_ROPE_LINEAR = 1
 HC_ROPE_LLAMA3 = 2
 HC_ROPE_YARN = 3
 HC_MAX_ROT_DIM = 256
+HC_MAX_ROPE_AXES = 8
 
 # hc_pool_kernel_time kinds
 KIND_GATHER, KIND_ZC_WRITE, KIND_ZC_READ, KIND_PADS, KIND_COMPARE, KIND_COPY_ENGINE, KIND_PACK, KIND_UNPACK = range(8)
@@ -109,11 +110,27 @@ class hc_attend_desc(ctypes.Structure):
                 + [("q_stride", _I64 * 2), ("out_stride", _I64 * 2), ("workspace", _V), ("workspace_bytes", _I64)])
 
 
-# The same two structures as the methods below fill them, once per layer and token: packed bytes
+class hc_fetch_desc(ctypes.Structure):
+    _fields_ = ([(n, _I32) for n in ("layer", "dtype", "kv_heads", "head_dim", "value_dim")]
+                + [("n", _I64)] + [(n, _V) for n in ("slots", "k", "v")]
+                + [("k_stride", _I64 * 2), ("v_stride", _I64 * 2)])
+
+
+class hc_extend_desc(ctypes.Structure):
+    _fields_ = ([("table", _V)] + [(n, _I64) for n in ("table_rows", "table_width", "table_stride")]
+                + [(n, _V) for n in ("lens", "added", "free_pages")] + [("n_free", _I64)]
+                + [(n, _V) for n in ("first_free", "kv_len", "q_start", "slots", "positions")]
+                + [("room", _I64), ("used", _V)])
+
+
+# The same structures as the methods below fill them, once per layer and token: packed bytes
 # take a fraction of the time of a ctypes structure.
 _STORE = struct.Struct("@6iq6P8qP")
 _ATTEND = struct.Struct("@9if8q6P4qPq")
+_FETCH = struct.Struct("@5iq3P4q")
+_EXTEND = struct.Struct("@P3q3Pq5PqP")
 assert _STORE.size == ctypes.sizeof(hc_store_desc) and _ATTEND.size == ctypes.sizeof(hc_attend_desc)
+assert _FETCH.size == ctypes.sizeof(hc_fetch_desc) and _EXTEND.size == ctypes.sizeof(hc_extend_desc)
 
 _D = ctypes.POINTER(hc_pool_desc)
 
@@ -151,9 +168,16 @@ _SIGS = {
     "hc_rope_create": (ctypes.c_int, [ctypes.POINTER(hc_rope_desc), ctypes.POINTER(_V)]),
     "hc_rope_destroy": (ctypes.c_int, [_V]),
     "hc_rope_frequencies": (ctypes.c_int, [_V, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+    "hc_rope_create_axes": (ctypes.c_int, [ctypes.POINTER(hc_rope_desc), _V, _I32, _I32, ctypes.POINTER(_V)]),
     "hc_store_tokens": (ctypes.c_int, [_V, _V, _V]),
+    "hc_mxfp4_row_bytes": (ctypes.c_int, [_I32, _I32, _I64P]),
+    "hc_store_tokens_mxfp4": (ctypes.c_int, [_V, _V, _V]),
+    "hc_fetch_tokens_mxfp4": (ctypes.c_int, [_V, _V, _V]),
     "hc_attend_workspace_bytes": (ctypes.c_int, [_V, _V, _I64P]),
     "hc_attend": (ctypes.c_int, [_V, _V, _V]),
+    "hc_attend_mxfp4_workspace_bytes": (ctypes.c_int, [_V, _V, _I64P]),
+    "hc_attend_mxfp4": (ctypes.c_int, [_V, _V, _V]),
+    "hc_extend_pages": (ctypes.c_int, [_V, _V, _V]),
     "hc_copy_pages": (ctypes.c_int, [_V, _V, _V, _I64, _V]),
     "hc_fork_pages": (ctypes.c_int, [_V, _V, _I64, _I64, _I64, _V, _V, _I64, _V, _I64, _V, _I64, _V, _V]),
     "hc_pages_workspace_bytes": (ctypes.c_int, [_V, _I64P]),
@@ -434,21 +458,38 @@ def _torch_int64():
 
 class Rope:
     """hc_rope: rotary positions, with their scaling for long contexts (see hc_rope_desc).
-    scaling: "none", "linear", "llama3" or "yarn"; magnitude None: the scaling's own."""
+    scaling: "none", "linear", "llama3" or "yarn"; magnitude None: the scaling's own.
+    Several axes of positions (hc_rope_create_axes): `sections`, how many pairs the first axis
+    has, then the second, ..., or `pair_axes`, every pair's axis; own_series: every axis with a
+    series of frequencies of its own.  Positions are then of (axes, tokens)."""
 
     SCALINGS = {"none": HC_ROPE_NONE, "linear": HC_ROPE_LINEAR, "llama3": HC_ROPE_LLAMA3, "yarn": HC_ROPE_YARN}
 
     def __init__(self, *, rot_dim: int, base: float = 10000.0, rot_offset: int = 0, interleaved: bool = False,
                  scaling: str = "none", factor: float = 1.0, original_context: int = 0, low_freq_factor: float = 1.0,
                  high_freq_factor: float = 4.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
-                 magnitude: float | None = None):
+                 magnitude: float | None = None, sections=None, pair_axes=None, own_series: bool = False):
+        if sections is not None:
+            if pair_axes is not None:
+                raise ValueError("sections and pair_axes say the same thing")
+            pair_axes = [a for a, n in enumerate(sections) for _ in range(n)]
+        if pair_axes is not None and len(pair_axes) != rot_dim // 2:
+            raise ValueError(f"{len(pair_axes)} pairs are given an axis, rot_dim {rot_dim} has {rot_dim // 2}")
         if scaling not in self.SCALINGS:
             raise ValueError(f"unknown scaling {scaling!r}")
         self.handle = _V()
         self.rot_dim = rot_dim
         d = hc_rope_desc(rot_dim, rot_offset, 1 if interleaved else 0, self.SCALINGS[scaling], base, factor,
                          low_freq_factor, high_freq_factor, beta_fast, beta_slow, magnitude or 0.0, original_context)
-        check(lib.hc_rope_create(ctypes.byref(d), ctypes.byref(self.handle)), "hc_rope_create")
+        if pair_axes is None:
+            self.axes = 1
+            if own_series:
+                raise ValueError("own_series without axes")
+            check(lib.hc_rope_create(ctypes.byref(d), ctypes.byref(self.handle)), "hc_rope_create")
+        else:
+            self.axes = len(sections) if sections is not None else max(pair_axes, default=0) + 1
+            check(lib.hc_rope_create_axes(ctypes.byref(d), (_I32 * len(pair_axes))(*pair_axes), self.axes,
+                                          1 if own_series else 0, ctypes.byref(self.handle)), "hc_rope_create_axes")
 
     def frequencies(self):
         """(radians per position of each pair, the factor on sines and cosines)."""
@@ -536,6 +577,22 @@ def _raw_stream(tensor) -> int:
         _current_raw_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream",
                                       lambda index: cuda.current_stream(index).cuda_stream)
     return _current_raw_stream(tensor.get_device())
+
+
+def mxfp4_row_bytes(heads: int, dim: int) -> int:
+    """Bytes of a token's row of `heads` heads of `dim` elements in a cache held in 4 bits."""
+    out = _I64()
+    check(lib.hc_mxfp4_row_bytes(heads, dim, ctypes.byref(out)), "hc_mxfp4_row_bytes")
+    return out.value
+
+
+_CACHES = ("elements", "mxfp4")  # what a pool's rows hold
+
+
+def _is_mxfp4(cache: str) -> bool:
+    if cache not in _CACHES:
+        raise ValueError(f"unknown cache {cache!r}: one of {', '.join(_CACHES)}")
+    return cache == "mxfp4"
 
 
 class Pool:
@@ -674,10 +731,12 @@ class Pool:
     # a torch stream, None for torch's current one; what a call returns newly made is that
     # stream's.
     def store_tokens(self, layer: int, slots, k, v=None, *, q=None, q_out=None, rope: Rope | None = None,
-                     positions=None, stream=None):
+                     positions=None, stream=None, cache: str = "elements"):
         """Keys k (rotated) and values v of new tokens into their slots of one layer; queries q
         rotated into q_out (q itself: in place; None: a new tensor).  k, v, q: (tokens, heads,
-        dim); v None for a latent cache.  Returns q_out."""
+        dim); v None for a latent cache.  positions: one per token, of a rope of several axes
+        (axes, tokens).  cache: "elements" (the pool's rows are of k's dtype) or "mxfp4" (rows of
+        4 bits).  Returns q_out."""
         n = _device_list(slots, "slots")
         k_at, (rows, kv_heads, dim), (k0, k1, _) = _heads(k, "k")
         if rows != n:
@@ -701,28 +760,53 @@ class Pool:
             raise ValueError("q_out without q")
         p_at = 0
         if rope is not None:
-            if _device_list(positions, "positions") != n:
-                raise ValueError("positions and slots differ in length")
+            if _device_list(positions, "positions") != n * rope.axes:
+                raise ValueError("positions and slots differ in length" if rope.axes == 1 else
+                                 f"positions must be {rope.axes} for each of {n} slots")
+            if rope.axes > 1 and tuple(positions.shape) != (rope.axes, n):
+                raise ValueError(f"positions must be of shape {(rope.axes, n)}")
             p_at = positions.data_ptr()
         d = _STORE.pack(layer, _dtype_codes[k.dtype], q_heads, kv_heads, dim, value_dim, n, slots.data_ptr(), p_at, q_at,
                         o_at, k_at, v_at, q0, q1, o0, o1, k0, k1, v0, v1,
                         0 if rope is None else rope.handle.value)
-        rc = lib.hc_store_tokens(self.handle, d, _on(stream, k, slots, positions, q, q_out, v))
+        call = lib.hc_store_tokens if cache == "elements" or not _is_mxfp4(cache) else lib.hc_store_tokens_mxfp4
+        rc = call(self.handle, d, _on(stream, k, slots, positions, q, q_out, v))
         if rc:
-            check(rc, "hc_store_tokens")
+            check(rc, call.__name__)
         return q_out
+
+    def fetch_tokens(self, layer: int, slots, k, v=None, *, stream=None):
+        """Rows of a cache held in 4 bits as elements: the key rows in `slots` into k and the value
+        rows into v (tokens, heads, dim), of bf16 or fp16; v None: only keys, for a latent cache.
+        The rows of slots that are -1 stay as they are.  Returns (k, v)."""
+        n = _device_list(slots, "slots")
+        k_at, (rows, heads, dim), (k0, k1, _) = _heads(k, "k")
+        if rows != n:
+            raise ValueError(f"k has {rows} rows for {n} slots")
+        v_at = v0 = v1 = wide = 0
+        if v is not None:
+            v_at, (rows, v_heads, wide), (v0, v1, _) = _heads(v, "v", k)
+            if rows != n or v_heads != heads:
+                raise ValueError(f"v has {rows} rows of {v_heads} heads for {n} slots and {heads} heads")
+        rc = lib.hc_fetch_tokens_mxfp4(self.handle, _FETCH.pack(layer, _dtype_codes[k.dtype], heads, dim, wide, n,
+                                                                slots.data_ptr(), k_at, v_at, k0, k1, v0, v1),
+                                       _on(stream, k, slots, v))
+        if rc:
+            check(rc, "hc_fetch_tokens_mxfp4")
+        return k, v
 
     def attend(self, layer: int, q, table, kv_len, *, kv_heads: int, q_start=None, max_q: int | None = None,
                max_kv: int | None = None, entry_tokens: int | None = None, causal: bool = True, window: int = 0,
                sinks: int = 0, scale: float | None = None, value_dim: int | None = None, out=None,
-               return_lse: bool = False, workspace=None, stream=None):
+               return_lse: bool = False, workspace=None, stream=None, cache: str = "elements"):
         """Attention of q (rows, heads, head_dim) over the cached tokens of each sequence:
         table (sequences, entries) of pages (entry_tokens: the pool's page_size, the default)
         or slots (entry_tokens=1), kv_len cached tokens per sequence, q_start the first query
         row of each sequence and the end of the last (None: one row each).  max_q, max_kv:
         no sequence has more rows, or tokens (None: what q and the table hold).  value_dim
         below head_dim: a latent cache, whose key rows hold the values.  scale None:
-        head_dim ** -0.5.  Returns (out, lse), lse None unless asked for."""
+        head_dim ** -0.5.  cache: "elements" (the pool's rows are of q's dtype) or "mxfp4" (rows
+        of 4 bits).  Returns (out, lse), lse None unless asked for."""
         q_at, (rows, heads, dim), (q0, q1, _) = _heads(q, "q")
         at, seqs, width, stride = _table(table, "table")
         if _device_list(kv_len, "kv_len") != seqs:
@@ -749,19 +833,48 @@ class Pool:
                 (1 if q_start is None else rows) if max_q is None else max_q,
                 width * entry if max_kv is None else max_kv, width, stride, q_at, o_at, l_at, s_at,
                 kv_len.data_ptr(), at, q0, q1, o0, o1)
+        call, bytes_of = ((lib.hc_attend, lib.hc_attend_workspace_bytes) if cache == "elements" or not _is_mxfp4(cache)
+                          else (lib.hc_attend_mxfp4, lib.hc_attend_mxfp4_workspace_bytes))
         if workspace is None:
             need = _I64()
-            rc = lib.hc_attend_workspace_bytes(self.handle, _ATTEND.pack(*args, 0, 0), ctypes.byref(need))
+            rc = bytes_of(self.handle, _ATTEND.pack(*args, 0, 0), ctypes.byref(need))
             if rc:
-                check(rc, "hc_attend_workspace_bytes")
+                check(rc, bytes_of.__name__)
             if need.value:
                 workspace = _new(stream, q, (need.value,), _torch().uint8)
         w_at, w_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), _staging_bytes(workspace, "workspace"))
-        rc = lib.hc_attend(self.handle, _ATTEND.pack(*args, w_at, w_bytes),
-                           _on(stream, q, table, kv_len, q_start, out, lse, workspace))
+        rc = call(self.handle, _ATTEND.pack(*args, w_at, w_bytes),
+                  _on(stream, q, table, kv_len, q_start, out, lse, workspace))
         if rc:
-            check(rc, "hc_attend")
+            check(rc, call.__name__)
         return out, lse
+
+    def extend_pages(self, table, lens, added, free_pages, *, tokens: int, first_free=None, stream=None):
+        """Grows the sequences of `table` (its new entries are written in place), of lens[s] tokens,
+        by added[s], with pages from free_pages[first_free[0]:] (None: from the first).  Returns
+        (kv_len, q_start, slots, positions, used): the new lengths, the first new token of each
+        sequence and the end of the last, the slot and position of `tokens` new tokens (behind
+        the last -1 and 0) and the number of pages taken (a one-element tensor)."""
+        at, rows, width, stride = _table(table, "table")
+        if _device_list(lens, "lens") != rows or _device_list(added, "added") != rows:
+            raise ValueError("lens and added must have an entry for each row of the table")
+        n_free = _device_list(free_pages, "free_pages")
+        first_at = 0
+        if first_free is not None:
+            if _device_list(first_free, "first_free") != 1:
+                raise ValueError("first_free must be one number")
+            first_at = first_free.data_ptr()
+        if tokens < 0:
+            raise ValueError("tokens must be >= 0")
+        out = _new(stream, table, (2 * rows + 2 + 2 * tokens,))  # one allocation for the five lists
+        o = out.data_ptr()
+        d = _EXTEND.pack(at, rows, width, stride, lens.data_ptr(), added.data_ptr(), free_pages.data_ptr(), n_free,
+                         first_at, o, o + 8 * rows, o + 8 * (2 * rows + 1), o + 8 * (2 * rows + 1 + tokens), tokens,
+                         o + 8 * (2 * rows + 1 + 2 * tokens))
+        rc = lib.hc_extend_pages(self.handle, d, _on(stream, table, lens, added, free_pages, first_free, out))
+        if rc:
+            check(rc, "hc_extend_pages")
+        return out.split_with_sizes((rows, rows + 1, tokens, tokens, 1))
 
     def copy_pages(self, src, dst, stream=None) -> None:
         """Pages src[i] to pages dst[i], in every layer and sub-buffer."""

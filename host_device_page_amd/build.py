@@ -14,7 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhc.so")
 SOURCES = ["hc_api.cpp", "hc_layout.cpp", "hc_plan.cpp", "hc_loader.cpp", "hc_h2h.cpp", "hc_kernels.hip", "hc_exchange.hip", "hc_noalloc.hip",
-           "hc_forward.cpp", "hc_store.hip", "hc_attend.hip", "hc_pages.hip", "hc_wrong.hip"]
+           "hc_forward.cpp", "hc_store.hip", "hc_attend.hip", "hc_attend_mxfp4.hip", "hc_pages.hip", "hc_extend.hip",
+           "hc_wrong.hip"]
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.environ.get("HIPCC", os.path.join(ROCM, "bin", "hipcc"))
 

@@ -13,6 +13,7 @@
 
 #include "hc_extent.h"
 #include "hc_forward.h"
+#include "hc_mxfp4.h"
 
 using hc::PoolView;
 using hc::set_error;
@@ -82,13 +83,13 @@ struct Span {
 bool overlap(const Span& a, const Span& b) { return hc::overlap(a.at, a.bytes, b.at, b.bytes); }
 Span span_of(const hc::Tensor& t) { return {t.at, t.bytes()}; }
 
-// Sub-buffer b holds token rows of exactly `elems` 2-byte elements.
-int check_rows(const PoolView& v, int b, int64_t elems, const char* what) {
+// Sub-buffer b holds token rows of exactly `elems` elements, of 2 bytes or in 4 bits.
+int check_rows(const PoolView& v, int b, int64_t elems, bool mxfp4, const char* what) {
   if (b >= v.geom->nsub || v.geom->sub[b].gran != HC_TOKEN_ROWS)
     return set_error(HC_ERR_INVALID, "the pool's sub-buffer %d does not hold %s token rows", b, what);
-  if (v.geom->sub[b].elem != 2 * elems)
-    return set_error(HC_ERR_INVALID, "%s rows of %lld elements, the pool's are %lld bytes", what, (long long)elems,
-                     (long long)v.geom->sub[b].elem);
+  if (v.geom->sub[b].elem != (mxfp4 ? hc::mxfp4_row(elems) : 2 * elems))
+    return set_error(HC_ERR_INVALID, "%s rows of %lld elements%s, the pool's are %lld bytes", what, (long long)elems,
+                     mxfp4 ? " in 4 bits" : "", (long long)v.geom->sub[b].elem);
   return HC_OK;
 }
 
@@ -110,10 +111,15 @@ Span layer_span(const PoolView& v, int b, int32_t layer) {
 
 extern "C" {
 
-int hc_rope_create(const hc_rope_desc* d, hc_rope** out) {
+int hc_rope_create(const hc_rope_desc* d, hc_rope** out) { return hc_rope_create_axes(d, nullptr, 1, 0, out); }
+
+int hc_rope_create_axes(const hc_rope_desc* d, const int32_t* pair_axes, int32_t axes, int32_t own_series,
+                        hc_rope** out) {
   if (!out) return set_error(HC_ERR_INVALID, "out is null");
   *out = nullptr;
   if (!d) return set_error(HC_ERR_INVALID, "desc is null");
+  if (axes < 1 || axes > HC_MAX_ROPE_AXES) return set_error(HC_ERR_INVALID, "axes must be in [1, %d]", HC_MAX_ROPE_AXES);
+  if (!pair_axes && axes > 1) return set_error(HC_ERR_INVALID, "pair_axes is null");
   if (d->rot_dim <= 0 || d->rot_dim > HC_MAX_ROT_DIM)
     return set_error(HC_ERR_INVALID, "rot_dim must be in [16, %d]", HC_MAX_ROT_DIM);
   if (d->rot_dim % 16 != 0) return set_error(HC_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16");
@@ -133,22 +139,26 @@ int hc_rope_create(const hc_rope_desc* d, hc_rope** out) {
     return set_error(HC_ERR_INVALID, "0 < beta_slow <= beta_fast is needed");
   if ((d->scaling == HC_ROPE_LLAMA3 || d->scaling == HC_ROPE_YARN) && d->original_context <= 0)
     return set_error(HC_ERR_INVALID, "original_context must be above 0");
-  hc_rope* r = new (std::nothrow) hc_rope();
-  if (!r) return set_error(HC_ERR_NOMEM, "rope allocation failed");
   const double pi2 = 6.283185307179586476925286766559;
   const int pairs = d->rot_dim / 2;
-  double lo = 0.0, hi = 0.0;
-  r->magnitude = d->magnitude > 0.0 ? d->magnitude : 1.0;
-  if (d->scaling == HC_ROPE_YARN) {
-    auto pair_of = [&](double turns) {
-      return pairs * log((double)d->original_context / (turns * pi2)) / log(d->base);
-    };
-    lo = fmax(floor(pair_of(d->beta_fast)), 0.0);
-    hi = fmin(ceil(pair_of(d->beta_slow)), (double)(d->rot_dim - 1));
-    if (d->magnitude == 0.0) r->magnitude = 0.1 * log(d->factor) + 1.0;
-  }
+  int32_t of_axis[HC_MAX_ROPE_AXES] = {};
   for (int i = 0; i < pairs; i++) {
-    const double f0 = exp(-log(d->base) * (2.0 * i / d->rot_dim));
+    const int32_t x = pair_axes ? pair_axes[i] : 0;
+    if (x < 0 || x >= axes) return set_error(HC_ERR_INVALID, "pair_axes[%d] = %d is not one of %d axes", i, x, axes);
+    of_axis[x]++;
+  }
+  for (int x = 0; x < axes; x++)
+    if (of_axis[x] == 0) return set_error(HC_ERR_INVALID, "axis %d has no pair", x);
+  hc_rope* r = new (std::nothrow) hc_rope();
+  if (!r) return set_error(HC_ERR_NOMEM, "rope allocation failed");
+  r->magnitude = d->magnitude > 0.0 ? d->magnitude : 1.0;
+  if (d->scaling == HC_ROPE_YARN && d->magnitude == 0.0) r->magnitude = 0.1 * log(d->factor) + 1.0;
+  int32_t at[HC_MAX_ROPE_AXES] = {};
+  for (int i = 0; i < pairs; i++) {
+    const int32_t axis = pair_axes ? pair_axes[i] : 0;
+    // pair j of a series of n
+    const int n = own_series ? of_axis[axis] : pairs, j = own_series ? at[axis]++ : i;
+    const double f0 = exp(-log(d->base) * (2.0 * j / (2 * n)));
     double keep = 1.0;  // share of the unscaled frequency
     if (d->scaling == HC_ROPE_LINEAR) {
       keep = 0.0;
@@ -156,7 +166,12 @@ int hc_rope_create(const hc_rope_desc* d, hc_rope** out) {
       const double turns = (double)d->original_context * f0 / pi2;
       keep = (turns - d->low_freq_factor) / (d->high_freq_factor - d->low_freq_factor);
     } else if (d->scaling == HC_ROPE_YARN) {
-      keep = 1.0 - (i - lo) / fmax(hi - lo, 0.001);
+      auto pair_of = [&](double turns) {
+        return n * log((double)d->original_context / (turns * pi2)) / log(d->base);
+      };
+      const double lo = fmax(floor(pair_of(d->beta_fast)), 0.0);
+      const double hi = fmin(ceil(pair_of(d->beta_slow)), (double)(2 * n - 1));
+      keep = 1.0 - (j - lo) / fmax(hi - lo, 0.001);
     }
     keep = fmin(fmax(keep, 0.0), 1.0);
     const double f = d->scaling == HC_ROPE_NONE ? f0 : f0 * keep + f0 / d->factor * (1.0 - keep);
@@ -166,7 +181,10 @@ int hc_rope_create(const hc_rope_desc* d, hc_rope** out) {
     turn -= floorl(turn);
     const long double scaled = turn * 18446744073709551616.0L;
     r->table.turns[i] = scaled >= 18446744073709551615.0L ? 0 : (uint64_t)(scaled + 0.5L);
+    r->table.axis[i] = (uint8_t)axis;
   }
+  r->table.axes = axes;
+  r->table.magnitude64 = r->magnitude;
   r->table.magnitude = (float)r->magnitude;
   r->table.rot_dim = d->rot_dim;
   r->table.rot_offset = d->rot_offset;
@@ -187,9 +205,11 @@ int hc_rope_frequencies(const hc_rope* r, double* f, double* magnitude) {
   return HC_OK;
 }
 
-int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
-  if (!pool || !d) return set_error(HC_ERR_INVALID, "null argument");
-  TraceRange range("hc_store_tokens");
+}  // extern "C"
+
+namespace {
+
+int store_tokens(hc_pool* pool, const hc_store_desc* d, bool mxfp4, void* stream) {
   PoolView v;
   hc::pool_view(pool, &v);
   HC_TRY(check_layer(v, d->layer, d->dtype));
@@ -198,11 +218,13 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
     return set_error(HC_ERR_INVALID, "bad head counts or sizes");
   if (d->head_dim % 8 != 0 || d->value_dim % 8 != 0)
     return set_error(HC_ERR_UNSUPPORTED, "head_dim and value_dim must be multiples of 8");
+  if (mxfp4 && (d->head_dim % hc::kMxBlock != 0 || d->value_dim % hc::kMxBlock != 0))
+    return set_error(HC_ERR_UNSUPPORTED, "head_dim and value_dim must be multiples of %d in 4 bits", hc::kMxBlock);
   if ((int64_t)d->q_heads * d->head_dim > (1 << 20))
     return set_error(HC_ERR_UNSUPPORTED, "q_heads * head_dim above 2^20");
   if (d->q_heads == 0 && (d->q || d->q_out)) return set_error(HC_ERR_INVALID, "queries given with q_heads 0");
-  HC_TRY(check_rows(v, 0, (int64_t)d->kv_heads * d->head_dim, "key"));
-  if (d->value_dim > 0) HC_TRY(check_rows(v, 1, (int64_t)d->kv_heads * d->value_dim, "value"));
+  HC_TRY(check_rows(v, 0, (int64_t)d->kv_heads * d->head_dim, mxfp4, "key"));
+  if (d->value_dim > 0) HC_TRY(check_rows(v, 1, (int64_t)d->kv_heads * d->value_dim, mxfp4, "value"));
   if (d->value_dim == 0 && d->v) return set_error(HC_ERR_INVALID, "values given with value_dim 0");
   if (d->rope && d->rope->table.rot_offset + d->rope->table.rot_dim > d->head_dim)
     return set_error(HC_ERR_INVALID, "the rotated elements [%d, %d) are not inside a head of %d",
@@ -211,7 +233,8 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
   hc::BufferCheck check(v.device);
   if (d->n == 0) return HC_OK;
   HC_TRY(check_list(d->slots, d->n, check, "slots"));
-  if (d->rope) HC_TRY(check_list(d->positions, d->n, check, "positions"));
+  const int64_t placed = d->rope ? d->n * d->rope->table.axes : 0;
+  if (d->rope) HC_TRY(check_list(d->positions, placed, check, "positions"));
   HC_TRY(check_tensor(d->k, d->k_stride, d->n, d->kv_heads, d->head_dim, false, check, "k"));
   if (d->value_dim > 0)
     HC_TRY(check_tensor(d->v, d->v_stride, d->n, d->kv_heads, d->value_dim, false, check, "v"));
@@ -227,7 +250,7 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
   const hc::Tensor k = {d->k, {d->k_stride[0], d->k_stride[1]}, d->n, d->kv_heads, d->head_dim};
   const hc::Tensor v_in = {d->v, {d->v_stride[0], d->v_stride[1]}, d->n, d->value_dim > 0 ? d->kv_heads : 0,
                            d->value_dim};
-  const Span slots = {d->slots, 8 * d->n}, positions = {d->positions, d->rope ? 8 * d->n : 0};
+  const Span slots = {d->slots, 8 * d->n}, positions = {d->positions, 8 * placed};
   if ((q_out.at != q.at && share(q_out, q)) || share(q_out, k) || share(q_out, v_in) ||
       overlap(span_of(q_out), slots) || overlap(span_of(q_out), positions))
     return set_error(HC_ERR_INVALID, "q_out overlaps what is read");
@@ -259,7 +282,67 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
   a.kv_heads = d->kv_heads;
   a.head_dim = d->head_dim;
   a.value_dim = d->value_dim;
-  return launched(hc::launch_store(a, d->dtype, v.num_cus, (hipStream_t)stream), "store");
+  return launched(hc::launch_store(a, d->dtype, mxfp4, v.num_cus, (hipStream_t)stream), "store");
+}
+
+}  // namespace
+
+extern "C" {
+
+int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
+  if (!pool || !d) return set_error(HC_ERR_INVALID, "null argument");
+  TraceRange range("hc_store_tokens");
+  return store_tokens(pool, d, false, stream);
+}
+
+int hc_mxfp4_row_bytes(int32_t heads, int32_t dim, int64_t* out_bytes) {
+  if (!out_bytes) return set_error(HC_ERR_INVALID, "null argument");
+  if (heads <= 0 || dim <= 0) return set_error(HC_ERR_INVALID, "bad head count or size");
+  if (dim % hc::kMxBlock != 0) return set_error(HC_ERR_UNSUPPORTED, "dim must be a multiple of %d", hc::kMxBlock);
+  *out_bytes = hc::mxfp4_row((int64_t)heads * dim);
+  return HC_OK;
+}
+
+int hc_store_tokens_mxfp4(hc_pool* pool, const hc_store_desc* d, void* stream) {
+  if (!pool || !d) return set_error(HC_ERR_INVALID, "null argument");
+  TraceRange range("hc_store_tokens_mxfp4");
+  return store_tokens(pool, d, true, stream);
+}
+
+int hc_fetch_tokens_mxfp4(hc_pool* pool, const hc_fetch_desc* d, void* stream) {
+  if (!pool || !d) return set_error(HC_ERR_INVALID, "null argument");
+  TraceRange range("hc_fetch_tokens_mxfp4");
+  PoolView v;
+  hc::pool_view(pool, &v);
+  HC_TRY(check_layer(v, d->layer, d->dtype));
+  if (d->n < 0 || d->n >= kMaxRows) return set_error(HC_ERR_INVALID, "n must be in [0, 2^31)");
+  if (d->kv_heads <= 0 || d->head_dim <= 0 || d->value_dim < 0)
+    return set_error(HC_ERR_INVALID, "bad head counts or sizes");
+  if (d->head_dim % hc::kMxBlock != 0 || d->value_dim % hc::kMxBlock != 0)
+    return set_error(HC_ERR_UNSUPPORTED, "head_dim and value_dim must be multiples of %d in 4 bits", hc::kMxBlock);
+  HC_TRY(check_rows(v, 0, (int64_t)d->kv_heads * d->head_dim, true, "key"));
+  if (d->value_dim > 0) HC_TRY(check_rows(v, 1, (int64_t)d->kv_heads * d->value_dim, true, "value"));
+  if (d->value_dim == 0 && d->v) return set_error(HC_ERR_INVALID, "values asked for with value_dim 0");
+  HC_TRY(hc::pool_forward(pool, stream, &v));
+  hc::BufferCheck check(v.device);
+  if (d->n == 0) return HC_OK;
+  HC_TRY(check_list(d->slots, d->n, check, "slots"));
+  HC_TRY(check_tensor(d->k, d->k_stride, d->n, d->kv_heads, d->head_dim, true, check, "k"));
+  if (d->value_dim > 0)
+    HC_TRY(check_tensor(d->v, d->v_stride, d->n, d->kv_heads, d->value_dim, true, check, "v"));
+  const hc::Tensor k = {d->k, {d->k_stride[0], d->k_stride[1]}, d->n, d->kv_heads, d->head_dim};
+  const hc::Tensor v_out = {d->v, {d->v_stride[0], d->v_stride[1]}, d->n, d->value_dim > 0 ? d->kv_heads : 0,
+                            d->value_dim};
+  bool shared = share(k, v_out);
+  for (const Span& x : {span_of(k), span_of(v_out)}) {
+    shared |= overlap(x, {d->slots, 8 * d->n});
+    for (int b = 0; b < (d->value_dim > 0 ? 2 : 1); b++) shared |= overlap(x, layer_span(v, b, d->layer));
+  }
+  if (shared) return set_error(HC_ERR_INVALID, "k and v must not overlap each other or what is read");
+  hc::FetchArgs a = {d->slots, layer_rows(v, 0, d->layer), d->value_dim > 0 ? layer_rows(v, 1, d->layer) : nullptr,
+                     (uint8_t*)d->k, (uint8_t*)d->v, v.wrong, d->n, v.geom->S, {d->k_stride[0], d->k_stride[1]},
+                     {d->v_stride[0], d->v_stride[1]}, d->kv_heads, d->head_dim, d->value_dim};
+  return launched(hc::launch_fetch_mxfp4(a, d->dtype, v.num_cus, (hipStream_t)stream), "fetch");
 }
 
 }  // extern "C"
@@ -267,7 +350,7 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* d, void* stream) {
 namespace {
 
 // The checks of sizes, and the kernel arguments that follow from them.
-int attend_sizes(const PoolView& v, const hc_attend_desc* d, hc::AttendArgs* a) {
+int attend_sizes(const PoolView& v, const hc_attend_desc* d, bool mxfp4, hc::AttendArgs* a) {
   HC_TRY(check_layer(v, d->layer, d->dtype));
   if (d->kv_heads <= 0 || d->q_heads <= 0 || d->q_heads % d->kv_heads != 0)
     return set_error(HC_ERR_INVALID, "q_heads %d is not a multiple of kv_heads %d", d->q_heads, d->kv_heads);
@@ -280,8 +363,8 @@ int attend_sizes(const PoolView& v, const hc_attend_desc* d, hc::AttendArgs* a) 
                      "head_dim / value_dim %d / %d with %d KV heads: 64 / 64, 128 / 128, or 576 / 512 with "
                      "value_in_key and one KV head",
                      d->head_dim, d->value_dim, d->kv_heads);
-  HC_TRY(check_rows(v, 0, (int64_t)d->kv_heads * d->head_dim, "key"));
-  if (!latent) HC_TRY(check_rows(v, 1, (int64_t)d->kv_heads * d->value_dim, "value"));
+  HC_TRY(check_rows(v, 0, (int64_t)d->kv_heads * d->head_dim, mxfp4, "key"));
+  if (!latent) HC_TRY(check_rows(v, 1, (int64_t)d->kv_heads * d->value_dim, mxfp4, "value"));
   if (d->entry_tokens != 1 && d->entry_tokens != v.geom->P)
     return set_error(HC_ERR_INVALID, "entry_tokens must be 1 or the pool's page_size %d", v.geom->P);
   if (!isfinite(d->scale)) return set_error(HC_ERR_INVALID, "scale must be finite");
@@ -304,6 +387,10 @@ int attend_sizes(const PoolView& v, const hc_attend_desc* d, hc::AttendArgs* a) 
   a->table_stride = d->table_stride;
   a->k_row = (int64_t)d->kv_heads * d->head_dim;
   a->v_row = latent ? a->k_row : (int64_t)d->kv_heads * d->value_dim;
+  if (mxfp4) {
+    a->k_row = v.geom->sub[0].elem;
+    a->v_row = v.geom->sub[latent ? 0 : 1].elem;
+  }
   a->num_seqs = d->num_seqs;
   a->q_rows = d->q_rows;
   a->max_q = d->max_q < d->q_rows ? d->max_q : d->q_rows;
@@ -326,27 +413,21 @@ int attend_sizes(const PoolView& v, const hc_attend_desc* d, hc::AttendArgs* a) 
   return HC_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int hc_attend_workspace_bytes(const hc_pool* pool, const hc_attend_desc* d, int64_t* out_bytes) {
+int attend_workspace_bytes(const hc_pool* pool, const hc_attend_desc* d, bool mxfp4, int64_t* out_bytes) {
   if (!pool || !d || !out_bytes) return set_error(HC_ERR_INVALID, "null argument");
   PoolView v;
   hc::pool_view(pool, &v);
   hc::AttendArgs a;
-  HC_TRY(attend_sizes(v, d, &a));
-  *out_bytes = hc::attend_workspace(a, d->head_dim, v.num_cus);
+  HC_TRY(attend_sizes(v, d, mxfp4, &a));
+  *out_bytes = (mxfp4 ? hc::attend_mxfp4_workspace : hc::attend_workspace)(a, d->head_dim, v.num_cus);
   return HC_OK;
 }
 
-int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
-  if (!pool || !d) return set_error(HC_ERR_INVALID, "null argument");
-  TraceRange range("hc_attend");
+int attend(hc_pool* pool, const hc_attend_desc* d, bool mxfp4, void* stream) {
   PoolView v;
   hc::pool_view(pool, &v);
   hc::AttendArgs a;
-  HC_TRY(attend_sizes(v, d, &a));
+  HC_TRY(attend_sizes(v, d, mxfp4, &a));
   HC_TRY(hc::pool_forward(pool, stream, &v));
   hc::BufferCheck check(v.device);
   if (d->q_rows == 0 || d->num_seqs == 0) return HC_OK;
@@ -358,7 +439,7 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
   if (d->q_start) HC_TRY(check_list(d->q_start, d->num_seqs + 1, check, "q_start"));
   HC_TRY(check_list(d->kv_len, d->num_seqs, check, "kv_len"));
   HC_TRY(check_extent(d->table, hc::table_bytes(d->num_seqs, d->table_width, d->table_stride), 8, true, check, "table"));
-  const int64_t work = hc::attend_workspace(a, d->head_dim, v.num_cus);
+  const int64_t work = (mxfp4 ? hc::attend_mxfp4_workspace : hc::attend_workspace)(a, d->head_dim, v.num_cus);
   if (work > 0) {
     if (d->workspace_bytes < work)
       return set_error(HC_ERR_INVALID, "workspace_bytes %lld below the %lld that are needed",
@@ -393,7 +474,33 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
   a.v_rows = layer_rows(v, d->value_in_key ? 0 : 1, d->layer);
   a.wrong = v.wrong;
   a.work = (float*)d->workspace;
-  return launched(hc::launch_attend(a, d->dtype, d->head_dim, v.num_cus, (hipStream_t)stream), "attention");
+  return launched((mxfp4 ? hc::launch_attend_mxfp4 : hc::launch_attend)(a, d->dtype, d->head_dim, v.num_cus,
+                                                                       (hipStream_t)stream),
+                  "attention");
+}
+
+}  // namespace
+
+extern "C" {
+
+int hc_attend_workspace_bytes(const hc_pool* pool, const hc_attend_desc* d, int64_t* out_bytes) {
+  return attend_workspace_bytes(pool, d, false, out_bytes);
+}
+
+int hc_attend(hc_pool* pool, const hc_attend_desc* d, void* stream) {
+  if (!pool || !d) return set_error(HC_ERR_INVALID, "null argument");
+  TraceRange range("hc_attend");
+  return attend(pool, d, false, stream);
+}
+
+int hc_attend_mxfp4_workspace_bytes(const hc_pool* pool, const hc_attend_desc* d, int64_t* out_bytes) {
+  return attend_workspace_bytes(pool, d, true, out_bytes);
+}
+
+int hc_attend_mxfp4(hc_pool* pool, const hc_attend_desc* d, void* stream) {
+  if (!pool || !d) return set_error(HC_ERR_INVALID, "null argument");
+  TraceRange range("hc_attend_mxfp4");
+  return attend(pool, d, true, stream);
 }
 
 }  // extern "C"
@@ -436,6 +543,45 @@ int check_work(const PoolView& v, const void* work, int64_t bytes, hc::BufferChe
 }  // namespace
 
 extern "C" {
+
+int hc_extend_pages(hc_pool* pool, const hc_extend_desc* d, void* stream) {
+  if (!pool || !d) return set_error(HC_ERR_INVALID, "null argument");
+  TraceRange range("hc_extend_pages");
+  PoolView v;
+  hc::pool_view(pool, &v);
+  HC_TRY(page_pool(v));
+  HC_TRY(table_sizes(d->table_rows, d->table_width, d->table_stride));
+  if (d->n_free < 0 || d->n_free >= kMaxRows) return set_error(HC_ERR_INVALID, "n_free must be in [0, 2^31)");
+  if (d->room < 0 || d->room >= kMaxRows) return set_error(HC_ERR_INVALID, "room must be in [0, 2^31)");
+  HC_TRY(hc::pool_forward(pool, stream, &v));
+  hc::BufferCheck check(v.device);
+  const int64_t n = d->table_rows;
+  const int64_t bytes = hc::table_bytes(n, d->table_width, d->table_stride);
+  HC_TRY(check_extent(d->table, bytes, 8, false, check, "table"));
+  HC_TRY(check_list(d->lens, n, check, "lens"));
+  HC_TRY(check_list(d->added, n, check, "added"));
+  HC_TRY(check_list(d->free_pages, d->n_free, check, "free_pages"));
+  if (d->first_free) HC_TRY(check_list(d->first_free, 1, check, "first_free"));
+  HC_TRY(check_out_list(d->kv_len, n, check, "kv_len"));
+  HC_TRY(check_out_list(d->q_start, n + 1, check, "q_start"));
+  HC_TRY(check_out_list(d->slots, d->room, check, "slots"));
+  HC_TRY(check_out_list(d->positions, d->room, check, "positions"));
+  HC_TRY(check_out_list(d->used, 1, check, "used"));
+  const Span writes[] = {{d->table, bytes}, {d->kv_len, 8 * n}, {d->q_start, 8 * (n + 1)}, {d->slots, 8 * d->room},
+                         {d->positions, 8 * d->room}, {d->used, 8}};
+  const Span reads[] = {{d->lens, 8 * n}, {d->added, 8 * n}, {d->free_pages, 8 * d->n_free},
+                        {d->first_free, d->first_free ? 8 : 0}};
+  bool shared = false;
+  for (int w = 0; w < 6; w++) {
+    for (const Span& r : reads) shared |= overlap(writes[w], r);
+    for (int o = 0; o < w; o++) shared |= overlap(writes[w], writes[o]);
+  }
+  if (shared) return set_error(HC_ERR_INVALID, "what is written must not overlap anything else");
+  const hc::ExtendArgs a = {{d->table, d->lens, n, d->table_width, d->table_stride}, d->added, d->free_pages,
+                            d->first_free, d->n_free, v.geom->S / v.geom->P, d->kv_len, d->q_start, d->slots,
+                            d->positions, d->used, d->room, v.wrong, v.geom->P};
+  return launched(hc::launch_extend_pages(a, (hipStream_t)stream), "extension");
+}
 
 int hc_copy_pages(hc_pool* pool, const int64_t* src, const int64_t* dst, int64_t n, void* stream) {
   if (!pool) return set_error(HC_ERR_INVALID, "pool is null");

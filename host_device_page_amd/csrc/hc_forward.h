@@ -20,6 +20,9 @@ struct RopeTable {
   uint64_t turns[HC_MAX_ROT_DIM / 2];
   float magnitude;
   int32_t rot_dim, rot_offset, interleaved;  // rot_dim 0: nothing is rotated
+  double magnitude64;
+  int32_t axes;                              // of positions: `axis` is read where there are several
+  uint8_t axis[HC_MAX_ROT_DIM / 2];          // whose position a pair takes
 };
 
 struct StoreArgs {
@@ -34,7 +37,18 @@ struct StoreArgs {
   int64_t q_stride[2], q_out_stride[2], k_stride[2], v_stride[2];  // elements
   int32_t q_heads, kv_heads, head_dim, value_dim;
 };
-hipError_t launch_store(const StoreArgs& a, int32_t dtype, int32_t num_cus, hipStream_t stream);
+hipError_t launch_store(const StoreArgs& a, int32_t dtype, bool mxfp4, int32_t num_cus, hipStream_t stream);
+
+struct FetchArgs {
+  const int64_t* slots;
+  const uint8_t *k_rows, *v_rows;  // the layer's sub-buffers
+  uint8_t *k, *v;
+  WrongWord* wrong;
+  int64_t n, S;
+  int64_t k_stride[2], v_stride[2];  // elements
+  int32_t kv_heads, head_dim, value_dim;
+};
+hipError_t launch_fetch_mxfp4(const FetchArgs& a, int32_t dtype, int32_t num_cus, hipStream_t stream);
 
 struct AttendArgs {
   const uint8_t* q;
@@ -55,6 +69,10 @@ struct AttendArgs {
   int32_t join_parts;                  // workgroups of the joining launch to a row tile
   float scale;
 };
+// The same over rows in 4 bits: k_row and v_row are bytes.
+hipError_t launch_attend_mxfp4(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t num_cus,
+                               hipStream_t stream);
+int64_t attend_mxfp4_workspace(const AttendArgs& a, int32_t head_dim, int32_t num_cus);
 // Bytes of workspace that launch_attend needs for these sizes.
 int64_t attend_workspace(const AttendArgs& a, int32_t head_dim, int32_t num_cus);
 hipError_t launch_attend(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t num_cus, hipStream_t stream);
@@ -73,6 +91,16 @@ struct ForkArgs {
   int64_t out_stride;
   int64_t* used;
 };
+struct ExtendArgs {
+  PageTable table;   // entries are written too
+  const int64_t *added, *free_pages, *first_free;
+  int64_t n_free, pages;
+  int64_t *kv_len, *q_start, *slots, *positions, *used;
+  int64_t room;
+  WrongWord* wrong;
+  int32_t P;
+};
+hipError_t launch_extend_pages(const ExtendArgs& a, hipStream_t stream);
 hipError_t launch_copy_pages(const Geom& g, const int64_t* src, const int64_t* dst, int64_t n, WrongWord* wrong,
                              int32_t num_cus, hipStream_t stream);
 hipError_t launch_fork_pages(const Geom& g, const ForkArgs& a, WrongWord* wrong, int32_t num_cus, hipStream_t stream);

@@ -13,12 +13,21 @@
 // pairs (half layout) or the one that holds four (interleaved) and writes the same places,
 // which is why queries may be rotated in place.
 //
+// Pairs of a rope of several axes take the position of their axis; everything else is the same, so that
+// the axis is looked up in kernels of their own (AXES) only.
+//
+// A cache held in 4 bits (MX): a lane takes 16 bytes of keys or values, four lanes a block of 32
+// elements and its scale, whose bits come from the largest magnitude's without a logarithm.  Rotated
+// keys are computed in 64 bits and reach the 4-bit rounding unrounded: in fp32 one of a million would be
+// on the wrong side of a border, half of its value off.
+//
 // Measured: 8192 tokens of 32 + 8 + 8 heads of 128, 201 MB, 45 us = 4.4 TB/s; 2048 tokens of a latent cache 19 us =
 // 4.3 TB/s; 32 tokens 3.9 us, their heads over several workgroups each.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "hc_forward.h"
+#include "hc_mxfp4.h"
 
 namespace hc {
 namespace {
@@ -40,9 +49,54 @@ __device__ __forceinline__ v4u narrow(f32x8 x) {  // rounds to nearest, the one 
   return __builtin_bit_cast(v4u, __builtin_convertvector(x, V8));
 }
 
+// A lane's eight elements of a head of keys (rotated: r is the vector's place in the rotated ones) or
+// values into a row of 4 bits; `pair` sines and cosines of the token.
 template <class V8>
+__device__ __forceinline__ void store_mxfp4(const StoreArgs& a, const v4u* src, uint8_t* row, int heads_before, int dim,
+                                            int x, int r, int rv, const double* s_cos, const double* s_sin) {
+  const f32x8 u = widen<V8>(src[x]);
+  float f[8];
+  if (r < 0 || r >= rv) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] = u[j];
+  } else if (a.rope.interleaved) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const double c = s_cos[r * 4 + j], s = s_sin[r * 4 + j];
+      f[2 * j] = mx_to_odd((double)u[2 * j] * c - (double)u[2 * j + 1] * s);
+      f[2 * j + 1] = mx_to_odd((double)u[2 * j + 1] * c + (double)u[2 * j] * s);
+    }
+  } else {  // the pair's other element is half a rotation away
+    const bool first = r < rv / 2;
+    const int p = first ? r : r - rv / 2;
+    const f32x8 w = widen<V8>(src[first ? x + rv / 2 : x - rv / 2]);
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const double c = s_cos[p * 8 + j], s = s_sin[p * 8 + j];
+      f[j] = mx_to_odd((double)u[j] * c + (double)w[j] * (first ? -s : s));
+    }
+  }
+  uint32_t top = 0;  // largest magnitude, as bits: NaN above infinity above all others
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    const uint32_t y = __float_as_uint(f[j]) & 0x7fffffffu;
+    top = y > top ? y : top;
+  }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    const uint32_t y = __shfl_xor(top, d);
+    top = y > top ? y : top;
+  }
+  const uint32_t byte = mx_scale_byte(top);
+  const int64_t at = (int64_t)heads_before * dim + x * 8;
+  *reinterpret_cast<uint32_t*>(row + at / 2) = byte == 255 ? 0 : mx_encode(f, mx_scale(byte));
+  if ((x & 3) == 0) row[mxfp4_codes((int64_t)a.kv_heads * dim) + at / kMxBlock] = (uint8_t)byte;
+}
+
+template <class V8, bool AXES, bool MX>
 __global__ __launch_bounds__(kThreads) void k_store_tokens(StoreArgs a, int32_t tokens, int32_t splits) {
   __shared__ float s_cos[kTokens][HC_MAX_ROT_DIM / 2], s_sin[kTokens][HC_MAX_ROT_DIM / 2];
+  __shared__ double s_cos64[MX ? kTokens : 1][HC_MAX_ROT_DIM / 2], s_sin64[MX ? kTokens : 1][HC_MAX_ROT_DIM / 2];
   __shared__ int64_t s_slot[kTokens];
   const int64_t t0 = (int64_t)(blockIdx.x / splits) * tokens;
   const int split = blockIdx.x % splits;
@@ -56,19 +110,31 @@ __global__ __launch_bounds__(kThreads) void k_store_tokens(StoreArgs a, int32_t 
   }
   for (int i = threadIdx.x; i < count * pairs; i += kThreads) {
     const int t = i / pairs, p = i - t * pairs;
-    const uint64_t turn = (uint64_t)a.positions[t0 + t] * a.rope.turns[p];
-    const float half = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // angle / pi, in [-1, 1)
-    float s, c;
-    sincospif(half, &s, &c);
-    s_cos[t][p] = c * a.rope.magnitude;
-    s_sin[t][p] = s * a.rope.magnitude;
+    const int64_t position = a.positions[AXES ? a.rope.axis[p] * a.n + t0 + t : t0 + t];
+    const uint64_t turn = (uint64_t)position * a.rope.turns[p];
+    if constexpr (MX) {
+      double s, c;
+      sincospi((double)(int64_t)turn * 0x1p-63, &s, &c);
+      s_cos64[t][p] = c * a.rope.magnitude64;
+      s_sin64[t][p] = s * a.rope.magnitude64;
+      s_cos[t][p] = (float)s_cos64[t][p];
+      s_sin[t][p] = (float)s_sin64[t][p];
+    } else {
+      const float half = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // angle / pi, in [-1, 1)
+      float s, c;
+      sincospif(half, &s, &c);
+      s_cos[t][p] = c * a.rope.magnitude;
+      s_sin[t][p] = s * a.rope.magnitude;
+    }
   }
   __syncthreads();
   // The heads of queries, keys and values in one row of work, cut evenly over the splits.
   const int d_vecs = a.head_dim / 8, v_vecs = a.value_dim / 8;
   const int q_work = a.q_heads * d_vecs, k_work = a.kv_heads * d_vecs, v_work = a.kv_heads * v_vecs;
   const int all = q_work + k_work + v_work;
-  const int w0 = (int)((int64_t)all * split / splits), w1 = (int)((int64_t)all * (split + 1) / splits);
+  // (MX: in whole blocks of four vectors, whose lanes work together)
+  constexpr int U = MX ? 4 : 1;
+  const int w0 = (int)((int64_t)(all / U) * split / splits) * U, w1 = (int)((int64_t)(all / U) * (split + 1) / splits) * U;
   const int r0 = a.rope.rot_offset / 8, rv = a.rope.rot_dim / 8;
   for (int i = threadIdx.x; i < count * (w1 - w0); i += kThreads) {
     const int t = i / (w1 - w0);
@@ -81,6 +147,15 @@ __global__ __launch_bounds__(kThreads) void k_store_tokens(StoreArgs a, int32_t 
     const int h = w / vecs, x = w - h * vecs;
     const int64_t* in = is_q ? a.q_stride : (is_v ? a.v_stride : a.k_stride);
     const uint8_t* from = (is_q ? a.q : (is_v ? a.v : a.k)) + 2 * ((t0 + t) * in[0] + h * in[1]);
+    if constexpr (MX) {
+      if (!is_q) {
+        const int dim = is_v ? a.value_dim : a.head_dim;
+        uint8_t* row = (is_v ? a.v_rows : a.k_rows) + slot * mxfp4_row((int64_t)a.kv_heads * dim);
+        store_mxfp4<V8>(a, reinterpret_cast<const v4u*>(from), row, h, dim, x, is_v ? -1 : x - r0, rv, s_cos64[t],
+                        s_sin64[t]);
+        continue;
+      }
+    }
     uint8_t* to = is_q ? a.q_out + 2 * ((t0 + t) * a.q_out_stride[0] + h * a.q_out_stride[1])
                        : (is_v ? a.v_rows + 2 * ((slot * a.kv_heads + h) * (int64_t)a.value_dim)
                                : a.k_rows + 2 * ((slot * a.kv_heads + h) * (int64_t)a.head_dim));
@@ -114,9 +189,41 @@ __global__ __launch_bounds__(kThreads) void k_store_tokens(StoreArgs a, int32_t 
   }
 }
 
+// Eight elements a lane: 4 bytes of codes in, 16 bytes out, neighbours next to each other on both sides.  Written bytes
+// bound it, four times those that are read.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void k_fetch_mxfp4(FetchArgs a) {
+  const int d_vecs = a.kv_heads * (a.head_dim / 8), all = d_vecs + a.kv_heads * (a.value_dim / 8);
+  const int64_t total = a.n * all;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t t = i / all;
+    int w = (int)(i - t * all);
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.S) {
+      if (w == 0 && slot != -1) report_wrong<DeviceAtomic>(a.wrong, kWrongIndex, t);
+      continue;
+    }
+    const bool is_v = w >= d_vecs;
+    w -= is_v ? d_vecs : 0;
+    const int dim = is_v ? a.value_dim : a.head_dim, h = w / (dim / 8), x = w - h * (dim / 8);
+    const int64_t elems = (int64_t)a.kv_heads * dim;
+    const uint8_t* row = (is_v ? a.v_rows : a.k_rows) + slot * mxfp4_row(elems);
+    const uint32_t codes = reinterpret_cast<const uint32_t*>(row)[w];
+    const float scale = mx_scale(row[mxfp4_codes(elems) + w / 4]);
+    const int64_t* to = is_v ? a.v_stride : a.k_stride;
+    reinterpret_cast<v4u*>((is_v ? a.v : a.k) + 2 * (t * to[0] + h * to[1]))[x] = mx_decode<BF16>(codes, scale);
+  }
+}
+
+template <class V8>
+void (*store_kernel(bool axes, bool mxfp4))(StoreArgs, int32_t, int32_t) {
+  if (mxfp4) return axes ? k_store_tokens<V8, true, true> : k_store_tokens<V8, false, true>;
+  return axes ? k_store_tokens<V8, true, false> : k_store_tokens<V8, false, false>;
+}
+
 }  // namespace
 
-hipError_t launch_store(const StoreArgs& a, int32_t dtype, int32_t num_cus, hipStream_t stream) {
+hipError_t launch_store(const StoreArgs& a, int32_t dtype, bool mxfp4, int32_t num_cus, hipStream_t stream) {
   if (a.n <= 0) return hipSuccess;
   // Few tokens: one a workgroup, and its heads over up to 8 workgroups.  Of 32 + 8 + 8 heads of 128, in a graph: one
   // token with its heads over 1, 8 and 16 workgroups 4.25, 3.23 and 3.18 us, 32 tokens 4.50, 3.32 and 3.52; four
@@ -128,8 +235,19 @@ hipError_t launch_store(const StoreArgs& a, int32_t dtype, int32_t num_cus, hipS
   while (splits < 8 && groups * splits * 2 <= fill) splits *= 2;
   if (groups * splits > 0x7fffffff) return hipErrorInvalidValue;
   (void)hipGetLastError();
-  auto kernel = dtype == HC_BF16 ? k_store_tokens<bf16x8> : k_store_tokens<f16x8>;
+  const bool axes = a.rope.rot_dim > 0 && a.rope.axes > 1;
+  auto kernel = dtype == HC_BF16 ? store_kernel<bf16x8>(axes, mxfp4) : store_kernel<f16x8>(axes, mxfp4);
   kernel<<<dim3((unsigned)(groups * splits)), kThreads, 0, stream>>>(a, tokens, splits);
+  return hipGetLastError();
+}
+
+hipError_t launch_fetch_mxfp4(const FetchArgs& a, int32_t dtype, int32_t num_cus, hipStream_t stream) {
+  if (a.n <= 0) return hipSuccess;
+  const int64_t lanes = a.n * a.kv_heads * ((a.head_dim + a.value_dim) / 8);
+  const int64_t most = (int64_t)num_cus * 32, groups = (lanes + kThreads - 1) / kThreads;
+  (void)hipGetLastError();
+  auto kernel = dtype == HC_BF16 ? k_fetch_mxfp4<true> : k_fetch_mxfp4<false>;
+  kernel<<<dim3((unsigned)(groups < most ? groups : most)), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -19,8 +19,9 @@
  *     staging buffer, the other TP ranks unpack the broadcast bytes into the
  *     same slots (device memory only; the broadcast is the caller's);
  *   the forward pass on the device pool (no page's; what runs between two
- *     transfers): new tokens rotated and stored in their slots, attention of new
- *     tokens over the cached ones, and page tables forked, packed and listed.
+ *     transfers): new tokens rotated and stored in their slots, in 16 or in 4 bits,
+ *     attention of new tokens over the cached ones, and page tables grown, forked,
+ *     packed and listed.
  *
  * Host layouts:
  *   HC_LAYOUT_PAGE_FIRST      per sub-buffer [page][layer][row][elem_bytes]
@@ -443,6 +444,17 @@ typedef struct hc_rope_desc {
 typedef struct hc_rope hc_rope;
 int hc_rope_create(const hc_rope_desc* desc, hc_rope** out);
 int hc_rope_destroy(hc_rope* rope); /* NULL is a no-op */
+/* A rope whose pairs take the positions of several axes (time, height and width of a picture or
+ * clip, say): pair i turns by positions[pair_axes[i]] * f_i.
+ *   pair_axes   rot_dim / 2 values in [0, axes), host memory; every axis has a pair
+ *   axes        1 to HC_MAX_ROPE_AXES.  A call that is given the rope reads axes * n positions, axis 0's
+ *               n first.
+ *   own_series  0: f_i as above, whichever axis a pair takes.  Otherwise every axis has a series of its
+ *               own: its j-th pair of m has base^(-j / m) before scaling, which then treats the axis
+ *               like a rotation of 2 m elements. */
+#define HC_MAX_ROPE_AXES 8
+int hc_rope_create_axes(const hc_rope_desc* desc, const int32_t* pair_axes, int32_t axes, int32_t own_series,
+                        hc_rope** out);
 /* The scaled frequencies, radians per position of each pair (rot_dim / 2 values), and
  * the factor on sines and cosines.  Host only. */
 int hc_rope_frequencies(const hc_rope* rope, double* out_frequencies, double* out_magnitude);
@@ -455,7 +467,7 @@ int hc_rope_frequencies(const hc_rope* rope, double* out_frequencies, double* ou
  *   slots      n int64, distinct; -1 marks a padding token: its rows and its q_out are
  *              left as they were and nothing is reported.  Any other slot outside the
  *              pool is skipped the same way and reported.
- *   positions  n int64, any value.
+ *   positions  n int64, any value; of a rope of several axes n for each, axis by axis.
  *   q, q_out   queries of q_heads heads, or both NULL (q_heads 0).  q_out may be q itself
  *              with the same strides (in place); otherwise inputs and outputs must not
  *              overlap, nor any of them the layer's rows.
@@ -480,6 +492,42 @@ typedef struct hc_store_desc {
   const hc_rope* rope;
 } hc_store_desc;
 int hc_store_tokens(hc_pool* pool, const hc_store_desc* desc, void* stream);
+
+/* A cache held in 4 bits.  A row of h heads of d elements (d a multiple of 32) is
+ *   h * d / 2 bytes of codes, element e of the row (head e / d) in byte e / 2, the lower half of it where
+ *     e is even: a sign (8) and 0 to 7 for 0, 0.5, 1, 1.5, 2, 3, 4 and 6;
+ *   h * d / 32 bytes of scales, byte b of elements 32 b to 32 b + 31, which are their codes' values times
+ *     2^(byte - 127); 255: they are NaN;
+ *   and bytes up to a multiple of 16 that are neither read nor written
+ * (the OCP microscaling format MXFP4), 4.25 bits an element.  Rows move in transfers and page calls like any
+ * other.  hc_mxfp4_row_bytes gives a row's size, the elem_bytes of the pool's sub-buffer. */
+int hc_mxfp4_row_bytes(int32_t heads, int32_t dim, int64_t* out_bytes);
+
+/* hc_store_tokens into such rows, of keys in sub-buffer 0 and of values in sub-buffer 1; queries are rotated
+ * as there.  A block's scale is the least power of two with its largest element within 7 of it (2^-127 at
+ * least), and an element is rounded to the nearest code, halves to even, those above 6 to 6: none
+ * is off by more than half of the step that it lies in.  Rotated keys are computed in 64 bits and rounded
+ * once, so that a value next to a border is stored as the formula has it.  A block that holds a NaN or an
+ * infinity (or a rotated key beyond fp32) is NaN.  head_dim and value_dim are multiples of 32. */
+int hc_store_tokens_mxfp4(hc_pool* pool, const hc_store_desc* desc, void* stream);
+
+/* Rows of such a cache as elements: k[i] and v[i] <- the key and value rows in slots[i], rounded to dtype (rows
+ * stored from elements of that type are exact; what fp16 cannot hold is infinite).
+ *   slots   n int64; -1: the row of k and v is left as it was and nothing is reported.  Any other slot
+ *           outside the pool is skipped the same way and reported.
+ *   v       NULL with value_dim 0: only keys (a latent cache).
+ *   strides as for hc_store_tokens; rows of k, and of v, must not overlap.  Nothing of k and v overlaps slots, the
+ *           layer's rows or each other. */
+typedef struct hc_fetch_desc {
+  int32_t layer, dtype;
+  int32_t kv_heads, head_dim, value_dim;
+  int64_t n;
+  const int64_t* slots;
+  void* k;
+  void* v;
+  int64_t k_stride[2], v_stride[2];
+} hc_fetch_desc;
+int hc_fetch_tokens_mxfp4(hc_pool* pool, const hc_fetch_desc* desc, void* stream);
 
 /* Attention of a chunk of new tokens over the cached tokens of their sequences, in one
  * layer.  Sequence s has query rows q_start[s] .. q_start[s + 1] - 1 of q and kv_len[s]
@@ -544,6 +592,13 @@ typedef struct hc_attend_desc {
 int hc_attend_workspace_bytes(const hc_pool* pool, const hc_attend_desc* desc, int64_t* out_bytes);
 int hc_attend(hc_pool* pool, const hc_attend_desc* desc, void* stream);
 
+/* hc_attend over a cache held in 4 bits: the same call in every respect but the rows, whose values are taken
+ * as dtype (exact where they were stored from that type; what fp16 cannot hold is infinite).  kv_heads 1 with
+ * head_dim / value_dim 576 / 512 and value_in_key is a latent cache here too: its value is the
+ * first 512 elements of the key row. */
+int hc_attend_mxfp4_workspace_bytes(const hc_pool* pool, const hc_attend_desc* desc, int64_t* out_bytes);
+int hc_attend_mxfp4(hc_pool* pool, const hc_attend_desc* desc, void* stream);
+
 /* Page tables.  Row s of a table names the device pages (slots p * P .. p * P + P - 1 for
  * page p < device_slots / P) of a sequence of lens[s] tokens: its first
  * ceil(lens[s] / P) entries.  What stands behind them is not read.  Several rows may name
@@ -552,6 +607,42 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* desc, void* stream);
  * hc_compact_pages).  The pool's device_slots must be a multiple of P.  Tables are read
  * with a row stride of table_stride >= table_width entries.  Data moves bit for bit, in
  * every layer and every sub-buffer (page blocks included). */
+
+/* Grows sequences by their new tokens and lists where those go: row s of the table, of lens[s] tokens, gets
+ * added[s] more.  In the order of the rows:
+ *   kv_len[s]   lens[s] + added[s]
+ *   q_start[s]  the rows' new tokens before row s; q_start[table_rows] all of them
+ *   table       entries ceil(lens[s] / P) to ceil(kv_len[s] / P) - 1 of row s, in place: the next pages of
+ *               free_pages, from entry *first_free on (NULL: from the first)
+ *   slots, positions  of new token j of row s, at q_start[s] + j: its position lens[s] + j and the slot of
+ *               that in the row's pages.  Behind the last token up to `room`: -1 (padding for
+ *               hc_store_tokens) and 0.
+ *   *used       the pages taken
+ * so that a step's lists are made where its lengths are: slots and positions for hc_store_tokens, kv_len, q_start
+ * and the table for hc_attend.  Data does not move.
+ *   A row whose lens, added or their sum is out of bounds (below 0, above table_width * P, added above room) is
+ * reported and taken to add nothing, its kv_len is lens[s] then.  New tokens that pass `room` are reported at
+ * their row and have no slot; the pages that they begin are counted and not entered.  A page that free_pages has no
+ * entry for, or names outside the pool, is -1 in the table and in its tokens' slots, and reported at its row;
+ * tokens in an old page that is outside the pool have slot -1 and are reported so too.
+ *   room is below 2^31; slots and positions hold that many entries.  Nothing that is written overlaps anything
+ * else. */
+typedef struct hc_extend_desc {
+  int64_t* table;
+  int64_t table_rows, table_width, table_stride;
+  const int64_t* lens;
+  const int64_t* added;
+  const int64_t* free_pages;
+  int64_t n_free;
+  const int64_t* first_free;
+  int64_t* kv_len;
+  int64_t* q_start;
+  int64_t* slots;
+  int64_t* positions;
+  int64_t room;
+  int64_t* used;
+} hc_extend_desc;
+int hc_extend_pages(hc_pool* pool, const hc_extend_desc* desc, void* stream);
 
 /* Copies page src[i] to page dst[i], i < n.  The dst pages are distinct, and none of them is
  * another pair's src (src[i] == dst[i] is allowed).  A pair with a page outside the pool is
