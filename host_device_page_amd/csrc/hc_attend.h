@@ -240,6 +240,19 @@ __device__ __forceinline__ void exact_row(const AttendArgs& a, int64_t s, int64_
   *l_out = l;
 }
 
+// (kernels of many rows, and of a latent cache)
+// The maximum that a row's weights are relative to is replaced only when it grows by more than
+// 2^8: until then weights of up to 2^8 are summed, which loses nothing in fp32 or as operands, and the
+// sums need not be scaled.
+constexpr float kGrow = 8.f;
+
+// Rows of a row tile: of the kernels of few rows (decoding), of many, and of a latent cache's.
+constexpr int kRowTile = 16;
+constexpr int kTileRows = 128;
+constexpr int kLatRows = 64;
+constexpr int kLatDim = 576;
+constexpr int kLatValue = 512;
+
 // ---------------------------------------------------------------- the list of work items
 // A sequence's query rows times the heads of a KV head's group make row lists of m * group rows,
 // row r being token r / group and head r % group of the group; R rows make a row tile.  An item is
@@ -414,6 +427,127 @@ __device__ __forceinline__ Part* parts_of(const AttendArgs& a) {
   return reinterpret_cast<Part*>(a.work + a.slots * partial_floats<DV>(R));
 }
 
+
+// ---------------------------------------------------------------- splits: how many, and their join
+// Joins the splits of a row tile, a wave a row.  A workgroup looks at the item of one place; all but the first
+// split of a tile that was split have nothing to do.  HEADS: KV heads of an item, R rows each.
+template <class T, int DV, int R, int HEADS = 1>
+__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+  typedef typename T::elem elem;
+  const int64_t first = blockIdx.x / a.join_parts;
+  const Part p = parts_of<DV, R * HEADS>(a)[first];
+  // a q_start that goes back (reported) can make more items than the call has room for
+  if (p.splits <= 1 || first + p.splits > a.slots) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t tile = p.tile_hk / a.kv_heads;
+  int hk = (int)(p.tile_hk - tile * a.kv_heads);
+  int rr = (int)(blockIdx.x % a.join_parts) * 4 + wave;
+  int64_t r = tile * R + rr;
+  if (HEADS > 1) {
+    const int per = a.join_parts / HEADS, part = (int)(blockIdx.x % a.join_parts), head = part / per;
+    hk = hk * HEADS + head;
+    rr = (part - head * per) * 4 + wave;
+    r = tile * R + rr;
+    if (rr >= R) return;
+    rr += head * R;
+  }
+  if (rr >= R * HEADS || r >= p.m * a.group) return;
+  constexpr int ND = DV / 64;
+  float m = -INFINITY, l = 0.f, o[ND] = {};
+#pragma unroll 4
+  for (int k = 0; k < (int)p.splits; k++) {
+    const float* po = a.work + (first + k) * partial_floats<DV>(R * HEADS);
+    const float pm = po[R * HEADS * DV + rr * 2], pl = po[R * HEADS * DV + rr * 2 + 1];
+    float v[ND];
+#pragma unroll
+    for (int c = 0; c < ND; c++) v[c] = po[rr * DV + c * 64 + lane];
+    const float next = fmaxf(m, pm);
+    const float zero = next == -INFINITY ? 0.f : next;
+    const float keep = __builtin_amdgcn_exp2f(m - zero), add = __builtin_amdgcn_exp2f(pm - zero);
+    m = next;
+    l = l * keep + pl * add;
+#pragma unroll
+    for (int c = 0; c < ND; c++) o[c] = o[c] * keep + v[c] * add;
+  }
+  const int64_t rt = r / a.group;
+  const int h = hk * a.group + (int)(r - rt * a.group);
+  elem* op = reinterpret_cast<elem*>(a.out) + (p.q0 + rt) * a.out_stride[0] + h * a.out_stride[1];
+#pragma unroll
+  for (int c = 0; c < ND; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
+  if (a.lse && lane == 0) a.lse[(p.q0 + rt) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Row tiles of R rows that a call can have at most: each sequence rounds up once.
+int64_t most_tiles(const AttendArgs& a, int R) {
+  return a.q_rows * a.group / R + (a.num_seqs < a.q_rows ? a.num_seqs : a.q_rows);
+}
+
+// How the list of items is made for a call of tiles of R rows, and the number of items at most: a split of
+// C keys has at least `min_split` of them, and the whole call's keys over C is at most `target`.
+//
+// min_split: few rows, with 64, 128 and 256 keys at least: one sequence of 4000 21.4, 15.8 and 15.2 us, 16 of 600 27.9,
+// 21.3 and 18.7, one of 1500 of a latent cache 18.8, 18.3 and 21.1.  Many rows, with 128, 256 and 512: a chunk of 64 behind
+// 1436 22.8, 22.3 and 26.6, of 256 behind 1744 35.1, 34.9 and 33.5, of 32 of a latent cache behind 1468 35.5, 36.1 and 43.6.
+//
+// Calls of many rows are split when their row tiles, which the host knows, are fewer than the target, or when some of
+// several sequences may be so long that their one tile each (a decoding row beside a chunk) would run on alone; else one
+// launch does all.  The second rule, applied and not: a chunk of 4096 beside one row of 32768 keys 250 and 876 us, beside
+// four of 65536 387 and 1668, a latent chunk of 512 beside one of 32768 71 and 1258; beside one of 16384 it would gain
+// too (255 and 517).  Calls whose sequences keep the GPU busy anyway pay for it: a chunk of 4096 beside 63
+// rows of 8192 686 and 670, of 32768 1772 and 1756, four fp16 prompts up to 4096 139 and 127; hence not for
+// shorter ones.
+//
+// A latent cache's target leaves places to the tiles themselves.  With the whole GPU as its target: 32 sequences
+// up to 6000 of 16 heads 52.4 us for 38.4, 16 sequences up to 16384 of 128 heads 129 for 90; but half the GPU, which
+// it comes down to, is too little where tiles are many: a chunk of 255 tokens of 32 heads 118 for 194, and from 128 tiles
+// on, where a call counts as filling that half and is not split, 64 sequences up to 16384 of 128 heads 358 for 705.
+//
+// Only split tiles have partial results.  A split tile of n > C keys has at most (n + C - 1) / C < 2 n / C
+// splits, so that they are less than twice the target, however many row tiles the call has.  A call of more
+// items than that has just those places, and takes the split tiles first; of another the list is left in the order
+// of the sequences, which is found sooner (a sequence of 1500 12.0 us for 12.8, 64 up to 8192 207.3 for 208.1).
+constexpr int64_t kLongKeys = 16384;
+struct Plan {
+  int64_t items, joins;  // joins: workgroups of the second launch, 0: no split can be
+  bool few_places;       // fewer places of partial results than items
+};
+// heads: KV heads of an item; a->kv_heads then counts those of them.
+Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus, int heads = 1) {
+  const bool latent = head_dim == kLatDim, few = R <= 32;
+  a->min_split = few ? 128 : 256;
+  Plan p = {most_tiles(*a, R) * a->kv_heads, 0, false};
+  // items that run at once: 8 or 2 workgroups a compute unit, and one of a latent cache, where the
+  // whole list, `tiles` longer than the target at most, should be one round
+  a->target = (int64_t)num_cus * (few ? 8 : 2);
+  if (latent) a->target = num_cus - p.items > num_cus / 2 ? num_cus - p.items : num_cus / 2;
+  a->join_parts = 0;
+  a->slots = 0;
+  const int64_t most_splits = (a->max_kv + a->min_split - 1) / a->min_split;
+  const bool fills = a->q_rows * a->group / R * a->kv_heads >= a->target;
+  if (most_splits > 1 && (few || !fills || (a->num_seqs > 1 && a->max_kv > kLongKeys))) {
+    const int64_t rows = a->max_q * a->group < R ? a->max_q * a->group : R;  // of a tile at most
+    a->join_parts = (int32_t)((rows + 3) / 4) * heads;
+    p.items += most_splits - 1 <= a->target / p.items ? p.items * (most_splits - 1) : a->target;
+    p.few_places = p.items > 2 * a->target;
+    a->slots = p.few_places ? 2 * a->target : p.items;
+    p.joins = a->slots * a->join_parts;
+  } else {
+    a->min_split = a->max_kv + 1;
+  }
+  return p;
+}
+
+// kernels: of calls whose items all have a place for a partial result, or that are not split, and of others.
+template <class T, int DV, int R, int HEADS = 1>
+hipError_t launch_split(void (*const (&kernels)[2])(AttendArgs), AttendArgs a, int32_t num_cus, hipStream_t stream) {
+  const Plan p = plan(&a, R, DV == kLatValue ? kLatDim : DV, num_cus, HEADS);
+  if (p.items > 0x7fffffff || p.joins > 0x7fffffff) return hipErrorInvalidValue;
+  kernels[p.few_places]<<<dim3((unsigned)p.items), 256, 0, stream>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.joins == 0) return e;
+  k_attend_join<T, DV, R, HEADS><<<dim3((unsigned)p.joins), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
 
 }  // namespace
 }  // namespace hc
