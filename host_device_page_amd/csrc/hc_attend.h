@@ -430,34 +430,26 @@ __device__ __forceinline__ Part* parts_of(const AttendArgs& a) {
 
 // ---------------------------------------------------------------- splits: how many, and their join
 // Joins the splits of a row tile, a wave a row.  A workgroup looks at the item of one place; all but the first
-// split of a tile that was split have nothing to do.  HEADS: KV heads of an item, R rows each.
-template <class T, int DV, int R, int HEADS = 1>
+// split of a tile that was split have nothing to do.
+template <class T, int DV, int R>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   typedef typename T::elem elem;
   const int64_t first = blockIdx.x / a.join_parts;
-  const Part p = parts_of<DV, R * HEADS>(a)[first];
+  const Part p = parts_of<DV, R>(a)[first];
   // a q_start that goes back (reported) can make more items than the call has room for
   if (p.splits <= 1 || first + p.splits > a.slots) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t tile = p.tile_hk / a.kv_heads;
-  int hk = (int)(p.tile_hk - tile * a.kv_heads);
-  int rr = (int)(blockIdx.x % a.join_parts) * 4 + wave;
-  int64_t r = tile * R + rr;
-  if (HEADS > 1) {
-    const int per = a.join_parts / HEADS, part = (int)(blockIdx.x % a.join_parts), head = part / per;
-    hk = hk * HEADS + head;
-    rr = (part - head * per) * 4 + wave;
-    r = tile * R + rr;
-    if (rr >= R) return;
-    rr += head * R;
-  }
-  if (rr >= R * HEADS || r >= p.m * a.group) return;
+  const int hk = (int)(p.tile_hk - tile * a.kv_heads);
+  const int rr = (int)(blockIdx.x % a.join_parts) * 4 + wave;
+  const int64_t r = tile * R + rr;
+  if (rr >= R || r >= p.m * a.group) return;
   constexpr int ND = DV / 64;
   float m = -INFINITY, l = 0.f, o[ND] = {};
 #pragma unroll 4
   for (int k = 0; k < (int)p.splits; k++) {
-    const float* po = a.work + (first + k) * partial_floats<DV>(R * HEADS);
-    const float pm = po[R * HEADS * DV + rr * 2], pl = po[R * HEADS * DV + rr * 2 + 1];
+    const float* po = a.work + (first + k) * partial_floats<DV>(R);
+    const float pm = po[R * DV + rr * 2], pl = po[R * DV + rr * 2 + 1];
     float v[ND];
 #pragma unroll
     for (int c = 0; c < ND; c++) v[c] = po[rr * DV + c * 64 + lane];
@@ -511,22 +503,27 @@ struct Plan {
   int64_t items, joins;  // joins: workgroups of the second launch, 0: no split can be
   bool few_places;       // fewer places of partial results than items
 };
-// heads: KV heads of an item; a->kv_heads then counts those of them.
-Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus, int heads = 1) {
+// Kernels with a rule of their own say the workgroups of a compute unit (per_cu) and the least keys of a split, and
+// of how many KV heads an item is (heads; a->kv_heads then counts items of a tile).  Few tiles' list should be one round
+// of workgroups, tiles included; of many, two rounds, since their tiles are of unlike lengths.  (64 sequences up to 8192
+// of 4-bit rows, few tiles: a target of the whole round 100 us, less the tiles 83; 256 such sequences in one round 316,
+// two 285, three 283; 128 up to 2048 54, 56, 63.)
+Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus, int heads = 0, int per_cu = 0, int least = 0) {
   const bool latent = head_dim == kLatDim, few = R <= 32;
-  a->min_split = few ? 128 : 256;
+  a->min_split = least ? least : few ? 128 : 256;
   Plan p = {most_tiles(*a, R) * a->kv_heads, 0, false};
   // items that run at once: 8 or 2 workgroups a compute unit, and one of a latent cache, where the
   // whole list, `tiles` longer than the target at most, should be one round
-  a->target = (int64_t)num_cus * (few ? 8 : 2);
-  if (latent) a->target = num_cus - p.items > num_cus / 2 ? num_cus - p.items : num_cus / 2;
+  a->target = (int64_t)num_cus * (per_cu ? per_cu : few ? 8 : 2);
+  if (per_cu) a->target = p.items * 4 <= a->target ? a->target - p.items : 2 * a->target;
+  if (latent && !per_cu) a->target = num_cus - p.items > num_cus / 2 ? num_cus - p.items : num_cus / 2;
   a->join_parts = 0;
   a->slots = 0;
   const int64_t most_splits = (a->max_kv + a->min_split - 1) / a->min_split;
   const bool fills = a->q_rows * a->group / R * a->kv_heads >= a->target;
   if (most_splits > 1 && (few || !fills || (a->num_seqs > 1 && a->max_kv > kLongKeys))) {
     const int64_t rows = a->max_q * a->group < R ? a->max_q * a->group : R;  // of a tile at most
-    a->join_parts = (int32_t)((rows + 3) / 4) * heads;
+    a->join_parts = (int32_t)(heads ? rows * heads : (rows + 3) / 4);
     p.items += most_splits - 1 <= a->target / p.items ? p.items * (most_splits - 1) : a->target;
     p.few_places = p.items > 2 * a->target;
     a->slots = p.few_places ? 2 * a->target : p.items;
@@ -538,15 +535,20 @@ Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus, int heads = 1
 }
 
 // kernels: of calls whose items all have a place for a partial result, or that are not split, and of others.
-template <class T, int DV, int R, int HEADS = 1>
-hipError_t launch_split(void (*const (&kernels)[2])(AttendArgs), AttendArgs a, int32_t num_cus, hipStream_t stream) {
-  const Plan p = plan(&a, R, DV == kLatValue ? kLatDim : DV, num_cus, HEADS);
+typedef void (*AttendKernel)(AttendArgs);
+hipError_t launch_planned(const AttendKernel (&kernels)[2], AttendKernel join, const AttendArgs& a, const Plan& p,
+                          hipStream_t stream) {
   if (p.items > 0x7fffffff || p.joins > 0x7fffffff) return hipErrorInvalidValue;
   kernels[p.few_places]<<<dim3((unsigned)p.items), 256, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.joins == 0) return e;
-  k_attend_join<T, DV, R, HEADS><<<dim3((unsigned)p.joins), 256, 0, stream>>>(a);
+  join<<<dim3((unsigned)p.joins), 256, 0, stream>>>(a);
   return hipGetLastError();
+}
+template <class T, int DV, int R>
+hipError_t launch_split(const AttendKernel (&kernels)[2], AttendArgs a, int32_t num_cus, hipStream_t stream) {
+  const Plan p = plan(&a, R, DV == kLatValue ? kLatDim : DV, num_cus);
+  return launch_planned(kernels, k_attend_join<T, DV, R>, a, p, stream);
 }
 
 }  // namespace

@@ -44,38 +44,101 @@ struct MxRows {
 
 // ---------------------------------------------------------------- few rows: decoding
 // Rows and products are the decoding kernel's of the cache of elements, 16 (token, head) pairs of a KV head; what differs is
-// how little is read: 68 bytes of a key's 128 dims.
+// how little is read, 68 bytes of a key's 128 dims, and that a row's heads lie next to each other in it.
 //
-// HEADS waves take a KV head each and the same keys, so that a workgroup reads HEADS * 64 bytes of a row in one
-// piece and its waves share the lines that a head's 64 bytes do not fill; the other waves share a head's
-// keys in turns of 64, and are joined at the end.
+// A workgroup takes up to four KV heads, and reads their part of a row in one piece, straight into LDS; from there
+// every wave takes its own head's codes and scales into registers, and the next tile is on its way while they
+// are computed.  Waves that share a head take 32 keys of a tile each and are joined at the end.  (Waves that load their
+// head's 64 bytes themselves ask for each line of memory several times: 64 sequences up to 8192 tokens took 93 us so,
+// and 130 with one head to a workgroup.)
 //
-//   K  straight into the operand registers: the order of the dims inside a product is free, so a lane
-//      takes D / 4 dims of a key next to each other, one load and one scale, and the queries the same.
-//   V  16 bytes a lane, a block of a key and its scale, through LDS as elements and back transposed.
-template <int D>
-__device__ __forceinline__ int few_place(int key, int chunk) {  // of 32 keys; written and read without conflicts
-  const int x = D == 128 ? 2 * (key & 7) | ((key >> 3) & 1) : 2 * ((key >> 1) & 3) | ((key >> 3) & 1);
-  return key * D * 2 + (chunk ^ x) * 16;
+// Measured: 64 sequences up to 8192 tokens, 32/8 heads of 128, 73 us and 7 us to join = 4.0 TB/s of rows; 256 of them
+// 4.1; 32 sequences in a window of 4096 with 4 sinks, scattered slots, fp16 heads of 64, 26 and 6 us; one
+// sequence of 1500 13 us.  Four workgroups a compute unit (128 registers a lane) for three: 82 us for 85 on the first.
+//
+//   K  the order of the dims inside a product is free, so a lane takes D / 4 dims of a key next to each other,
+//      one read and one scale, and the queries the same.
+//   V  a block of 32 dims of a key and its scale a lane, 64 dims at a time through LDS as elements and back
+//      transposed.
+constexpr int kFewKeys = 32;  // of a wave and tile
+
+// Where the 16-byte chunk of a key's 64 dims of V lies; written and read without conflicts.
+__device__ __forceinline__ int few_place(int key, int chunk) {
+  const int x = ((key >> 1) & 1) << 2 | ((key >> 2) & 1) << 1 | ((key >> 3) & 1);
+  return key * 128 + (chunk ^ x) * 16;
+}
+
+// A tile of rows in LDS: CPR chunks of codes a key, in places that 16 keys' same chunk does not share, and
+// S4 dwords of scales.
+template <int D, int HEADS>
+struct FewStage {
+  static constexpr int W = 4;  // waves
+  static constexpr int KW = W / HEADS;
+  static constexpr int KEYS = kFewKeys * KW;
+  static constexpr int CPR = HEADS * D / 32;
+  static constexpr int CODES = KEYS * CPR * 16;
+  static constexpr int S4 = HEADS * D / 128 > 0 ? HEADS * D / 128 : 1;
+  static constexpr int SCALES = KEYS * S4 * 4;
+  static constexpr int LOADS = KEYS * CPR / (64 * W);  // of a wave, K and V each
+  static __device__ __forceinline__ int turn(int key) { return CPR >= 16 ? key & 15 : (key / (16 / CPR)) & (CPR - 1); }
+  static __device__ __forceinline__ int place(int key, int chunk) { return (key * CPR + (chunk ^ turn(key))) * 16; }
+};
+
+// The maximum over the four lanes that are 16 apart, without LDS.
+__device__ __forceinline__ float max_of_quads(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t y = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// 4 bytes a lane from memory into LDS, lane i to lds + 4 i (lds the same in all lanes), as lds_load.
+__device__ __forceinline__ void lds_load_dword(const uint8_t* from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
+}
+
+// The items of a tile in another order: eight splits of one group of KV heads, then the same eight of the next, so that
+// items which read the same rows are eight workgroups apart, on the same XCD at the same time, and its L2 reads
+// the lines that both of them need once.  (`index`, where an item's partial result lies, stays in the list's order.)
+__device__ __forceinline__ void pair_groups(const AttendArgs& a, Item* it) {
+  const int at = it->hk * it->splits + it->split, whole = it->splits / 8 * 8;
+  if (at < whole * a.kv_heads) {
+    const int chunk = at / (8 * a.kv_heads), rest = at - chunk * 8 * a.kv_heads;
+    it->hk = rest / 8;
+    it->split = chunk * 8 + rest % 8;
+  } else {
+    const int rest = at - whole * a.kv_heads, left = it->splits - whole;
+    it->hk = rest / left;
+    it->split = whole + rest - it->hk * left;
+  }
+  it->index += it->hk * it->splits + it->split - at;
 }
 
 template <class T, int D, int HEADS, bool SPLIT_FIRST>
-__global__ __launch_bounds__(256, 2) void k_attend_mxfp4_few(AttendArgs a) {
+__global__ __launch_bounds__(256, 4) void k_attend_mxfp4_few(AttendArgs a) {
   typedef typename T::v8 v8;
   typedef typename T::elem elem;
   typedef MxRows<T, D, D, HEADS> Rows;
-  constexpr int KW = 4 / HEADS;         // waves that share a head's keys
+  typedef FewStage<D, HEADS> Stage;
+  constexpr int W = Stage::W;
+  constexpr int KW = Stage::KW;         // waves that share a head's keys
+  constexpr int G = Stage::KEYS;
   constexpr int KS = D / 32;            // product steps over the head: dwords of a lane and key
   constexpr int DT = D / 16;            // 16-dim tiles of the output
-  constexpr int VL = 64 * (D / 32) / 64;  // V loads of a lane
-  constexpr int VK = 64 / VL;           // keys of one
+  constexpr int VL = D / 64;            // 64 dims of V at a time
   constexpr int R = kRowTile;
+  constexpr int SL = G <= 64 ? 1 : G / 64;  // keys of a lane
   typedef uint32_t kw_t __attribute__((ext_vector_type(KS)));
-  __shared__ __align__(16) uint8_t s_v[4][32 * D * 2];
-  __shared__ float s_ml[4][64][2];
+  // codes of K and V, their scales, and 64 dims of 32 keys a wave; behind the loop the waves' sums
+  constexpr int kStage = 2 * (Stage::CODES + Stage::SCALES), kAll = kStage + W * kFewKeys * 128;
+  constexpr int kJoin = KW > 1 ? W * 64 * DT * 16 : 0;
+  __shared__ __align__(16) uint8_t s_all[kAll > kJoin ? kAll : kJoin];
+  __shared__ float s_ml[W][64][2];
   __shared__ int64_t s_plan[8];
   Item it;
   if (!find_item<true, SPLIT_FIRST>(a, R, s_plan, parts_of<D, R * HEADS>(a), &it)) return;
+  if (a.kv_heads > 1) pair_groups(a, &it);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4, kw = wave / HEADS, hw = wave - kw * HEADS;
   const int hk = it.hk * HEADS + hw;
@@ -91,7 +154,6 @@ __global__ __launch_bounds__(256, 2) void k_attend_mxfp4_few(AttendArgs a) {
   const int p_first = it.q.kv - it.q.m + r0 / a.group, p_last = it.q.kv - it.q.m + (r0 + rows - 1) / a.group;
   const Span span = span_of(a, it.q.kv, p_first, p_last);
   // this split's part of the span
-  constexpr int G = 64 * KW;
   const int part = ((span.n + it.splits - 1) / it.splits + G - 1) / G * G;
   const int i0 = (int64_t)it.split * part < span.n ? it.split * part : span.n;
   const int i1 = i0 + part < span.n ? i0 + part : span.n;
@@ -109,137 +171,185 @@ __global__ __launch_bounds__(256, 2) void k_attend_mxfp4_few(AttendArgs a) {
   }
   f32x4 o[DT] = {};
   float m = -INFINITY, l = 0.f;
-  // V: a lane's block, and its key among the VK of a load: 16 lanes next to each other write 16 places
-  const int block = lane % (D / 32);
-  const int vkey = D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) + ((lane >> 3) & 1) * 8
-                            : ((lane >> 1) & 1) + ((lane >> 2) & 1) * 2 + ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 8 +
-                                  (lane >> 5) * 16;
-  const int64_t codes = mxfp4_codes((int64_t)a.kv_heads * HEADS * D);
-  const uint8_t* kc_at = a.k_rows + hk * (D / 2) + quad * (D / 8);
-  const uint8_t* ks_at = a.k_rows + codes + hk * (D / 32) + quad * KS / 4;
-  const uint8_t* vc_at = a.v_rows + hk * (D / 2) + block * 16;
-  const uint8_t* vs_at = a.v_rows + codes + hk * (D / 32) + block;
-  uint8_t* sv = s_v[wave];
-  // Slot of the tile's key `lane`, kNoSlot past the end and for a key that no row sees: with one
-  // token a tile (decoding) that is every hidden key, whose values then are zeros in the product.
-  auto entry = [&](int base) {
-    const int i = base + lane;
-    const int j = span.key(i < i1 ? i : i0);
-    Entry e = {0, -1, 0};
-    if (i < i1 && (p_first != p_last || visible(a, p_first, j))) e = entry_of(a, it.s, (uint32_t)j);
-    return e;
+  uint8_t* sk = s_all;
+  uint8_t* sv = s_all + Stage::CODES;
+  uint8_t* ssk = s_all + 2 * Stage::CODES;
+  uint8_t* ssv = ssk + Stage::SCALES;
+  uint8_t* st_v = s_all + kStage + wave * kFewKeys * 128;
+  // The table entry of a tile's key `lane` on its way, without a branch: past the end it is the last key's.
+  const int64_t* table = a.table + it.s * a.table_stride;
+  struct Key {
+    int64_t page;
+    uint32_t e, rest;  // place in the table's row, token inside the entry
+    bool seen;         // with one token a tile (decoding) a hidden key is none
   };
-  kw_t kc[4];
-  v4u vc[VL];
-  uint32_t ks[4], vs[VL];
-  auto load_k = [&](uint32_t slot) {
+  auto key_of = [&](int i) {
+    const uint32_t j = span.key(i < i1 ? i : i1 - 1);
+    Key k;
+    k.e = (uint32_t)(((uint64_t)j * a.entry_magic) >> a.entry_shift);  // j / entry
+    k.rest = j - k.e * (uint32_t)a.entry;
+    k.page = table[k.e];
+    k.seen = i < i1 && (p_first != p_last || visible(a, p_first, (int)j));
+    return k;
+  };
+  // Its slot (0 for no key, of which `there` then has no bit); a bad entry is remembered for the end.
+  uint32_t bad = ~0u;
+  auto slot_in = [&](const Key& k, uint64_t* there) {
+    const bool ok = k.page >= 0 && k.page < a.entries;
+    bad = k.seen && !ok && k.e < bad ? k.e : bad;
+    *there = __ballot(k.seen && ok);
+    return k.seen && ok ? (uint32_t)k.page * (uint32_t)a.entry + k.rest : 0u;
+  };
+  // A tile's rows on their way into LDS.  (Rows of K and V are equally long.)
+  const uint32_t row_bytes = (uint32_t)a.k_row;
+  const int codes = (int)mxfp4_codes((int64_t)a.kv_heads * HEADS * D);
+  const uint8_t* k_at = a.k_rows + it.hk * HEADS * (D / 2);
+  const uint8_t* v_at = a.v_rows + it.hk * HEADS * (D / 2);
+  const int scale0 = codes + (it.hk * HEADS * (D / 32) & ~3);  // a single head of 64 has two bytes of a dword
+  auto load = [&](const uint32_t (&slot)[SL]) {
+    auto slot_at = [&](int key) {
+      uint32_t x = __shfl(slot[0], key & 63);
+      for (int n = 1; n < SL; n++) {
+        const uint32_t y = __shfl(slot[n], key & 63);
+        x = key >> 6 == n ? y : x;
+      }
+      return x;
+    };
 #pragma unroll
-    for (int t = 0; t < 4; t++) {
-      const uint32_t sl = __shfl(slot, t * 16 + col);
-      const uint64_t at = sl == kNoSlot ? 0 : (uint64_t)sl * a.k_row;
-      kc[t] = *reinterpret_cast<const kw_t*>(kc_at + at);
-      ks[t] = ks_at[at];
+    for (int n = 0; n < Stage::LOADS; n++) {
+      const int at = (n * W + wave) * 64 + lane, key = at / Stage::CPR, chunk = at % Stage::CPR ^ Stage::turn(key);
+      const uint64_t off = (uint64_t)slot_at(key) * row_bytes + chunk * 16;
+      lds_load(k_at + off, lds_offset(sk + (n * W + wave) * 1024));
+      lds_load(v_at + off, lds_offset(sv + (n * W + wave) * 1024));
+    }
+    // dwords of scales, K's and then V's: 64 a wave
+    constexpr int N = G * Stage::S4;
+    if (wave * 64 < 2 * N) {
+      const int at = wave * 64 + lane, is_v = at >= N, d = at - (is_v ? N : 0), key = d / Stage::S4;
+      const uint8_t* rows_at = is_v ? a.v_rows : a.k_rows;
+      lds_load_dword(rows_at + (uint64_t)slot_at(key) * row_bytes + scale0 + d % Stage::S4 * 4, lds_offset(ssk + wave * 256));
     }
   };
-  auto load_v = [&](uint32_t slot) {
+  // V: a lane's block of 64 dims, and its key: 16 lanes next to each other write 16 places
+  const int block = lane & 1;
+  const int vkey = ((lane >> 1) & 1) | ((lane >> 2) & 3) << 2 | ((lane >> 4) & 1) << 1 | (lane >> 5) << 4;
+  const int key0 = kw * kFewKeys;  // the wave's first of the tile
+  const int byte0 = hw * (D / 32) + (HEADS * D < 128 ? (hk & 1) * 2 : 0);
+  uint64_t there[SL] = {}, there_next[SL] = {};
+  uint32_t slot[SL];
+  Key next[SL];
+  if (i0 < i1) {
 #pragma unroll
-    for (int x = 0; x < VL; x++) {
-      const uint32_t sl = __shfl(slot, x * VK + vkey);
-      const uint64_t at = sl == kNoSlot ? 0 : (uint64_t)sl * a.v_row;
-      const v4u y = *reinterpret_cast<const v4u*>(vc_at + at);
-      const uint32_t z = vs_at[at];
-      vc[x] = sl == kNoSlot ? v4u{0, 0, 0, 0} : y;
-      vs[x] = sl == kNoSlot ? 127 : z;
-    }
-  };
-  int base = i0 + kw * 64;
-  Entry next_entry = entry(base + G);
-  uint32_t slot = slot_from(a, entry(base)), slot_next = kNoSlot;
-  if (base < i1) {
-    load_k(slot);
-    load_v(slot);
+    for (int n = 0; n < SL; n++) slot[n] = slot_in(key_of(i0 + n * 64 + lane), &there[n]);
+    load(slot);
+#pragma unroll
+    for (int n = 0; n < SL; n++) next[n] = key_of(i0 + G + n * 64 + lane);
   }
-  for (; base < i1; base += G) {
-    f32x4 st[4] = {};
+  for (int tile0 = i0; tile0 < i1; tile0 += G) {
+    const int base = tile0 + key0;  // the wave's keys
+    const bool more = tile0 + G < i1;
 #pragma unroll
-    for (int t = 0; t < 4; t++)
+    for (int n = 0; n < SL; n++) slot[n] = more ? slot_in(next[n], &there_next[n]) : 0;
+    lds_arrived();
+    __syncthreads();
+    kw_t kc[2];
+    v4u vc[VL];
+    uint32_t ks[2], vs[VL];
 #pragma unroll
-      for (int i = 0; i < KS; i++)
+    for (int t = 0; t < 2; t++) {
+      const int key = key0 + t * 16 + col;
+      if (D == 128)
+        kc[t] = *reinterpret_cast<const kw_t*>(sk + Stage::place(key, hw * 4 + quad));
+      else
+        kc[t] = *reinterpret_cast<const kw_t*>(sk + Stage::place(key, hw * 2 + quad / 2) + (quad & 1) * 8);
+      ks[t] = ssk[key * Stage::S4 * 4 + byte0 + quad * KS / 4];
+    }
+#pragma unroll
+    for (int g = 0; g < VL; g++) {
+      const int key = key0 + vkey;
+      vc[g] = *reinterpret_cast<const v4u*>(sv + Stage::place(key, hw * (D / 32) + g * 2 + block));
+      vs[g] = ssv[key * Stage::S4 * 4 + byte0 + g * 2 + block];
+    }
+    __syncthreads();  // every wave has its codes: the next tile's may come
+    if (more) {
+      load(slot);
+#pragma unroll
+      for (int n = 0; n < SL; n++) next[n] = key_of(tile0 + 2 * G + n * 64 + lane);
+    }
+    const uint32_t here = (uint32_t)(there[SL > 1 ? key0 / 64 : 0] >> (key0 & 63));  // the wave's keys
+    f32x4 st[2] = {};
+#pragma unroll
+    for (int i = 0; i < KS; i++)
+#pragma unroll
+      for (int t = 0; t < 2; t++)
         st[t] = T::mfma16(__builtin_bit_cast(v8, mx_decode<kIsBf16<T>>(kc[t][i], mx_scale(ks[t]))), q[i], st[t]);
-    const uint64_t there = __ballot(slot != kNoSlot);
-    const bool more = base + G < i1;
-    slot_next = slot_from(a, next_entry);
-    next_entry = entry(base + 2 * G);
-    if (more) load_k(slot_next);
-    float x[16];
+    float x[8];
 #pragma unroll
-    for (int e = 0; e < 16; e++) x[e] = st[e / 4][e % 4];
+    for (int e = 0; e < 8; e++) x[e] = st[e / 4][e % 4];
     // hidden keys: past the end, bad entries, and those that this row does not see
-    const bool whole = there == ~0ull && (!a.causal || (span.key(base + 63) <= p_first &&
-                                                        (a.window == 0 || p_last - span.key(base) < a.window)));
+    const bool whole = here == ~0u && (!a.causal || (span.key(base + kFewKeys - 1) <= p_first &&
+                                                     (a.window == 0 || p_last - span.key(base) < a.window)));
     if (!whole) {
-      const uint64_t see = sees(a, span, there, p, base) >> (quad * 4);
-      const uint32_t part2[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
+      const uint32_t see = (uint32_t)sees(a, span, here, p, base) >> (quad * 4);
 #pragma unroll
-      for (int e = 0; e < 16; e++) x[e] = (part2[e / 8] >> (e % 8 / 4 * 16 + e % 4)) & 1 ? x[e] : -INFINITY;
+      for (int e = 0; e < 8; e++) x[e] = (see >> (e / 4 * 16 + e % 4)) & 1 ? x[e] : -INFINITY;
     }
     float top = x[0];
 #pragma unroll
-    for (int e = 1; e < 16; e++) top = fmaxf(top, x[e]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
+    for (int e = 1; e < 8; e++) top = fmaxf(top, x[e]);
+    top = max_of_quads(top);
     if (__any((top - m) * c > kGrow || (m == -INFINITY && top != -INFINITY))) {
-      const float next = fmaxf(m, top);
-      const float keep = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - next) * c);
-      m = next;
+      const float grown = fmaxf(m, top);
+      const float keep = grown == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - grown) * c);
+      m = grown;
       l *= keep;
 #pragma unroll
       for (int d = 0; d < DT; d++) o[d] *= keep;
     }
     const float zero = m == -INFINITY ? 0.f : m * c;
+    f32x8 w;
     float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; e++) {
-      x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -zero));
-      sum += x[e];
+    for (int e = 0; e < 8; e++) {
+      w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -zero));
+      sum += w[e];
     }
     l += sum;  // this lane's keys; the quads are summed at the end
+    const v8 wt = __builtin_convertvector(w, v8);  // the weight's one rounding, as the product's operand
+    if (here != ~0u && !((here >> vkey) & 1)) {  // what was fetched in place of no key must not reach the product
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
+      for (int g = 0; g < VL; g++) vc[g] = v4u{0, 0, 0, 0}, vs[g] = 127;
+    }
+#pragma unroll
+    for (int g = 0; g < VL; g++) {
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int y = u * VL / 2; y < (u + 1) * VL / 2; y++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          *reinterpret_cast<v4u*>(sv + few_place<D>((y - u * VL / 2) * VK + vkey, block * 4 + i)) =
-              mx_decode<kIsBf16<T>>(vc[y][i], mx_scale(vs[y]));
-      if (u == 1 && more) load_v(slot_next);
-      f32x8 w;
-#pragma unroll
-      for (int e = 0; e < 8; e++) w[e] = x[u * 8 + e];
-      const v8 wt = __builtin_convertvector(w, v8);  // the weight's one rounding, as the product's operand
+      for (int i = 0; i < 4; i++)
+        *reinterpret_cast<v4u*>(st_v + few_place(vkey, block * 4 + i)) = mx_decode<kIsBf16<T>>(vc[g][i], mx_scale(vs[g]));
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int d = 0; d < DT; d++) {
+      for (int d = 0; d < 4; d++) {
         s16x4 v[2];
 #pragma unroll
         for (int t = 0; t < 2; t++) {
           const int key = t * 16 + quad * 4 + col / 4;
           v[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4)(sv + few_place<D>(key, d * 2 + (col & 3) / 2) + (col & 1) * 8));
+              (lds_s16x4)(st_v + few_place(key, d * 2 + (col & 3) / 2) + (col & 1) * 8));
         }
         const v8 vt = __builtin_bit_cast(v8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        o[d] = T::mfma16(vt, wt, o[d]);
+        o[g * 4 + d] = T::mfma16(vt, wt, o[g * 4 + d]);
       }
     }
-    slot = slot_next;
+#pragma unroll
+    for (int n = 0; n < SL; n++) there[n] = there_next[n];
   }
+  if (bad != ~0u) flag(a.wrong, kWrongIndex, it.s * a.table_stride + bad);
+  __syncthreads();  // the tiles are done with
+  float* s_q = reinterpret_cast<float*>(s_all) + wave * (KW > 1 ? 64 * DT * 4 : D);  // this wave's
   if (KW > 1) {  // the first wave of a head takes in the others', a lane its own places
-    __builtin_amdgcn_wave_barrier();
-    f32x4* so = reinterpret_cast<f32x4*>(sv);
     if (kw > 0) {
 #pragma unroll
-      for (int d = 0; d < DT; d++) so[d * 64 + lane] = o[d];
+      for (int d = 0; d < DT; d++) reinterpret_cast<f32x4*>(s_q)[d * 64 + lane] = o[d];
       s_ml[wave][lane][0] = m;
       s_ml[wave][lane][1] = l;
     }
@@ -254,7 +364,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_mxfp4_few(AttendArgs a) {
       m = next;
       l = l * keep + s_ml[from][lane][1] * add;
 #pragma unroll
-      for (int d = 0; d < DT; d++) o[d] = o[d] * keep + reinterpret_cast<const f32x4*>(s_v[from])[d * 64 + lane] * add;
+      for (int d = 0; d < DT; d++) o[d] = o[d] * keep + reinterpret_cast<const f32x4*>(s_all)[(from * DT + d) * 64 + lane] * add;
     }
   }
   l += __shfl_xor(l, 16);
@@ -296,8 +406,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_mxfp4_few(AttendArgs a) {
     again &= again - 1;
     const int ta = (r0 + y) / a.group, ha = hk * a.group + (r0 + y - ta * a.group);
     float oo[D / 64], mm, ll;
-    exact_row<T, D, D, Rows>(a, it.s, it.q.q0 + ta, ha, it.q.kv - it.q.m + ta, span, i0, i1, reinterpret_cast<float*>(sv),
-                             oo, &mm, &ll);
+    exact_row<T, D, D, Rows>(a, it.s, it.q.q0 + ta, ha, it.q.kv - it.q.m + ta, span, i0, i1, s_q, oo, &mm, &ll);
     elem* oa = reinterpret_cast<elem*>(a.out) + (it.q.q0 + ta) * a.out_stride[0] + ha * a.out_stride[1];
     for (int x = 0; x < D / 64; x++) {
       if (it.splits > 1) part_o[(hw * R + y) * D + x * 64 + lane] = oo[x];
@@ -312,6 +421,74 @@ __global__ __launch_bounds__(256, 2) void k_attend_mxfp4_few(AttendArgs a) {
       }
     }
   }
+}
+
+// Joins the splits of rows, PER waves of a workgroup a row: with the greatest maximum known first, from one load a split
+// over the lanes, the sums are loaded together instead of one after the other.  A workgroup looks at the
+// item of one place; all but the first split of a tile that was split have nothing to do.
+template <class T, int D, int HEADS, int PER>
+__global__ __launch_bounds__(256) void k_attend_mxfp4_join(AttendArgs a) {
+  typedef typename T::elem elem;
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  constexpr int R = kRowTile, ND = D / 64;
+  __shared__ float s_w[4][64], s_o[4][D], s_l[4];
+  const int64_t first = blockIdx.x / a.join_parts;
+  const Part p = parts_of<D, R * HEADS>(a)[first];
+  // a q_start that goes back (reported) can make more items than the call has room for
+  if (p.splits <= 1 || first + p.splits > a.slots) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), turn = wave % PER;
+  const int64_t tile = p.tile_hk / a.kv_heads;
+  const int part = (int)(blockIdx.x % a.join_parts), per = a.join_parts / HEADS, hw = part / per;
+  const int y = (part - hw * per) * (4 / PER) + wave / PER;
+  const int64_t r = tile * R + y;
+  const bool some = y < R && r < p.m * a.group;
+  const int hk = (int)(p.tile_hk - tile * a.kv_heads) * HEADS + hw, rr = hw * R + (some ? y : 0), splits = (int)p.splits;
+  const float* part_o = a.work + first * partial_floats<D>(R * HEADS) + rr * D;
+  const float* part_ml = a.work + first * partial_floats<D>(R * HEADS) + R * HEADS * D + rr * 2;
+  auto ml = [&](int k) { return *reinterpret_cast<const f2*>(part_ml + k * partial_floats<D>(R * HEADS)); };
+  float m = -INFINITY;
+  for (int k = lane; k < splits; k += 64) m = fmaxf(m, ml(k)[0]);
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float zero = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[ND] = {};
+  for (int k0 = turn; k0 < splits; k0 += 64 * PER) {  // splits k0, k0 + PER, ...
+    const int mine = k0 + PER * lane, left = (splits - k0 + PER - 1) / PER, n = left < 64 ? left : 64;
+    f2 v = {-INFINITY, 0.f};
+    if (mine < splits) v = ml(mine);
+    const float w = __builtin_amdgcn_exp2f(v[0] - zero);
+    l += v[1] * w;
+    s_w[wave][lane] = w;
+    __builtin_amdgcn_wave_barrier();
+    const float* po = part_o + k0 * partial_floats<D>(R * HEADS) + lane;
+#pragma unroll 8
+    for (int j = 0; j < n; j++) {
+      const float f = s_w[wave][j];
+#pragma unroll
+      for (int c = 0; c < ND; c++) o[c] += po[c * 64] * f;
+      po += PER * partial_floats<D>(R * HEADS);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+  if (PER > 1) {
+#pragma unroll
+    for (int c = 0; c < ND; c++) s_o[wave][c * 64 + lane] = o[c];
+    if (lane == 0) s_l[wave] = l;
+    __syncthreads();
+    if (turn > 0) return;
+    for (int w = 1; w < PER; w++) {
+      l += s_l[wave + w];
+#pragma unroll
+      for (int c = 0; c < ND; c++) o[c] += s_o[wave + w][c * 64 + lane];
+    }
+  }
+  if (!some) return;
+  const int64_t rt = r / a.group;
+  const int h = hk * a.group + (int)(r - rt * a.group);
+  elem* op = reinterpret_cast<elem*>(a.out) + (p.q0 + rt) * a.out_stride[0] + h * a.out_stride[1];
+#pragma unroll
+  for (int c = 0; c < ND; c++) op[c * 64 + lane] = (elem)(l == 0.f ? 0.f : o[c] / l);
+  if (a.lse && lane == 0) a.lse[(p.q0 + rt) * a.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- tiles of 4-bit rows, as elements into LDS
@@ -433,14 +610,35 @@ int tile_rows(const AttendArgs& a, int32_t head_dim) {
   return rows <= 2 * kRowTile ? kRowTile : kTileRows;
 }
 
-// KV heads of an item of few rows: as many as divide the heads.
+// KV heads of an item of few rows: as many as divide the heads, up to the waves.  (Eight, with eight waves: 64
+// sequences up to 8192 of eight heads 83 us for 82, one sequence of 1500 15.6 for 14.0, 32 in a window of 4096 of fp16
+// heads of 64 31.5 for 34.)
 int heads_of(const AttendArgs& a) { return a.kv_heads % 4 == 0 ? 4 : a.kv_heads % 2 == 0 ? 2 : 1; }
+
+// How calls of few rows are split: four workgroups a compute unit, splits of 32 keys and more (of 64: a sequence of 1500
+// 14.0 us for 13.0) and no more than 128 of them (of 32768 keys: 64 splits 33 us, 128 24, 512 57).  And joined: where
+// there are few rows a workgroup a row, else a wave, for whose 64 sequences empty workgroups cost more (6.6 us
+// for 9.8; one of 32768 33 for 5).
+constexpr int kFewPerCu = 4, kFewLeast = 32, kFewSplits = 128, kFewAlone = 512;
+Plan few_plan(AttendArgs* a, int32_t head_dim, int heads, int32_t num_cus, bool* alone = nullptr) {
+  const int least = (int)(a->max_kv / kFewSplits);
+  Plan p = plan(a, kRowTile, head_dim, num_cus, heads, kFewPerCu, least > kFewLeast ? least : kFewLeast);
+  const bool row = a->q_rows * a->q_heads <= kFewAlone;
+  if (alone) *alone = row;
+  if (p.joins > 0 && !row) {
+    a->join_parts = (a->join_parts / heads + 3) / 4 * heads;
+    p.joins = a->slots * a->join_parts;
+  }
+  return p;
+}
 
 template <class T, int D, int HEADS>
 hipError_t launch_few(AttendArgs a, int32_t num_cus, hipStream_t stream) {
   a.kv_heads /= HEADS;
-  return launch_split<T, D, kRowTile, HEADS>({k_attend_mxfp4_few<T, D, HEADS, false>, k_attend_mxfp4_few<T, D, HEADS, true>}, a,
-                                             num_cus, stream);
+  bool alone;
+  const Plan p = few_plan(&a, D, HEADS, num_cus, &alone);
+  return launch_planned({k_attend_mxfp4_few<T, D, HEADS, false>, k_attend_mxfp4_few<T, D, HEADS, true>},
+                        alone ? k_attend_mxfp4_join<T, D, HEADS, 4> : k_attend_mxfp4_join<T, D, HEADS, 1>, a, p, stream);
 }
 template <class T, int D>
 hipError_t launch_heads(const AttendArgs& a, int32_t num_cus, hipStream_t stream) {
@@ -475,10 +673,12 @@ hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hi
 
 int64_t attend_mxfp4_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_cus) {
   if (args.q_rows <= 0 || args.num_seqs <= 0) return 0;
-  const int R = tile_rows(args, head_dim), heads = head_dim != kLatDim && R == kRowTile ? heads_of(args) : 1;
+  const int R = tile_rows(args, head_dim);
+  const bool few = head_dim != kLatDim && R == kRowTile;
+  const int heads = few ? heads_of(args) : 1;
   AttendArgs a = args;
   a.kv_heads /= heads;
-  const Plan p = plan(&a, R, head_dim, num_cus, heads);
+  const Plan p = few ? few_plan(&a, head_dim, heads, num_cus) : plan(&a, R, head_dim, num_cus);
   if (p.joins == 0) return 0;
   const int64_t floats = head_dim == 64    ? partial_floats<64>(R * heads)
                          : head_dim == 128 ? partial_floats<128>(R * heads)
