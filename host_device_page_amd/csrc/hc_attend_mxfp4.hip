@@ -84,6 +84,45 @@ struct FewStage {
   static __device__ __forceinline__ int place(int key, int chunk) { return (key * CPR + (chunk ^ turn(key))) * 16; }
 };
 
+// The keys of a split, where they are.
+struct FewKeys {
+  const AttendArgs& a;
+  const int64_t* table;  // the sequence's row
+  int64_t row;
+  Span span;
+  int i1, p;
+  bool one;              // a tile of one token (decoding), at position p: a key that it does not see is none
+  uint32_t bad = ~0u;    // the first entry that is not in the pool, kept for the end
+  struct Key {
+    int64_t page;
+    uint32_t e, rest;  // place in the table's row, token inside the entry
+    bool seen;
+  };
+  __device__ __forceinline__ FewKeys(const AttendArgs& args, int64_t s, const Span& sp, int end, int p_first, int p_last)
+      : a(args), table(args.table + s * args.table_stride), row(s * args.table_stride), span(sp), i1(end), p(p_first),
+        one(p_first == p_last) {}
+  // The table entry of the i-th on its way, without a branch: past the end it is the last one's.
+  __device__ __forceinline__ Key at(int i) const {
+    const uint32_t j = span.key(i < i1 ? i : i1 - 1);
+    Key k;
+    k.e = (uint32_t)(((uint64_t)j * a.entry_magic) >> a.entry_shift);  // j / entry
+    k.rest = j - k.e * (uint32_t)a.entry;
+    k.page = table[k.e];
+    k.seen = i < i1 && (!one || visible(a, p, (int)j));
+    return k;
+  }
+  // Its slot; 0 for no key, of which `there` then has no bit.
+  __device__ __forceinline__ uint32_t slot(const Key& k, uint64_t* there) {
+    const bool ok = k.page >= 0 && k.page < a.entries;
+    bad = k.seen && !ok && k.e < bad ? k.e : bad;
+    *there = __ballot(k.seen && ok);
+    return k.seen && ok ? (uint32_t)k.page * (uint32_t)a.entry + k.rest : 0u;
+  }
+  __device__ __forceinline__ void report() const {
+    if (bad != ~0u) flag(a.wrong, kWrongIndex, row + bad);
+  }
+};
+
 // The maximum over the four lanes that are 16 apart, without LDS.
 __device__ __forceinline__ float max_of_quads(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -176,30 +215,7 @@ __global__ __launch_bounds__(256, 4) void k_attend_mxfp4_few(AttendArgs a) {
   uint8_t* ssk = s_all + 2 * Stage::CODES;
   uint8_t* ssv = ssk + Stage::SCALES;
   uint8_t* st_v = s_all + kStage + wave * kFewKeys * 128;
-  // The table entry of a tile's key `lane` on its way, without a branch: past the end it is the last key's.
-  const int64_t* table = a.table + it.s * a.table_stride;
-  struct Key {
-    int64_t page;
-    uint32_t e, rest;  // place in the table's row, token inside the entry
-    bool seen;         // with one token a tile (decoding) a hidden key is none
-  };
-  auto key_of = [&](int i) {
-    const uint32_t j = span.key(i < i1 ? i : i1 - 1);
-    Key k;
-    k.e = (uint32_t)(((uint64_t)j * a.entry_magic) >> a.entry_shift);  // j / entry
-    k.rest = j - k.e * (uint32_t)a.entry;
-    k.page = table[k.e];
-    k.seen = i < i1 && (p_first != p_last || visible(a, p_first, (int)j));
-    return k;
-  };
-  // Its slot (0 for no key, of which `there` then has no bit); a bad entry is remembered for the end.
-  uint32_t bad = ~0u;
-  auto slot_in = [&](const Key& k, uint64_t* there) {
-    const bool ok = k.page >= 0 && k.page < a.entries;
-    bad = k.seen && !ok && k.e < bad ? k.e : bad;
-    *there = __ballot(k.seen && ok);
-    return k.seen && ok ? (uint32_t)k.page * (uint32_t)a.entry + k.rest : 0u;
-  };
+  FewKeys keys(a, it.s, span, i1, p_first, p_last);
   // A tile's rows on their way into LDS.  (Rows of K and V are equally long.)
   const uint32_t row_bytes = (uint32_t)a.k_row;
   const int codes = (int)mxfp4_codes((int64_t)a.kv_heads * HEADS * D);
@@ -237,19 +253,19 @@ __global__ __launch_bounds__(256, 4) void k_attend_mxfp4_few(AttendArgs a) {
   const int byte0 = hw * (D / 32) + (HEADS * D < 128 ? (hk & 1) * 2 : 0);
   uint64_t there[SL] = {}, there_next[SL] = {};
   uint32_t slot[SL];
-  Key next[SL];
+  FewKeys::Key next[SL];
   if (i0 < i1) {
 #pragma unroll
-    for (int n = 0; n < SL; n++) slot[n] = slot_in(key_of(i0 + n * 64 + lane), &there[n]);
+    for (int n = 0; n < SL; n++) slot[n] = keys.slot(keys.at(i0 + n * 64 + lane), &there[n]);
     load(slot);
 #pragma unroll
-    for (int n = 0; n < SL; n++) next[n] = key_of(i0 + G + n * 64 + lane);
+    for (int n = 0; n < SL; n++) next[n] = keys.at(i0 + G + n * 64 + lane);
   }
   for (int tile0 = i0; tile0 < i1; tile0 += G) {
     const int base = tile0 + key0;  // the wave's keys
     const bool more = tile0 + G < i1;
 #pragma unroll
-    for (int n = 0; n < SL; n++) slot[n] = more ? slot_in(next[n], &there_next[n]) : 0;
+    for (int n = 0; n < SL; n++) slot[n] = more ? keys.slot(next[n], &there_next[n]) : 0;
     lds_arrived();
     __syncthreads();
     kw_t kc[2];
@@ -274,7 +290,7 @@ __global__ __launch_bounds__(256, 4) void k_attend_mxfp4_few(AttendArgs a) {
     if (more) {
       load(slot);
 #pragma unroll
-      for (int n = 0; n < SL; n++) next[n] = key_of(tile0 + 2 * G + n * 64 + lane);
+      for (int n = 0; n < SL; n++) next[n] = keys.at(tile0 + 2 * G + n * 64 + lane);
     }
     const uint32_t here = (uint32_t)(there[SL > 1 ? key0 / 64 : 0] >> (key0 & 63));  // the wave's keys
     f32x4 st[2] = {};
@@ -343,7 +359,7 @@ __global__ __launch_bounds__(256, 4) void k_attend_mxfp4_few(AttendArgs a) {
 #pragma unroll
     for (int n = 0; n < SL; n++) there[n] = there_next[n];
   }
-  if (bad != ~0u) flag(a.wrong, kWrongIndex, it.s * a.table_stride + bad);
+  keys.report();
   __syncthreads();  // the tiles are done with
   float* s_q = reinterpret_cast<float*>(s_all) + wave * (KW > 1 ? 64 * DT * 4 : D);  // this wave's
   if (KW > 1) {  // the first wave of a head takes in the others', a lane its own places
@@ -420,6 +436,311 @@ __global__ __launch_bounds__(256, 4) void k_attend_mxfp4_few(AttendArgs a) {
         a.lse[(it.q.q0 + ta) * a.q_heads + ha] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
       }
     }
+  }
+}
+
+// A latent cache, up to 16 rows a tile: one row of 320 bytes is key and value.  A wave takes 32 keys, by itself: their
+// rows come straight into its own part of LDS, their scores leave the weights in the registers that the sums
+// take them from, for all 512 dims, and the waves meet at the split's end only.  What bounds it is the
+// conversion of every code twice, as key and as value, on two waves a SIMD.
+//
+// V needs no transposition: which dims a product's 16 rows are is free, so they are every eighth, of which a lane has
+// the eight in one dword of a key's codes; two keys' pairs of dims become two dims' pairs of keys by two byte
+// permutations.  (Through LDS as elements, as above: 64 KiB a wave and tile, 7.3 us a tile of 128 keys on two
+// workgroups a compute unit.)
+constexpr int kMxLatKeys = 4 * kFewKeys;  // of a tile of all waves
+// A wave's rows in LDS: chunks 0 to 7 and 8 to 15 of 8 keys by 128 bytes, then chunks 16 to 19 (the last codes and the
+// scales) of 16 keys by 64, each what one load brings.  Places are turned by the key, so that 16 keys' same chunk is
+// in 16 places.
+constexpr int kMxLatTail = 8192;
+constexpr int kMxLatStage = 10240;
+__device__ __forceinline__ int mx_lat_turn(int key) { return (key >> 1) & 7; }
+__device__ __forceinline__ int mx_lat_tail_turn(int key) { return (key >> 2) & 3; }
+
+template <class T, bool SPLIT_FIRST>
+__global__ __launch_bounds__(256, 2) void k_attend_mxfp4_latent_few(AttendArgs a) {
+  typedef typename T::v8 v8;
+  typedef typename T::elem elem;
+  typedef MxRows<T, kLatDim, kLatValue> Rows;
+  constexpr int R = kRowTile;
+  constexpr int DT = kLatValue / 16, KS = kLatDim / 32;
+  constexpr int G = kMxLatKeys;
+  constexpr int kQ = KS * 64 * 16, kStages = 4 * kMxLatStage, kJoin = 2 * 4 * 64 * (DT / 4) * 16;
+  __shared__ __align__(16) uint8_t s_all[kStages + kQ > kJoin ? kStages + kQ : kJoin];  // behind the loop two quarters of the four waves' sums
+  __shared__ float s_ml[4][64][2];
+  __shared__ uint32_t s_nan;
+  __shared__ int64_t s_plan[8];
+  Item it;
+  if (!find_item<true, SPLIT_FIRST>(a, R, s_plan, parts_of<kLatValue, R>(a), &it)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, quad = lane >> 4;
+  const int rows_all = it.q.m * a.group;
+  const int r0 = it.tile * R;
+  const int rows = rows_all - r0 < R ? rows_all - r0 : R;
+  // this lane's row
+  const bool live = col < rows;
+  const int r = r0 + (live ? col : 0);
+  const int tok = r / a.group, h = r - tok * a.group;
+  const int64_t row = it.q.q0 + tok;
+  const int p = it.q.kv - it.q.m + tok;
+  const int p_first = it.q.kv - it.q.m + r0 / a.group, p_last = it.q.kv - it.q.m + (r0 + rows - 1) / a.group;
+  const Span span = span_of(a, it.q.kv, p_first, p_last);
+  // this split's part of the span
+  const int part = ((span.n + it.splits - 1) / it.splits + G - 1) / G * G;
+  const int i0 = (int64_t)it.split * part < span.n ? it.split * part : span.n;
+  const int i1 = i0 + part < span.n ? i0 + part : span.n;
+  // weights are exp2(c * score - c * maximum); a negative scale turns the queries' sign
+  const float c = weight_scale(a);
+  uint8_t* sk = s_all + wave * kMxLatStage;
+  v4u* s_q = reinterpret_cast<v4u*>(s_all + kStages);
+  f32x4 o[DT] = {};
+  float m = -INFINITY, l = 0.f;
+  FewKeys keys(a, it.s, span, i1, p_first, p_last);
+  const uint32_t row_bytes = (uint32_t)a.k_row;
+  auto load = [&](uint32_t slot) {
+#pragma unroll
+    for (int n = 0; n < 4; n++) {
+      const int key = n * 8 + lane / 8;
+      const uint8_t* at = a.k_rows + (uint64_t)__shfl(slot, key) * row_bytes + ((lane & 7) ^ mx_lat_turn(key)) * 16;
+      lds_load(at, lds_offset(sk + n * 1024));
+      lds_load(at + 128, lds_offset(sk + 4096 + n * 1024));
+    }
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+      const int key = n * 16 + lane / 4;
+      lds_load(a.k_rows + (uint64_t)__shfl(slot, key) * row_bytes + 256 + ((lane & 3) ^ mx_lat_tail_turn(key)) * 16,
+               lds_offset(sk + kMxLatTail + n * 1024));
+    }
+  };
+  // K: key col (and 16 on), chunk 4 g + quad: two cases of g.  Scales 4 g + quad, and the last two blocks.
+  const uint8_t *k_at[2], *v_at[2][2];
+  for (int g = 0; g < 2; g++)
+    k_at[g] = sk + col / 8 * 1024 + col % 8 * 128 + ((g * 4 + quad) ^ mx_lat_turn(col)) * 16;
+  const uint8_t* tail = sk + kMxLatTail + col * 64;
+  const uint8_t* k_tail = tail + ((quad / 2) ^ mx_lat_tail_turn(col)) * 16 + (quad & 1) * 8;
+  const uint8_t* k_scale = tail + (2 ^ mx_lat_tail_turn(col)) * 16 + quad;
+  const uint8_t* k_last = tail + (3 ^ mx_lat_tail_turn(col)) * 16 + quad / 2;
+  // V: keys 4 quad + r (and 16 on), chunk 4 g + col / 4, dword col % 4: two cases of g, two of r.
+  for (int g = 0; g < 2; g++)
+    for (int u = 0; u < 2; u++)
+      v_at[g][u] = sk + quad / 2 * 1024 + (quad & 1) * 512 + u * 256 +
+                   ((g * 4 + col / 4) ^ mx_lat_turn(quad * 4 + u * 2)) * 16 + (col & 3) * 4;
+  const uint8_t* v_scale = sk + kMxLatTail + quad * 256 + (2 ^ quad) * 16 + col / 4;
+  int base = i0 + wave * kFewKeys;  // keys of lanes 0 to 31, and of 32 to 63 again
+  uint64_t there = 0;
+  FewKeys::Key next = {};
+  FewKeys::Key first = {};
+  if (base < i1) first = keys.at(base + (lane & 31));
+  // Queries as the products take them, a wave every fourth: of the first 16 blocks a lane has 32 dims of one in four
+  // products, of the last two 16 dims in two.  On their way before the rows, and waited for behind.
+  v4u q_in[(KS + 3) / 4];
+  {
+    const v4u* qp = reinterpret_cast<const v4u*>(a.q + 2 * (row * a.q_stride[0] + h * a.q_stride[1]));
+#pragma unroll
+    for (int n = 0; n < (KS + 3) / 4; n++) {
+      const int i = n * 4 + wave < KS ? n * 4 + wave : KS - 1;
+      q_in[n] = qp[i < 16 ? (i / 4 * 4 + quad) * 4 + i % 4 : 64 + quad * 2 + i - 16];
+    }
+  }
+  if (base < i1) {
+    load(keys.slot(first, &there));
+    if (base + G < i1) next = keys.at(base + G + (lane & 31));
+  }
+  {
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int n = 0; n < (KS + 3) / 4; n++)
+      if (n * 4 + wave < KS) s_q[(n * 4 + wave) * 64 + lane] = live ? q_in[n] ^ flip : v4u{0, 0, 0, 0};
+  }
+  __syncthreads();  // the queries are in LDS
+  for (; base < i1; base += G) {
+    const bool more = base + G < i1;
+    lds_arrived();
+    __builtin_amdgcn_wave_barrier();
+    f32x4 st[2] = {};
+#pragma unroll
+    for (int g = 0; g < 5; g++) {
+      v4u kc[2];
+      float ks[2];
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        if (g < 4) {
+          kc[t] = *reinterpret_cast<const v4u*>(k_at[g & 1] + g / 2 * 4096 + t * 2048);
+          ks[t] = mx_scale(k_scale[t * 1024 + g * 4]);
+        } else {
+          typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+          const u2 y = *reinterpret_cast<const u2*>(k_tail + t * 1024);
+          kc[t] = v4u{y[0], y[1], 0, 0};
+          ks[t] = mx_scale(k_last[t * 1024]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < (g < 4 ? 4 : 2); i++) {
+        const v8 q = __builtin_bit_cast(v8, s_q[(g * 4 + i) * 64 + lane]);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+          st[t] = T::mfma16(__builtin_bit_cast(v8, mx_decode<kIsBf16<T>>(kc[t][i], ks[t])), q, st[t]);
+      }
+    }
+    const uint32_t here = (uint32_t)there;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) x[e] = st[e / 4][e % 4];
+    // hidden keys: past the end, bad entries, and those that this row does not see
+    const bool whole = here == ~0u && (!a.causal || (span.key(base + kFewKeys - 1) <= p_first &&
+                                                     (a.window == 0 || p_last - span.key(base) < a.window)));
+    if (!whole) {
+      const uint32_t see = (uint32_t)sees(a, span, here, p, base) >> (quad * 4);
+#pragma unroll
+      for (int e = 0; e < 8; e++) x[e] = (see >> (e / 4 * 16 + e % 4)) & 1 ? x[e] : -INFINITY;
+    }
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; e++) top = fmaxf(top, x[e]);
+    top = max_of_quads(top);
+    if (__any((top - m) * c > kGrow || (m == -INFINITY && top != -INFINITY))) {
+      const float grown = fmaxf(m, top);
+      const float keep = grown == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - grown) * c);
+      m = grown;
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < DT; d++) o[d] *= keep;
+    }
+    const float zero = m == -INFINITY ? 0.f : m * c;
+    f32x8 w;
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -zero));
+      sum += w[e];
+    }
+    l += sum;  // this lane's keys; the quads are summed at the end
+    const v8 wt = __builtin_convertvector(w, v8);  // the weight's one rounding, as the product's operand
+    // four of a lane's keys at a time: 4 quad + r, and 16 on
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      uint32_t vc[8];
+      float vs[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        vc[e] = *reinterpret_cast<const uint32_t*>(v_at[g & 1][e % 4 / 2] + g / 2 * 4096 + e / 4 * 2048 + e % 2 * 128);
+        vs[e] = mx_scale(v_scale[e / 4 * 1024 + e % 4 * 64 + g * 4]);
+      }
+      if (here != ~0u) {  // what was fetched in place of no key must not reach the product: its value is zero
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const bool some = (here >> (e / 4 * 16 + quad * 4 + e % 4)) & 1;
+          vc[e] = some ? vc[e] : 0u;
+          vs[e] = some ? vs[e] : 1.f;
+        }
+      }
+      v4u d[8];  // a key's eight dims
+#pragma unroll
+      for (int e = 0; e < 8; e++) d[e] = mx_decode<kIsBf16<T>>(vc[e], vs[e]);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        v4u even, odd;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          even[e] = __builtin_amdgcn_perm(d[2 * e + 1][i], d[2 * e][i], 0x05040100u);
+          odd[e] = __builtin_amdgcn_perm(d[2 * e + 1][i], d[2 * e][i], 0x07060302u);
+        }
+        o[g * 8 + 2 * i] = T::mfma16(__builtin_bit_cast(v8, even), wt, o[g * 8 + 2 * i]);
+        o[g * 8 + 2 * i + 1] = T::mfma16(__builtin_bit_cast(v8, odd), wt, o[g * 8 + 2 * i + 1]);
+      }
+    }
+    if (more) {
+      load(keys.slot(next, &there));
+      if (base + 2 * G < i1) next = keys.at(base + 2 * G + (lane & 31));
+    }
+  }
+  keys.report();
+  // The waves' sums are joined by quarters of the dims, one a wave, two at a time in LDS.
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  s_ml[wave][lane][0] = m;
+  s_ml[wave][lane][1] = l;
+  if (threadIdx.x == 0) s_nan = 0;
+  __syncthreads();  // the tiles are done with
+  float f[4], m_all = -INFINITY, l_all = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; w++) m_all = fmaxf(m_all, s_ml[w][lane][0]);
+#pragma unroll
+  for (int w = 0; w < 4; w++) {
+    f[w] = __builtin_amdgcn_exp2f((s_ml[w][lane][0] - (m_all == -INFINITY ? 0.f : m_all)) * c);
+    l_all += s_ml[w][lane][1] * f[w];
+  }
+  f32x4* so = reinterpret_cast<f32x4*>(s_all);
+  f32x4 acc[DT / 4];
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    if (half) __syncthreads();
+#pragma unroll
+    for (int d = 0; d < DT / 2; d++) so[(wave * (DT / 2) + d) * 64 + lane] = o[half * (DT / 2) + d];
+    __syncthreads();
+    if (wave / 2 == half) {
+#pragma unroll
+      for (int d = 0; d < DT / 4; d++) {
+        acc[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < 4; w++) acc[d] += so[(w * (DT / 2) + (wave & 1) * (DT / 4) + d) * 64 + lane] * f[w];
+      }
+    }
+  }
+  bool nan = false;
+#pragma unroll
+  for (int d = 0; d < DT / 4; d++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) nan |= acc[d][e] != acc[d][e];
+  uint64_t bits = __ballot(nan && live && l_all == l_all);
+  bits |= bits >> 32;
+  bits = (bits | bits >> 16) & 0xffff;
+  if (lane == 0 && bits) atomicOr(&s_nan, (uint32_t)bits);
+  __syncthreads();
+  uint32_t again = s_nan;
+  const float log2_max = m_all == -INFINITY ? -INFINITY : m_all * c;  // of the weights, in the joining kernel's unit
+  float* part_o = a.work + it.index * partial_floats<kLatValue>(R);
+  float* part_ml = part_o + R * kLatValue;
+  auto finish = [&](int y, int64_t row_y, int head, float mm, float ll) {
+    if (it.splits > 1) {
+      part_ml[y * 2] = mm;
+      part_ml[y * 2 + 1] = ll;
+    } else if (a.lse) {
+      a.lse[row_y * a.q_heads + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    }
+  };
+  if (live && !((again >> col) & 1)) {
+    const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+    elem* op = reinterpret_cast<elem*>(a.out) + row * a.out_stride[0] + h * a.out_stride[1];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const int dim = wave * 128 + quad * 32 + e * 8;
+      f32x8 y;
+#pragma unroll
+      for (int d = 0; d < 8; d++) y[d] = acc[d][e];
+      if (it.splits > 1)
+        *reinterpret_cast<f32x8*>(part_o + col * kLatValue + dim) = y;
+      else
+        *reinterpret_cast<v8*>(op + dim) = __builtin_convertvector(y * inv, v8);
+    }
+    if (wave == 0 && quad == 0) finish(col, row, h, log2_max, l_all);
+  }
+  // rows that came out NaN, shared out over the waves
+  float* s_row = reinterpret_cast<float*>(s_all) + wave * kLatDim;
+  while (again) {
+    const int y = __builtin_ctz(again);
+    again &= again - 1;
+    if ((y & 3) != wave) continue;
+    const int ta = (r0 + y) / a.group, ha = r0 + y - ta * a.group;
+    float oo[kLatValue / 64], mm, ll;
+    exact_row<T, kLatDim, kLatValue, Rows>(a, it.s, it.q.q0 + ta, ha, it.q.kv - it.q.m + ta, span, i0, i1, s_row, oo, &mm,
+                                           &ll);
+    elem* oa = reinterpret_cast<elem*>(a.out) + (it.q.q0 + ta) * a.out_stride[0] + ha * a.out_stride[1];
+    for (int x = 0; x < kLatValue / 64; x++) {
+      if (it.splits > 1) part_o[y * kLatValue + x * 64 + lane] = oo[x];
+      else oa[x * 64 + lane] = (elem)(ll == 0.f ? 0.f : oo[x] / ll);
+    }
+    if (lane == 0) finish(y, it.q.q0 + ta, ha, mm, ll);
   }
 }
 
@@ -606,7 +927,7 @@ struct MxLatent {
 
 int tile_rows(const AttendArgs& a, int32_t head_dim) {
   const int64_t rows = a.max_q * a.group;
-  if (head_dim == kLatDim) return rows <= 16 ? 16 : rows <= 32 ? 32 : kLatRows;
+  if (head_dim == kLatDim) return rows <= 2 * kRowTile ? kRowTile : kLatRows;
   return rows <= 2 * kRowTile ? kRowTile : kTileRows;
 }
 
@@ -619,10 +940,13 @@ int heads_of(const AttendArgs& a) { return a.kv_heads % 4 == 0 ? 4 : a.kv_heads 
 // 14.0 us for 13.0) and no more than 128 of them (of 32768 keys: 64 splits 33 us, 128 24, 512 57).  And joined: where
 // there are few rows a workgroup a row, else a wave, for whose 64 sequences empty workgroups cost more (6.6 us
 // for 9.8; one of 32768 33 for 5).
-constexpr int kFewPerCu = 4, kFewLeast = 32, kFewSplits = 128, kFewAlone = 512;
+// A latent cache: two workgroups a compute unit and tiles of 128 keys (32 sequences up to 6000 of 16 heads 35 us; one
+// workgroup 38, four 50; 128 sequences 81, 79 and 90).
+constexpr int kFewPerCu = 4, kFewLeast = 32, kFewSplits = 128, kFewAlone = 512, kMxLatPerCu = 2;
 Plan few_plan(AttendArgs* a, int32_t head_dim, int heads, int32_t num_cus, bool* alone = nullptr) {
-  const int least = (int)(a->max_kv / kFewSplits);
-  Plan p = plan(a, kRowTile, head_dim, num_cus, heads, kFewPerCu, least > kFewLeast ? least : kFewLeast);
+  const bool latent = head_dim == kLatDim;
+  const int most = (int)(a->max_kv / kFewSplits), tile = latent ? kMxLatKeys : kFewLeast;
+  Plan p = plan(a, kRowTile, head_dim, num_cus, heads, latent ? kMxLatPerCu : kFewPerCu, most > tile ? most : tile);
   const bool row = a->q_rows * a->q_heads <= kFewAlone;
   if (alone) *alone = row;
   if (p.joins > 0 && !row) {
@@ -650,10 +974,12 @@ hipError_t launch_heads(const AttendArgs& a, int32_t num_cus, hipStream_t stream
          : heads == 2 ? launch_few<T, D, 2>(a, num_cus, stream)
                       : launch_few<T, D, 1>(a, num_cus, stream);
 }
-template <class T, int RB>
-hipError_t launch_latent_few(const AttendArgs& a, int32_t num_cus, hipStream_t stream) {
-  return launch_split<T, kLatValue, 16 * RB>({k_attend_latent_few<T, RB, MxLatent<T>, false>,
-                                              k_attend_latent_few<T, RB, MxLatent<T>, true>}, a, num_cus, stream);
+template <class T>
+hipError_t launch_latent_few(AttendArgs a, int32_t num_cus, hipStream_t stream) {
+  bool alone;
+  const Plan p = few_plan(&a, kLatDim, 1, num_cus, &alone);
+  return launch_planned({k_attend_mxfp4_latent_few<T, false>, k_attend_mxfp4_latent_few<T, true>},
+                        alone ? k_attend_mxfp4_join<T, kLatValue, 1, 4> : k_attend_mxfp4_join<T, kLatValue, 1, 1>, a, p, stream);
 }
 
 template <class T>
@@ -662,9 +988,8 @@ hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hi
   if (head_dim == 64) return launch_heads<T, 64>(a, num_cus, stream);
   if (head_dim == 128) return launch_heads<T, 128>(a, num_cus, stream);
   const int R = tile_rows(a, head_dim);
-  return R == 16   ? launch_latent_few<T, 1>(a, num_cus, stream)
-         : R == 32 ? launch_latent_few<T, 2>(a, num_cus, stream)
-                   : launch_split<T, kLatValue, kLatRows>(
+  return R == kRowTile ? launch_latent_few<T>(a, num_cus, stream)
+         : launch_split<T, kLatValue, kLatRows>(
                          {k_attend_latent<T, MxLatent<T>, false>, k_attend_latent<T, MxLatent<T>, true>}, a, num_cus,
                          stream);
 }
@@ -674,8 +999,8 @@ hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hi
 int64_t attend_mxfp4_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_cus) {
   if (args.q_rows <= 0 || args.num_seqs <= 0) return 0;
   const int R = tile_rows(args, head_dim);
-  const bool few = head_dim != kLatDim && R == kRowTile;
-  const int heads = few ? heads_of(args) : 1;
+  const bool few = R == kRowTile;
+  const int heads = few && head_dim != kLatDim ? heads_of(args) : 1;
   AttendArgs a = args;
   a.kv_heads /= heads;
   const Plan p = few ? few_plan(&a, head_dim, heads, num_cus) : plan(&a, R, head_dim, num_cus);
