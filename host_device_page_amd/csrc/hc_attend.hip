@@ -321,6 +321,7 @@ struct ElementTiles {
       lds_load(vl + at, lds_offset(v + (x * W + wave) * 1024));
     }
   }
+  __device__ __forceinline__ void step(int, const uint8_t*, const uint8_t*) {}
   __device__ __forceinline__ void arrive(bool, const uint8_t*, const uint8_t*) { lds_arrived(); }
   static __device__ __forceinline__ int k_place(int row, int chunk) { return tile_k_place<D>(row, chunk); }
   static __device__ __forceinline__ int v_place(int row, int chunk) { return tile_v_place<D>(row, chunk); }
@@ -357,6 +358,7 @@ struct ElementLatent {
   static constexpr bool kZeros = false;
   __device__ __forceinline__ explicit ElementLatent(const AttendArgs&) {}
   __device__ __forceinline__ void load(const AttendArgs& a, uint32_t slot, const uint8_t* to) { latent_load(a, slot, to); }
+  __device__ __forceinline__ void step(int, const uint8_t*) {}
   __device__ __forceinline__ void arrive(bool, const uint8_t*) { lds_arrived(); }
 };
 

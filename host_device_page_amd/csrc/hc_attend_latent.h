@@ -70,7 +70,8 @@ __device__ __forceinline__ bool latent_item(const AttendArgs& a, int64_t* s_plan
 
 // Source, in the kernels below: how a tile of keys gets into LDS.
 //   load(a, slot, to)    starts on the tile whose key `lane` is in `slot`, into LDS `to`
-//   arrive(more, to)     after the products over the tile before: what load started (more: it did) is in LDS
+//   step(s, to)          beside the s-th of the four products of weights and values of many rows: may put a part there
+//   arrive(first, to)    what load started is in LDS, behind the four steps but for the first tile
 //   kZeros               keys that are not there arrive as zeros
 //   Rows                 one row of the cache, for exact_row
 
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
   uint32_t slot = slot_from(a, t.entry(a, t.i0));
   Source source(a);
   if (t.i0 < t.i1) source.load(a, slot, s_k);
-  source.arrive(t.i0 < t.i1, s_k);
+  source.arrive(true, s_k);
   if (threadIdx.x == 0) s_nan[0] = 0;
   __syncthreads();
   int off = 0;
@@ -269,7 +270,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent_few(AttendArgs a) {
         }
       }
       off = kLatTile - off;
-      source.arrive(base + kLatKeys < t.i1, s_k + off);
+      source.arrive(false, s_k + off);
       __syncthreads();
       base += kLatKeys;
       if (base >= t.i1) break;
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
   uint32_t slot = slot_from(a, t.entry(a, t.i0));
   Source source(a);
   if (t.i0 < t.i1) source.load(a, slot, s_k);
-  source.arrive(t.i0 < t.i1, s_k);
+  source.arrive(true, s_k);
   if (threadIdx.x < 2) s_nan[threadIdx.x] = 0;
   __syncthreads();
   int off = 0;
@@ -467,6 +468,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
 #pragma unroll
       for (int s = 0; s < 4; s++) {
         if (s < 3) fetch(s + 1, (s + 1) & 1);
+        source.step(s, s_k + (kLatTile - off));
 #pragma unroll
         for (int d = 0; d < DT; d++) {
           o[0][d] = T::mfma32(vf[s & 1][d], w[s & 1][0], o[0][d]);
@@ -475,7 +477,7 @@ __global__ __launch_bounds__(256, 1) void k_attend_latent(AttendArgs a) {
         __builtin_amdgcn_sched_barrier(0);
       }
       off = kLatTile - off;
-      source.arrive(base + kLatKeys < t.i1, s_k + off);
+      source.arrive(false, s_k + off);
       __syncthreads();
       base += kLatKeys;
       if (base >= t.i1) break;

@@ -814,7 +814,7 @@ __global__ __launch_bounds__(256) void k_attend_mxfp4_join(AttendArgs a) {
 
 // ---------------------------------------------------------------- tiles of 4-bit rows, as elements into LDS
 // A tile's codes wait in registers while the tile before is computed, 16 bytes and a scale for a
-// block of 32 elements, and are written to LDS as elements behind its products, by one wave for all four.
+// block of 32 elements, and are written to LDS as elements beside its second product, by one wave for all four.
 // 16 lanes next to each other write all banks.
 template <class T, int D>
 struct MxTiles {
@@ -824,8 +824,8 @@ struct MxTiles {
   const uint8_t *codes_at[N], *scales_at[N];
   int key, block;
   bool is_v;  // N == 1
-  v4u codes[N];
-  uint32_t scales[N];
+  v4u codes[N] = {};
+  uint32_t scales[N] = {};
   __device__ __forceinline__ MxTiles(const AttendArgs& a, int hk) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t scales0 = mxfp4_codes((int64_t)a.kv_heads * D);
@@ -856,17 +856,20 @@ struct MxTiles {
       scales[n] = sl == kNoSlot ? 127 : z;
     }
   }
-  __device__ __forceinline__ void arrive(bool more, uint8_t* k, uint8_t* v) {
-    if (!more) return;
+  // Behind the last tile the codes of the one before are written again, to LDS that is done with.
+  __device__ __forceinline__ void step(int i, uint8_t* k, uint8_t* v) {
+    const int chunk = block * 4 + i;
 #pragma unroll
-    for (int n = 0; n < N; n++)
+    for (int n = 0; n < N; n++) {
+      const v4u y = mx_decode<kIsBf16<T>>(codes[n][i], mx_scale(scales[n]));
+      if (N == 2) *reinterpret_cast<v4u*>(n ? v + v_place(key, chunk) : k + k_place(key, chunk)) = y;
+      else *reinterpret_cast<v4u*>(is_v ? v + v_place(key, chunk) : k + k_place(key, chunk)) = y;
+    }
+  }
+  __device__ __forceinline__ void arrive(bool first, uint8_t* k, uint8_t* v) {
+    if (!first) return;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const v4u y = mx_decode<kIsBf16<T>>(codes[n][i], mx_scale(scales[n]));
-        const int chunk = block * 4 + i;
-        if (N == 2) *reinterpret_cast<v4u*>(n ? v + v_place(key, chunk) : k + k_place(key, chunk)) = y;
-        else *reinterpret_cast<v4u*>(is_v ? v + v_place(key, chunk) : k + k_place(key, chunk)) = y;
-      }
+    for (int i = 0; i < 4; i++) step(i, k, v);
   }
   // Where a row's chunk lies: read, 16 rows' same chunk of K and four rows' 32 dims of V lie in different banks.
   static __device__ __forceinline__ int k_place(int row, int chunk) {
@@ -885,8 +888,8 @@ struct MxLatent {
   typedef MxRows<T, kLatDim, kLatValue> Rows;
   static constexpr bool kZeros = true;
   static constexpr int N = 5;  // rounds over the workgroup's 16 sixteens of lanes, the last of them half empty
-  v4u codes[N];
-  uint32_t scales[N];
+  v4u codes[N] = {};
+  uint32_t scales[N] = {};
   __device__ __forceinline__ explicit MxLatent(const AttendArgs&) {}
   // Pair of blocks, key and the lane's block of the pair, in round n; false: none.
   static __device__ __forceinline__ bool place(int n, int* pair, int* key, int* b) {
@@ -911,24 +914,120 @@ struct MxLatent {
       scales[n] = sl == kNoSlot ? 127 : z;
     }
   }
-  __device__ __forceinline__ void arrive(bool more, uint8_t* to) {
-    if (!more) return;
+  // (Behind the last tile as in MxTiles.)
+  __device__ __forceinline__ void round(int n, uint8_t* to) {
+    int pair, key, b;
+    if (!place(n, &pair, &key, &b)) return;
 #pragma unroll
-    for (int n = 0; n < N; n++) {
-      int pair, key, b;
-      if (!place(n, &pair, &key, &b)) continue;
+    for (int i = 0; i < 4; i++)
+      *reinterpret_cast<v4u*>(to + pair * kLatBlock + key * 128 + ((b * 4 + i) ^ lat_swizzle(key)) * 16) =
+          mx_decode<kIsBf16<T>>(codes[n][i], mx_scale(scales[n]));
+  }
+  __device__ __forceinline__ void step(int s, uint8_t* to) {
+    round(s, to);
+    if (s == 3) round(4, to);
+  }
+  __device__ __forceinline__ void arrive(bool first, uint8_t* to) {
+    if (!first) return;
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        *reinterpret_cast<v4u*>(to + pair * kLatBlock + key * 128 + ((b * 4 + i) ^ lat_swizzle(key)) * 16) =
-            mx_decode<kIsBf16<T>>(codes[n][i], mx_scale(scales[n]));
-    }
+    for (int s = 0; s < 4; s++) step(s, to);
   }
 };
 
+// ---------------------------------------------------------------- many rows of a latent cache: its tokens as elements first
+// Every row tile of a sequence converts all keys that it sees, beside products that one wave a SIMD leaves waiting.
+// Where a sequence has many tiles and the call's tokens as elements are not many bytes, they are converted once, by a launch of
+// their own, into the workspace, with a table that says where, and the kernels over elements do the rest.  (A
+// bad entry, or bad lengths, are reported here; what those kernels report of this table goes to words that
+// nobody reads.)
+//
+// Measured, converted in the kernel and first: four sequences of 8000 tokens and 16 heads with 8 new tokens each 50 and
+// 57 us, 16 64 and 67, 32 97 and 89, 64 179 and 144, 128 467 and 341; a chunk of 512 behind 3988 with 32 heads 281 and
+// 226.  (K and V of heads of 128: 512 new tokens each 322 and 330, a chunk of 2048 behind 14336 612 and 590 for 67 MB of
+// workspace; not done.)
+constexpr int kExpandTokens = 16;                       // of a workgroup
+constexpr int64_t kExpandRows = 8 * kLatRows;           // of a sequence, at least
+constexpr int64_t kExpandBytes = (int64_t)256 << 20;    // of the workspace, at most
+
+// The workspace: words for reports, the rows, the table, then what the attention needs.
+struct Expand {
+  int64_t tokens, table_at, work_at;
+};
+Expand expand_of(const AttendArgs& a) {
+  Expand e;
+  e.tokens = a.num_seqs * a.max_kv;
+  e.table_at = 256 + e.tokens * kLatDim * 2;
+  e.work_at = (e.table_at + e.tokens * 8 + 255) / 256 * 256;
+  return e;
+}
+bool expands(const AttendArgs& a, int32_t head_dim) {
+  return head_dim == kLatDim && a.max_kv > 0 && a.max_q * a.group >= kExpandRows &&
+         a.num_seqs <= kExpandBytes / (kLatDim * 2 + 8) / a.max_kv;
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_expand_latent(AttendArgs a, Expand e) {
+  __shared__ uint32_t s_slot[kExpandTokens];
+  const int64_t per = (a.max_kv + kExpandTokens - 1) / kExpandTokens, s = blockIdx.x / per;
+  const int j0 = (int)(blockIdx.x - s * per) * kExpandTokens;
+  const Seq q = sequence(a, s);
+  if (!q.ok && j0 == 0 && threadIdx.x == 0) flag(a.wrong, kWrongLengths, s);
+  if (q.m == 0 || j0 >= q.kv) return;
+  const Span span = span_of(a, q.kv, q.kv - q.m, q.kv - 1);  // of all the sequence's rows: nothing else is read
+  const int64_t row0 = s * a.max_kv + j0;
+  uint8_t* work = reinterpret_cast<uint8_t*>(a.work);
+  if (threadIdx.x < kExpandTokens) {
+    const int j = j0 + threadIdx.x;
+    uint32_t slot = kNoSlot;
+    if (j < span.sk || (j >= span.lo && j < span.lo + span.n - span.sk)) slot = slot_of(a, s, (uint32_t)j);
+    s_slot[threadIdx.x] = slot;
+    if (j < q.kv) reinterpret_cast<int64_t*>(work + e.table_at)[row0 + threadIdx.x] = slot == kNoSlot ? -1 : row0 + threadIdx.x;
+  }
+  __syncthreads();
+  constexpr int kVecs = kLatDim / 8;
+  for (int i = threadIdx.x; i < kExpandTokens * kVecs; i += 256) {
+    const int t = i / kVecs, w = i - t * kVecs;
+    if (s_slot[t] == kNoSlot) continue;
+    const uint8_t* row = a.k_rows + (uint64_t)s_slot[t] * a.k_row;
+    const uint32_t codes = reinterpret_cast<const uint32_t*>(row)[w];
+    const float scale = mx_scale(row[mxfp4_codes(kLatDim) + w / 4]);
+    reinterpret_cast<v4u*>(work + 256 + (row0 + t) * kLatDim * 2)[w] = mx_decode<BF16>(codes, scale);
+  }
+}
+
+// The call over the elements.
+AttendArgs expanded(const AttendArgs& args, const Expand& e) {
+  AttendArgs a = args;
+  uint8_t* w = reinterpret_cast<uint8_t*>(a.work);
+  a.wrong = reinterpret_cast<WrongWord*>(w);
+  a.k_rows = a.v_rows = w + 256;
+  a.k_row = a.v_row = kLatDim;
+  a.table = reinterpret_cast<const int64_t*>(w + e.table_at);
+  a.table_width = a.table_stride = a.max_kv;
+  a.entry = 1;  // slots
+  a.entry_shift = 31;
+  a.entry_magic = 1u << 31;
+  a.entries = e.tokens;
+  a.work = reinterpret_cast<float*>(w + e.work_at);
+  return a;
+}
+
+hipError_t launch_expanded(const AttendArgs& a, int32_t dtype, int32_t num_cus, hipStream_t stream) {
+  const Expand e = expand_of(a);
+  const int64_t groups = a.num_seqs * ((a.max_kv + kExpandTokens - 1) / kExpandTokens);
+  (void)hipGetLastError();
+  (dtype == HC_BF16 ? k_expand_latent<true> : k_expand_latent<false>)<<<dim3((unsigned)groups), 256, 0, stream>>>(a, e);
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess ? err : launch_attend(expanded(a, e), dtype, kLatDim, num_cus, stream);
+}
+
+// The kernel for a call: the rows of its row tiles.  64 sequences up to 8192 tokens, 32/8 heads of 128, with several
+// new tokens each, in tiles of 16 and of 128 rows: 20 rows of a KV head 96 and 312 us, 32 rows 127 and 315, 48 rows 165
+// and 317, 64 rows 195 and 325; 32 sequences up to 6000 tokens of a latent cache, in tiles of 16 and of 64 rows: 20 rows
+// 32.0 and 49.2 us, 32 rows 36.3 and 51.4, 64 rows 48.8 and 58.4, 128 rows 110.6 and 102.1.
 int tile_rows(const AttendArgs& a, int32_t head_dim) {
   const int64_t rows = a.max_q * a.group;
-  if (head_dim == kLatDim) return rows <= 2 * kRowTile ? kRowTile : kLatRows;
-  return rows <= 2 * kRowTile ? kRowTile : kTileRows;
+  return rows <= 4 * kRowTile ? kRowTile : head_dim == kLatDim ? kLatRows : kTileRows;
 }
 
 // KV heads of an item of few rows: as many as divide the heads, up to the waves.  (Eight, with eight waves: 64
@@ -999,6 +1098,10 @@ hipError_t launch_for(const AttendArgs& a, int32_t head_dim, int32_t num_cus, hi
 int64_t attend_mxfp4_workspace(const AttendArgs& args, int32_t head_dim, int32_t num_cus) {
   if (args.q_rows <= 0 || args.num_seqs <= 0) return 0;
   const int R = tile_rows(args, head_dim);
+  if (expands(args, head_dim)) {
+    const Expand e = expand_of(args);
+    return e.work_at + attend_workspace(expanded(args, e), head_dim, num_cus);
+  }
   const bool few = R == kRowTile;
   const int heads = few && head_dim != kLatDim ? heads_of(args) : 1;
   AttendArgs a = args;
@@ -1013,6 +1116,7 @@ int64_t attend_mxfp4_workspace(const AttendArgs& args, int32_t head_dim, int32_t
 
 hipError_t launch_attend_mxfp4(const AttendArgs& a, int32_t dtype, int32_t head_dim, int32_t num_cus, hipStream_t stream) {
   if (a.q_rows <= 0 || a.num_seqs <= 0) return hipSuccess;
+  if (expands(a, head_dim)) return launch_expanded(a, dtype, num_cus, stream);
   return dtype == HC_BF16 ? launch_for<Bf16>(a, head_dim, num_cus, stream) : launch_for<F16>(a, head_dim, num_cus, stream);
 }
 

@@ -26,7 +26,8 @@ constexpr int kTileKeys = 64;
 
 // Source: how a tile of keys and values gets into LDS, and where their 16-byte chunks lie there.
 //   load(a, slot, k, v)    starts on the tile whose key `lane` is in `slot`, into LDS k and v
-//   arrive(more, k, v)     after the products over the tile before: what load started (more: it did) is in LDS
+//   step(s, k, v)          beside the s-th of the four products of weights and values: may put a part of it there
+//   arrive(first, k, v)    what load started is in LDS, behind the four steps but for the first tile
 //   kZeros                 values of keys that are not there arrive as zeros
 //   Rows                   one row of the cache, for exact_row
 template <class T, int D, class Source, bool SPLIT_FIRST>
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
   Entry next_entry = entry(i0 + kTileKeys);
   uint32_t slot = slot_from(a, entry(i0));
   if (i0 < i1) source.load(a, slot, s_k[0], s_v[0]);
-  source.arrive(i0 < i1, s_k[0], s_v[0]);
+  source.arrive(true, s_k[0], s_v[0]);
   __syncthreads();
   int buf = 0;
   for (int base = i0; base < i1; base += kTileKeys) {
@@ -142,6 +143,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 4; s++) {
+      source.step(s, s_k[buf ^ 1], s_v[buf ^ 1]);
       f32x8 w;
 #pragma unroll
       for (int e = 0; e < 8; e++) w[e] = x[s * 8 + e];
@@ -162,7 +164,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
     }
     __builtin_amdgcn_s_setprio(0);
     buf ^= 1;
-    source.arrive(base + kTileKeys < i1, s_k[buf], s_v[buf]);
+    source.arrive(false, s_k[buf], s_v[buf]);
     __syncthreads();
   }
   l += __shfl_xor(l, 32);
