@@ -144,10 +144,15 @@ __device__ __forceinline__ uint32_t slot_of(const AttendArgs& a, int64_t s, uint
 // registers.  Nothing waits for it but lds_arrived, of the wave that loaded.
 // (m0 is reserved, which the compiler remarks on: it keeps no values of its own there, but what it puts there for an
 // instruction has to be put there again behind this.)
+// OFFSET: bytes on from there, in memory and in LDS (the instruction adds its offset to both addresses).
 #pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void lds_load(const uint8_t* from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory", "m0");
+template <int OFFSET>
+__device__ __forceinline__ void lds_load_at(const uint8_t* from, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds), "v"(from),
+               "n"(OFFSET)
+               : "memory", "m0");
 }
+__device__ __forceinline__ void lds_load(const uint8_t* from, uint32_t lds) { lds_load_at<0>(from, lds); }
 __device__ __forceinline__ void lds_arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);

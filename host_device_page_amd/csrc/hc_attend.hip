@@ -301,16 +301,12 @@ struct ElementTiles {
   // one in every instruction.  Rows of K and V are equally far apart, so a key's lane works out where its
   // rows are once and the lanes that fetch them only add their own part.
   static constexpr int RL = 64 / CH;  // rows of an instruction
-  int wave, from;                     // a lane's first row, the next W RL on
-  const uint8_t *kl, *vl;
-  __device__ __forceinline__ ElementTiles(const AttendArgs& a, int hk) {
-    const int lane = threadIdx.x & 63;
-    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    from = wave * RL + lane / CH;
-    kl = a.k_rows + 2 * (int64_t)hk * D + k_chunk<D>(from, lane % CH) * 16;
-    vl = a.v_rows + 2 * (int64_t)hk * D + v_chunk<D>(from, lane % CH) * 16;
-  }
-  __device__ __forceinline__ void load(const AttendArgs& a, uint32_t slot, const uint8_t* k, const uint8_t* v) {
+  const int wave, from;               // a lane's first row, the next W RL on
+  const uint8_t *const kl, *const vl;
+  __device__ __forceinline__ ElementTiles(const AttendArgs& a, int hk, int lane, int w)
+      : wave(w), from(w * RL + lane / CH), kl(a.k_rows + 2 * (int64_t)hk * D + k_chunk<D>(from, lane % CH) * 16),
+        vl(a.v_rows + 2 * (int64_t)hk * D + v_chunk<D>(from, lane % CH) * 16) {}
+  __device__ __forceinline__ void load(const AttendArgs& a, uint32_t slot, const uint8_t* k, const uint8_t* v) const {
     const uint64_t row = slot == kNoSlot ? 0 : (uint64_t)slot * (2 * a.k_row);
     const uint32_t lo = (uint32_t)row, hi = (uint32_t)(row >> 32);
 #pragma unroll
@@ -328,14 +324,6 @@ struct ElementTiles {
 };
 
 // 64 keys of a latent cache.
-// 16 bytes a lane from memory into LDS, lane i to lds + 16 i (lds the same in all lanes), past the
-// registers, from OFFSET bytes on in memory (the instruction adds its offset to both addresses).
-template <int OFFSET>
-__device__ __forceinline__ void lds_load_at(const uint8_t* from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" ::"s"(lds), "v"(from),
-               "n"(OFFSET)
-               : "memory", "m0");
-}
 template <int... B>
 __device__ __forceinline__ void latent_load_key(const uint8_t* from, uint32_t lds, std::integer_sequence<int, B...>) {
   (lds_load_at<B * 128>(from, lds + B * (kLatBlock - 128)), ...);

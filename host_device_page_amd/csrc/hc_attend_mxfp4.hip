@@ -457,6 +457,9 @@ constexpr int kMxLatStage = 10240;
 __device__ __forceinline__ int mx_lat_turn(int key) { return (key >> 1) & 7; }
 __device__ __forceinline__ int mx_lat_tail_turn(int key) { return (key >> 2) & 3; }
 
+// Waits for this wave's reads of LDS, which a load into it does not.
+__device__ __forceinline__ void lds_read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 template <class T, bool SPLIT_FIRST>
 __global__ __launch_bounds__(256, 2) void k_attend_mxfp4_latent_few(AttendArgs a) {
   typedef typename T::v8 v8;
@@ -650,7 +653,9 @@ __global__ __launch_bounds__(256, 2) void k_attend_mxfp4_latent_few(AttendArgs a
       }
     }
     if (more) {
-      load(keys.slot(next, &there));
+      const uint32_t slot = keys.slot(next, &there);
+      lds_read();  // the tile's codes are in registers: the next one's may come
+      load(slot);
       if (base + 2 * G < i1) next = keys.at(base + 2 * G + (lane & 31));
     }
   }
@@ -826,8 +831,7 @@ struct MxTiles {
   bool is_v;  // N == 1
   v4u codes[N] = {};
   uint32_t scales[N] = {};
-  __device__ __forceinline__ MxTiles(const AttendArgs& a, int hk) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __device__ __forceinline__ MxTiles(const AttendArgs& a, int hk, int lane, int wave) {
     const int64_t scales0 = mxfp4_codes((int64_t)a.kv_heads * D);
     if (D == 128) {
       key = wave * 16 + ((lane >> 2) & 3) * 4 + (lane >> 4);

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256, 2) void k_attend_tiles(AttendArgs a) {
     if (i < i1) e = entry_of(a, it.s, (uint32_t)span.key(i));
     return e;
   };
-  Source source(a, it.hk);
+  Source source(a, it.hk, lane, wave);
   f32x16 o[DT] = {};
   float m = -INFINITY, l = 0.f;
   Entry next_entry = entry(i0 + kTileKeys);

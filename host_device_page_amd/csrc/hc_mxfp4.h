@@ -47,15 +47,12 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
   return e < 0 ? 0 : (uint32_t)e;
 }
 
-// A double as an fp32 value between the same two 4-bit borders: cut towards zero, the lowest bit set where
-// anything was cut (no border has that bit, so it stays on its side of every one).
-__device__ __forceinline__ float mx_to_odd(double x) {
+// A double as an fp32 value between the same two 4-bit borders.  Borders (between codes, and of a block's scale) have
+// three bits; rounded to 24, a value can come to lie on one that it was next to, and is then put back.
+__device__ __forceinline__ float mx_beside(double x) {
   const float y = (float)x;
   uint32_t u = __float_as_uint(y);
-  if ((double)y != x && u << 1 < 0xff000000u) {
-    if (fabs((double)y) > fabs(x)) u -= 1;
-    u |= 1;
-  }
+  if ((u & 0x1fffffu) == 0 && (double)y != x && u << 1 < 0xff000000u) u += fabs((double)y) > fabs(x) ? -1 : 1;
   return __uint_as_float(u);
 }
 

@@ -595,7 +595,8 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* desc, void* stream);
 /* hc_attend over a cache held in 4 bits: the same call in every respect but the rows, whose values are taken
  * as dtype (exact where they were stored from that type; what fp16 cannot hold is infinite).  kv_heads 1 with
  * head_dim / value_dim 576 / 512 and value_in_key is a latent cache here too: its value is the
- * first 512 elements of the key row. */
+ * first 512 elements of the key row.  (Chunks of a latent cache are converted to elements in the workspace
+ * first, where num_seqs * max_kv rows of them are no more than 256 MiB.) */
 int hc_attend_mxfp4_workspace_bytes(const hc_pool* pool, const hc_attend_desc* desc, int64_t* out_bytes);
 int hc_attend_mxfp4(hc_pool* pool, const hc_attend_desc* desc, void* stream);
 
