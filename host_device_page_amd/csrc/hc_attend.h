@@ -510,9 +510,11 @@ struct Plan {
 };
 // Kernels with a rule of their own say the workgroups of a compute unit (per_cu) and the least keys of a split, and
 // of how many KV heads an item is (heads; a->kv_heads then counts items of a tile).  Few tiles' list should be one round
-// of workgroups, tiles included; of many, two rounds, since their tiles are of unlike lengths.  (64 sequences up to 8192
-// of 4-bit rows, few tiles: a target of the whole round 100 us, less the tiles 83; 256 such sequences in one round 316,
-// two 285, three 283; 128 up to 2048 54, 56, 63.)
+// of workgroups, tiles included; of many, two rounds, since their tiles are of unlike lengths, but of a latent cache one,
+// whose partial results are long.  (4-bit rows.  64 sequences up to 8192, few tiles: a target of the whole round
+// 100 us, less the tiles 82; up to half a round of tiles for a quarter: 128 up to 2048 54 for 56.  Many, in one round and in
+// two: 256 up to 8192 317 and 285, 512 up to 2000 198 and 168, all of 1000 148 and 157; of a latent cache 512 of 500
+// 46 and 76, 128 up to 6000 68 and 76, 256 117 and 117.)
 Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus, int heads = 0, int per_cu = 0, int least = 0) {
   const bool latent = head_dim == kLatDim, few = R <= 32;
   a->min_split = least ? least : few ? 128 : 256;
@@ -520,7 +522,7 @@ Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus, int heads = 0
   // items that run at once: 8 or 2 workgroups a compute unit, and one of a latent cache, where the
   // whole list, `tiles` longer than the target at most, should be one round
   a->target = (int64_t)num_cus * (per_cu ? per_cu : few ? 8 : 2);
-  if (per_cu) a->target = p.items * 4 <= a->target ? a->target - p.items : 2 * a->target;
+  if (per_cu) a->target = 2 * p.items <= a->target ? a->target - p.items : latent ? a->target : 2 * a->target;
   if (latent && !per_cu) a->target = num_cus - p.items > num_cus / 2 ? num_cus - p.items : num_cus / 2;
   a->join_parts = 0;
   a->slots = 0;

@@ -1044,7 +1044,7 @@ int heads_of(const AttendArgs& a) { return a.kv_heads % 4 == 0 ? 4 : a.kv_heads 
 // there are few rows a workgroup a row, else a wave, for whose 64 sequences empty workgroups cost more (6.6 us
 // for 9.8; one of 32768 33 for 5).
 // A latent cache: two workgroups a compute unit and tiles of 128 keys (32 sequences up to 6000 of 16 heads 35 us; one
-// workgroup 38, four 50; 128 sequences 81, 79 and 90).
+// workgroup 38, four 50).
 constexpr int kFewPerCu = 4, kFewLeast = 32, kFewSplits = 128, kFewAlone = 512, kMxLatPerCu = 2;
 Plan few_plan(AttendArgs* a, int32_t head_dim, int heads, int32_t num_cus, bool* alone = nullptr) {
   const bool latent = head_dim == kLatDim;

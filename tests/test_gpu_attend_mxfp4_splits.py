@@ -169,3 +169,15 @@ def test_two_calls_at_once():
             c.compare(*x, want)
         c.pool.sync()
         c.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_latent_chunks_whose_bound_is_too_far_to_convert(dtype):
+    """The same rows under a bound of tokens whose elements would be too many bytes."""
+    c = Case4(kv=(90, 40), q=(35, 1), page=16, dtype=dtype, extra_width=20000, **LATENT).upload()
+    c.check(max_kv=300000)
+    near, far = c.run(), c.run(max_kv=300000)
+    torch.cuda.synchronize()
+    F.close(far[0], near[0].double().cpu(), 2 * c.want()[2], "out")
+    c.pool.sync()
+    c.close()
