@@ -245,10 +245,9 @@ __device__ __forceinline__ void exact_row(const AttendArgs& a, int64_t s, int64_
   *l_out = l;
 }
 
-// (kernels of many rows, and of a latent cache)
-// The maximum that a row's weights are relative to is replaced only when it grows by more than
-// 2^8: until then weights of up to 2^8 are summed, which loses nothing in fp32 or as operands, and the
-// sums need not be scaled.
+// In the kernels of many rows, of a latent cache and of 4-bit rows the maximum that a row's weights are relative to
+// is replaced only when it grows by more than 2^8: until then weights of up to 2^8 are summed, which loses nothing
+// in fp32 or as operands, and the sums need not be scaled.
 constexpr float kGrow = 8.f;
 
 // Rows of a row tile: of the kernels of few rows (decoding), of many, and of a latent cache's.

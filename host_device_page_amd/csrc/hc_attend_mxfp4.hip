@@ -949,7 +949,7 @@ struct MxLatent {
 // 57 us, 16 64 and 67, 32 97 and 89, 64 179 and 144, 128 467 and 341; a chunk of 512 behind 3988 with 32 heads 281 and
 // 226.  (K and V of heads of 128: 512 new tokens each 322 and 330, a chunk of 2048 behind 14336 612 and 590 for 67 MB of
 // workspace; not done.)
-constexpr int kExpandTokens = 16;                       // of a workgroup
+constexpr int kExpandTokens = 8;                       // of a workgroup
 constexpr int64_t kExpandRows = 8 * kLatRows;           // of a sequence, at least
 constexpr int64_t kExpandBytes = (int64_t)256 << 20;    // of the workspace, at most
 
@@ -1041,11 +1041,11 @@ int heads_of(const AttendArgs& a) { return a.kv_heads % 4 == 0 ? 4 : a.kv_heads 
 
 // How calls of few rows are split: four workgroups a compute unit, splits of 32 keys and more (of 64: a sequence of 1500
 // 14.0 us for 13.0) and no more than 128 of them (of 32768 keys: 64 splits 33 us, 128 24, 512 57).  And joined: where
-// there are few rows a workgroup a row, else a wave, for whose 64 sequences empty workgroups cost more (6.6 us
-// for 9.8; one of 32768 33 for 5).
+// there are few rows a workgroup a row (a sequence of 32768 24 us, by waves 35), else a wave, since empty workgroups
+// cost more then (32 sequences of 16 heads in a window 34.3 us by workgroups, 32.4 by waves).
 // A latent cache: two workgroups a compute unit and tiles of 128 keys (32 sequences up to 6000 of 16 heads 35 us; one
 // workgroup 38, four 50).
-constexpr int kFewPerCu = 4, kFewLeast = 32, kFewSplits = 128, kFewAlone = 512, kMxLatPerCu = 2;
+constexpr int kFewPerCu = 4, kFewLeast = 32, kFewSplits = 128, kFewAlone = 128, kMxLatPerCu = 2;
 Plan few_plan(AttendArgs* a, int32_t head_dim, int heads, int32_t num_cus, bool* alone = nullptr) {
   const bool latent = head_dim == kLatDim;
   const int most = (int)(a->max_kv / kFewSplits), tile = latent ? kMxLatKeys : kFewLeast;

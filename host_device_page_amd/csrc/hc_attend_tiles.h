@@ -20,8 +20,6 @@ namespace {
 // four prompts of unequal lengths up to 4096 of fp16 16/4 heads of 64, 114 to 121 us = 530 to 560 TFLOP/s, of
 // equal lengths 646, one of 16384 757: short prompts behind long ones leave places empty at the end. Waves in a product go before others (s_setprio): two waves of a
 // SIMD that multiply at the same time would also compute weights at the same time, 574 us for 557.
-//
-
 constexpr int kTileKeys = 64;
 
 // Source: how a tile of keys and values gets into LDS, and where their 16-byte chunks lie there.

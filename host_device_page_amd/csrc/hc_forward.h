@@ -1,5 +1,5 @@
-// Arguments of the forward-pass kernels (hc_store.hip, hc_attend.hip, hc_pages.hip) as
-// hc_forward.cpp hands them over, checked.  Plain values only, so a launch recorded into
+// Arguments of the forward-pass kernels (hc_store.hip, hc_attend.hip, hc_attend_mxfp4.hip, hc_pages.hip,
+// hc_extend.hip) as hc_forward.cpp hands them over, checked.  Plain values only, so a launch recorded into
 // a graph carries everything it needs.
 #pragma once
 
