@@ -142,6 +142,8 @@ __device__ __forceinline__ void lds_load_dword(const uint8_t* from, uint32_t lds
 // the lines that both of them need once.  (`index`, where an item's partial result lies, stays in the list's order.)
 __device__ __forceinline__ void pair_groups(const AttendArgs& a, Item* it) {
   const int at = it->hk * it->splits + it->split, whole = it->splits / 8 * 8;
+  // a q_start that goes back (reported) can make more items than there are places: the last tile stays as it is
+  if (it->index - at + it->splits * a.kv_heads > a.slots) return;
   if (at < whole * a.kv_heads) {
     const int chunk = at / (8 * a.kv_heads), rest = at - chunk * 8 * a.kv_heads;
     it->hk = rest / 8;

@@ -181,3 +181,30 @@ def test_latent_chunks_whose_bound_is_too_far_to_convert(dtype):
     F.close(far[0], near[0].double().cpu(), 2 * c.want()[2], "out")
     c.pool.sync()
     c.close()
+
+
+@pytest.mark.parametrize("heads", [dict(hq=16, hk=8, d=128), dict(hq=16, hk=8, d=64), dict(hq=12, hk=6, d=128),
+                                   dict(hq=6, hk=3, d=64), dict(hq=16, hk=1, d=576)], ids=NAMES)
+def test_sequences_that_are_named_twice(heads):
+    """A q_start that goes back between sequences is reported; the list of work is then longer than the launch, which ends
+    inside a tile, and what is left of it stays inside the workspace."""
+    n = 20011
+    c = Case4(kv=(n,), q=(1,), page=64, **heads).upload()
+    seqs = 33
+    c.on["q_start"] = (torch.arange(seqs + 1) % 2).cuda()
+    c.on["kv_len"] = torch.full((seqs,), n).cuda()
+    c.on["table"] = c.table.expand(seqs, -1).contiguous().cuda()
+    need = ctypes.c_int64()
+    width = c.table.shape[1]
+    d = B.hc_attend_desc(layer=1, dtype=B.HC_BF16, q_heads=c.hq, kv_heads=c.hk, head_dim=c.d, value_dim=c.dv,
+                         value_in_key=int(c.d != c.dv), causal=1, entry_tokens=64, scale=1.0, num_seqs=seqs, q_rows=1,
+                         max_q=1, max_kv=n, table_width=width, table_stride=width)
+    assert B.lib.hc_attend_mxfp4_workspace_bytes(c.pool.handle, ctypes.byref(d), ctypes.byref(need)) == B.HC_OK
+    raw = torch.full((need.value + (1 << 24),), 0xff, dtype=torch.uint8, device="cuda")
+    mid = raw[1 << 23:(1 << 23) + need.value]
+    out, _ = c.run(workspace=mid, max_q=1, max_kv=n)
+    with pytest.raises(B.HcError, match="lengths out of bounds; first flagged list position 1"):
+        c.pool.sync()
+    assert raw[:1 << 23].eq(0xff).all() and raw[(1 << 23) + need.value:].eq(0xff).all()
+    assert out.isfinite().all()
+    c.close()
