@@ -56,6 +56,21 @@ __device__ __forceinline__ float mx_beside(double x) {
   return __uint_as_float(u);
 }
 
+// Elements before their rounding by a scale so large that its codes go past the element type: 4 * 2^14 is 2^16, which fp16 does not
+// hold, though it holds elements up to 65504 that round to it.  An element below the power of two behind the type's
+// largest value (2^16, and of bf16 any that is finite) is held down to the largest code that the type holds:
+// 3 * 2^14, 1.5 * 2^15, 0.5 * 2^16 and none from 2^17 on, of bf16 3 * 2^126.  Scales above 2^14 and elements from 2^16
+// on are rotated keys', which fp16 has no number for.  (Holding elements down where rows are read would be nearer,
+// 65504 for 65536, at the price of two instructions a pair of elements in every attention.)
+template <bool BF16>
+__device__ __forceinline__ void mx_hold(float* x, uint32_t scale_byte) {
+  if (scale_byte <= (BF16 ? 252u : 140u)) return;
+  const float behind = BF16 ? INFINITY : 0x1p16f;
+  const float most = BF16 ? 0x1.8p127f : scale_byte <= 142 ? 0x1.8p15f : scale_byte == 143 ? 0x1p15f : 0.f;
+  for (int j = 0; j < 8; j++)
+    if (fabsf(x[j]) < behind) x[j] = copysignf(fminf(fabsf(x[j]), most), x[j]);
+}
+
 __device__ __forceinline__ uint32_t mx_encode(const float* x, float scale) {
   uint32_t w = 0;
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], scale, 0);

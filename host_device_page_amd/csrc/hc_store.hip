@@ -90,6 +90,7 @@ __device__ __forceinline__ void store_mxfp4(const StoreArgs& a, const v4u* src, 
     top = y > top ? y : top;
   }
   const uint32_t byte = mx_scale_byte(top);
+  mx_hold<__is_same(V8, bf16x8)>(f, byte);
   const int64_t at = (int64_t)heads_before * dim + x * 8;
   *reinterpret_cast<uint32_t*>(row + at / 2) = byte == 255 ? 0 : mx_encode(f, mx_scale(byte));
   if ((x & 3) == 0) row[mxfp4_codes((int64_t)a.kv_heads * dim) + at / kMxBlock] = (uint8_t)byte;

@@ -506,13 +506,16 @@ int hc_mxfp4_row_bytes(int32_t heads, int32_t dim, int64_t* out_bytes);
 /* hc_store_tokens into such rows, of keys in sub-buffer 0 and of values in sub-buffer 1; queries are rotated
  * as there.  A block's scale is the least power of two with its largest element within 7 of it (2^-127 at
  * least), and an element is rounded to the nearest code, halves to even, those above 6 to 6: none
- * is off by more than half of the step that it lies in.  Rotated keys are computed in 64 bits and rounded
- * once, so that a value next to a border is stored as the formula has it.  A block that holds a NaN or an
- * infinity (or a rotated key beyond fp32) is NaN.  head_dim and value_dim are multiples of 32. */
+ * is off by more than half of the step that it lies in.  At the end of dtype's range the nearest code may stand for
+ * more than dtype holds; then it is the largest that stands for less, so that a finite element is read as a finite
+ * one (fp16 from 57376 and bf16 from 1.7578125 * 2^127 on as 0.75 * 2^16 and 0.75 * 2^128).  Rotated keys are computed
+ * in 64 bits and rounded once, so that a value next to a border is stored as the formula has it; of fp16 keys those of 2^16 and
+ * more keep their code, which is infinite when it is read as fp16.  A block that holds a NaN or an infinity (or a rotated key
+ * beyond fp32) is NaN.  head_dim and value_dim are multiples of 32. */
 int hc_store_tokens_mxfp4(hc_pool* pool, const hc_store_desc* desc, void* stream);
 
 /* Rows of such a cache as elements: k[i] and v[i] <- the key and value rows in slots[i], rounded to dtype (rows
- * stored from elements of that type are exact; what fp16 cannot hold is infinite).
+ * stored from elements of that type, and not rotated, are exact and finite; what fp16 cannot hold is infinite).
  *   slots   n int64; -1: the row of k and v is left as it was and nothing is reported.  Any other slot
  *           outside the pool is skipped the same way and reported.
  *   v       NULL with value_dim 0: only keys (a latent cache).
@@ -593,7 +596,7 @@ int hc_attend_workspace_bytes(const hc_pool* pool, const hc_attend_desc* desc, i
 int hc_attend(hc_pool* pool, const hc_attend_desc* desc, void* stream);
 
 /* hc_attend over a cache held in 4 bits: the same call in every respect but the rows, whose values are taken
- * as dtype (exact where they were stored from that type; what fp16 cannot hold is infinite).  kv_heads 1 with
+ * as dtype, as hc_fetch_tokens_mxfp4 reads them.  kv_heads 1 with
  * head_dim / value_dim 576 / 512 and value_in_key is a latent cache here too: its value is the
  * first 512 elements of the key row.  (Chunks of a latent cache are converted to elements in the workspace
  * first, where num_seqs * max_kv rows of them are no more than 256 MiB.) */
