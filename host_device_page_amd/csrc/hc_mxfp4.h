@@ -48,11 +48,13 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
 }
 
 // A double as an fp32 value between the same two 4-bit borders.  Borders (between codes, and of a block's scale) have
-// three bits; rounded to 24, a value can come to lie on one that it was next to, and is then put back.
+// three bits; rounded to 24, a value can come to lie on one that it was next to, and is then put back.  (Below 2^-126, where
+// the least scale has its borders, fp32's step is 2^-149 and the lowest border 2^-129, bit 20.  What has only bits from there on
+// and is no border may be put back as well: it stays between the same two.)
 __device__ __forceinline__ float mx_beside(double x) {
   const float y = (float)x;
   uint32_t u = __float_as_uint(y);
-  if ((u & 0x1fffffu) == 0 && (double)y != x && u << 1 < 0xff000000u) u += fabs((double)y) > fabs(x) ? -1 : 1;
+  if ((u & 0xfffffu) == 0 && (double)y != x && u << 1 < 0xff000000u) u += fabs((double)y) > fabs(x) ? -1 : 1;
   return __uint_as_float(u);
 }
 
