@@ -6,7 +6,7 @@
 //
 // Two prefix sums over the rows and then every token by itself.  One launch: each workgroup takes a range
 // of tokens and goes over all rows for the sums, 8 bytes each of two lists, instead of waiting for
-// another to publish them; a token that begins a page enters it in the table, so nothing that a workgroup
+// another to publish them; a token that begins a page enters it in the table, so no entry that a workgroup
 // reads is written by another.  Latency bounds it, a batch's lists are a few hundred kilobytes at most: 64 sequences
 // with a token each 3.5 us, 512 with 67000 tokens 7 us.  (Quotients in 32 bits where they fit gave nothing.)
 #include <hip/hip_runtime.h>
@@ -76,6 +76,15 @@ __global__ __launch_bounds__(kMaxThreads) void k_extend_pages(ExtendArgs a) {
       a.q_start[s] = start + x;
       a.kv_len[s] = g.len + g.added;
       if (!g.ok || (g.added > 0 && start + x + g.added > a.room)) report_wrong<DeviceAtomic>(a.wrong, kWrongLengths, s);
+    }
+    // Pages that begin past the room: kv_len counts their tokens, so what stood in their entries would be taken for the
+    // row's own page by the next call.  A workgroup takes every gridDim.x-th entry of a row.
+    if (s < a.table.rows && g.added > 0 && start + x + g.added > a.room) {
+      int64_t* row = const_cast<int64_t*>(a.table.entries) + s * a.table.stride;
+      const int64_t held = (g.len + a.P - 1) / a.P, fits = a.room - (start + x);  // tokens that have room, or below 0
+      const int64_t kept = fits > 0 ? (g.len + fits + a.P - 1) / a.P : held;
+      for (int64_t e = kept + blockIdx.x; e < held + g.fresh; e += gridDim.x)
+        if (row[e] >= 0 && row[e] < a.pages) row[e] = -1;
     }
     const int64_t lo = start > t0 ? start : t0, hi = start + x_sum < t1 ? start + x_sum : t1;
     for (int64_t t = lo + threadIdx.x; t < hi; t += blockDim.x) {

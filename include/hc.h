@@ -626,7 +626,10 @@ int hc_attend_mxfp4(hc_pool* pool, const hc_attend_desc* desc, void* stream);
  * and the table for hc_attend.  Data does not move.
  *   A row whose lens, added or their sum is out of bounds (below 0, above table_width * P, added above room) is
  * reported and taken to add nothing, its kv_len is lens[s] then.  New tokens that pass `room` are reported at
- * their row and have no slot; the pages that they begin are counted and not entered.  A page that free_pages has no
+ * their row and have no slot; the pages that they begin are counted and not entered, and an entry of theirs that names a
+ * page of the pool becomes -1, so that a later call with lens = kv_len finds no other sequence's page there.  (kv_len
+ * counts tokens without a slot: they were not stored, hc_attend reports the missing pages and leaves them out, and in a page
+ * that the row has it reads what the page held.)  A page that free_pages has no
  * entry for, or names outside the pool, is -1 in the table and in its tokens' slots, and reported at its row;
  * tokens in an old page that is outside the pool have slot -1 and are reported so too.
  *   room is below 2^31; slots and positions hold that many entries.  Nothing that is written overlaps anything
