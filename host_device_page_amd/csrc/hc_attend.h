@@ -527,7 +527,8 @@ Plan plan(AttendArgs* a, int R, int32_t head_dim, int32_t num_cus, int heads = 0
   a->slots = 0;
   const int64_t most_splits = (a->max_kv + a->min_split - 1) / a->min_split;
   const bool fills = a->q_rows * a->group / R * a->kv_heads >= a->target;
-  if (most_splits > 1 && (few || !fills || (a->num_seqs > 1 && a->max_kv > kLongKeys))) {
+  // (a call whose sequences have no rows has no tile to split, however many rows the tensor has)
+  if (most_splits > 1 && a->max_q > 0 && (few || !fills || (a->num_seqs > 1 && a->max_kv > kLongKeys))) {
     const int64_t rows = a->max_q * a->group < R ? a->max_q * a->group : R;  // of a tile at most
     a->join_parts = (int32_t)(heads ? rows * heads : (rows + 3) / 4);
     p.items += most_splits - 1 <= a->target / p.items ? p.items * (most_splits - 1) : a->target;

@@ -3,7 +3,8 @@
 abi_cpu: gcc, host only.  gpu_roundtrip: gcc against the HIP runtime API and the
 C oracle.  sanitize_host_{tsan,asan}: the loader and host-to-host sources built under
 a sanitizer; plan_host_asan: the write-back planner under ASan + UBSan (host code
-only); forward_host_asan: the host arithmetic of the forward-pass calls, likewise.  Binaries land next to their sources
+only); forward_host_asan: the host arithmetic of the forward-pass calls, likewise; attend_plan:
+how attention calls are split.  Binaries land next to their sources
 (git-ignored)."""
 import os
 import subprocess
@@ -57,6 +58,18 @@ def build_sanitized(kind: str, program: str = "sanitize_host") -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"building {program} ({kind}) failed:\n{r.stderr}")
+    return out
+
+
+def build_attend_plan() -> str:
+    """The attention calls' host side as a program; hipcc, since it shares headers with the kernels (none is in it)."""
+    out = os.path.join(HERE, "attend_plan")
+    cmd = [os.path.join(ROCM, "bin", "hipcc"), "--offload-arch=gfx950", "-O1", "-std=c++17", "-Wall", "-Wno-unused",
+           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(PKG, "csrc"), os.path.join(HERE, "attend_plan.hip"), "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building attend_plan failed:\n{r.stderr}")
     return out
 
 
