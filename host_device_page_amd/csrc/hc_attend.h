@@ -110,7 +110,7 @@ __device__ __forceinline__ float weight_scale(const AttendArgs& a) {
   return a.scale == 0.f ? 0x1p-149f : fabsf(a.scale) * kLog2e;
 }
 
-constexpr uint32_t kNoSlot = 0xffffffffu;  // layers hold fewer rows: 2^32 of the smallest are 512 GiB
+constexpr uint32_t kNoSlot = (uint32_t)kMaxAttendSlots;  // pools of an attention call have fewer
 
 // Slot of key j (below 2^31) of sequence s in two steps, so that a kernel can load a table entry long
 // before it needs the slot: a wait for a load waits for all that were issued before it.

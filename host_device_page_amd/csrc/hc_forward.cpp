@@ -365,6 +365,7 @@ int attend_sizes(const PoolView& v, const hc_attend_desc* d, bool mxfp4, hc::Att
                      d->head_dim, d->value_dim, d->kv_heads);
   HC_TRY(check_rows(v, 0, (int64_t)d->kv_heads * d->head_dim, mxfp4, "key"));
   if (!latent) HC_TRY(check_rows(v, 1, (int64_t)d->kv_heads * d->value_dim, mxfp4, "value"));
+  if (v.geom->S > hc::kMaxAttendSlots) return set_error(HC_ERR_UNSUPPORTED, "device_slots above 2^32 - 1");
   if (d->entry_tokens != 1 && d->entry_tokens != v.geom->P)
     return set_error(HC_ERR_INVALID, "entry_tokens must be 1 or the pool's page_size %d", v.geom->P);
   if (!isfinite(d->scale)) return set_error(HC_ERR_INVALID, "scale must be finite");

@@ -50,6 +50,9 @@ struct FetchArgs {
 };
 hipError_t launch_fetch_mxfp4(const FetchArgs& a, int32_t dtype, int32_t num_cus, hipStream_t stream);
 
+// Attention keeps slots in 32 bits, the last of them for "no slot".  (2^32 rows of one head of 64 in 4 bits, the smallest, are
+// 192 GiB, which a layer can have.)
+constexpr int64_t kMaxAttendSlots = 0xffffffff;
 struct AttendArgs {
   const uint8_t* q;
   uint8_t* out;

@@ -561,7 +561,8 @@ int hc_fetch_tokens_mxfp4(hc_pool* pool, const hc_fetch_desc* desc, void* stream
  *              they were, and reported; a table entry outside the pool hides its tokens
  *              and is reported.
  *   head_dim, value_dim  64/64 or 128/128, or 576/512 with value_in_key and kv_heads = 1.
- *              num_seqs, q_rows, max_q and max_kv are at most 2^30.
+ *              num_seqs, q_rows, max_q and max_kv are at most 2^30, the pool's device_slots
+ *              at most 2^32 - 1.
  *   q_heads    a multiple of kv_heads; q_heads / kv_heads <= 128.
  *   q, out     strides in elements of the row and of the head, as for hc_store_tokens.  out,
  *              lse and the workspace overlap nothing that the call reads.

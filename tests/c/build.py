@@ -3,8 +3,8 @@
 abi_cpu: gcc, host only.  gpu_roundtrip: gcc against the HIP runtime API and the
 C oracle.  sanitize_host_{tsan,asan}: the loader and host-to-host sources built under
 a sanitizer; plan_host_asan: the write-back planner under ASan + UBSan (host code
-only); forward_host_asan: the host arithmetic of the forward-pass calls, likewise; attend_plan:
-how attention calls are split.  Binaries land next to their sources
+only); forward_host_asan: the host arithmetic of the forward-pass calls, likewise; attend_host_asan:
+the entry points of attention over a made-up pool; attend_plan: how its calls are split.  Binaries land next to their sources
 (git-ignored)."""
 import os
 import subprocess
@@ -39,7 +39,7 @@ SANITIZERS = {
 }
 HOST_SOURCES = {"sanitize_host": ["hc_loader.cpp", "hc_h2h.cpp", "hc_layout.cpp"],
                 "plan_host": ["hc_plan.cpp", "hc_layout.cpp"],
-                "forward_host": []}
+                "forward_host": [], "attend_host": ["hc_forward.cpp"]}
 
 
 # ThreadSanitizer comes from ROCm's clang: its runtime intercepts pthread_cond_clockwait,
