@@ -806,7 +806,8 @@ class Pool:
         no sequence has more rows, or tokens (None: what q and the table hold).  value_dim
         below head_dim: a latent cache, whose key rows hold the values.  scale None:
         head_dim ** -0.5.  cache: "elements" (the pool's rows are of q's dtype) or "mxfp4" (rows
-        of 4 bits).  Returns (out, lse), lse None unless asked for."""
+        of 4 bits, whose sequences are split by max_kv: the least bound that is known is the
+        fastest).  Returns (out, lse), lse None unless asked for."""
         q_at, (rows, heads, dim), (q0, q1, _) = _heads(q, "q")
         at, seqs, width, stride = _table(table, "table")
         if _device_list(kv_len, "kv_len") != seqs:

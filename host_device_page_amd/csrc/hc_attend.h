@@ -263,7 +263,8 @@ constexpr int kLatValue = 512;
 // (sequence, KV head, row tile, split): `splits` items share a tile's keys.  Every workgroup works
 // out the list for itself from the lengths, so that its number of items follows the lengths as
 // they are on the device: a sequence gets a split per C keys, C being the whole call's keys over
-// the wanted number of items.
+// the wanted number of items, but min_split at least, which the host knows: some keys, and over 4-bit rows a share of
+// the call's max_kv, so that there a bound far above the lengths makes fewer items.
 struct Item {
   int64_t s;
   Seq q;

@@ -949,7 +949,11 @@ struct MxLatent {
 //
 // Measured, converted in the kernel and first: four sequences of 8000 tokens and 16 heads with 8 new tokens each 50 and
 // 57 us, 16 64 and 67, 32 97 and 89, 64 179 and 144, 128 467 and 341; a chunk of 512 behind 3988 with 32 heads 281 and
-// 226.  (K and V of heads of 128: 512 new tokens each 322 and 330, a chunk of 2048 behind 14336 612 and 590 for 67 MB of
+// 226.  One rule for the whole call: the decoding rows beside a chunk are converted too.  Converted in the kernel and first, 16
+// heads, 63 decoding rows of 1800 to 3600 beside a chunk of 32 behind 1500 83 and 125 us (the chunk alone 38, the rows alone
+// 39), beside one of 512 behind 3000 216 and 209; 32 heads, 31 rows up to 6000 beside a chunk of 512 behind 3988 596 and 458,
+// of 2048 behind 2000 1090 and 835; 128 heads, 512 behind 3988 1359 and 1013.  And a max_kv so far above the lengths that the
+// rows would not fit turns it off (the chunk of 512 alone 269 for 200).  (K and V of heads of 128: 512 new tokens each 322 and 330, a chunk of 2048 behind 14336 612 and 590 for 67 MB of
 // workspace; not done.)
 constexpr int kExpandTokens = 8;                       // of a workgroup
 constexpr int64_t kExpandRows = 8 * kLatRows;           // of a sequence, at least
@@ -1042,7 +1046,12 @@ int tile_rows(const AttendArgs& a, int32_t head_dim) {
 int heads_of(const AttendArgs& a) { return a.kv_heads % 4 == 0 ? 4 : a.kv_heads % 2 == 0 ? 2 : 1; }
 
 // How calls of few rows are split: four workgroups a compute unit, splits of 32 keys and more (of 64: a sequence of 1500
-// 14.0 us for 13.0) and no more than 128 of them (of 32768 keys: 64 splits 33 us, 128 24, 512 57).  And joined: where
+// 14.0 us for 13.0) and no more than 128 of them (of 32768 keys: 64 splits 33 us, 128 24, 512 57; all of eight KV heads, four
+// an item, whose tiles are 32 keys; two an item walk 64 and one 128, to which a split's part is rounded up, so
+// that some of their splits have no key: a sequence of 1500 with 1, 2, 3 and 4 KV heads 13.0, 12.8, 13.3 and 13.3 us).  The
+// least split is a 128th of max_kv, not of the length, which only the device knows: under a bound of 8192, 32768, 131072 and 2^20 a
+// sequence of 1500 15.1, 21.5, 43 and 74 us for 14.4 under its own length, a window of 4096 in 32768 under 131072 and 2^20 46
+// and 184 for 22; 64 sequences up to 8192 under 131072 122 for 118.  And joined: where
 // there are few rows a workgroup a row (a sequence of 32768 24 us, by waves 35), else a wave, since empty workgroups
 // cost more then (32 sequences of 16 heads in a window 34.3 us by workgroups, 32.4 by waves).
 // A latent cache: two workgroups a compute unit and tiles of 128 keys (32 sequences up to 6000 of 16 heads 35 us; one

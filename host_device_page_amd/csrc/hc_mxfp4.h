@@ -63,7 +63,7 @@ __device__ __forceinline__ float mx_beside(double x) {
 // largest value (2^16, and of bf16 any that is finite) is held down to the largest code that the type holds:
 // 3 * 2^14, 1.5 * 2^15, 0.5 * 2^16 and none from 2^17 on, of bf16 3 * 2^126.  Scales above 2^14 and elements from 2^16
 // on are rotated keys', which fp16 has no number for.  (Holding elements down where rows are read would be nearer,
-// 65504 for 65536, at the price of two instructions a pair of elements in every attention.)
+// 65504 for 65536, at the price of more instructions on every element of every attention.)
 template <bool BF16>
 __device__ __forceinline__ void mx_hold(float* x, uint32_t scale_byte) {
   if (scale_byte <= (BF16 ? 252u : 140u)) return;

@@ -500,7 +500,8 @@ int hc_store_tokens(hc_pool* pool, const hc_store_desc* desc, void* stream);
  *     2^(byte - 127); 255: they are NaN;
  *   and bytes up to a multiple of 16 that are neither read nor written
  * (the OCP microscaling format MXFP4), 4.25 bits an element.  Rows move in transfers and page calls like any
- * other.  hc_mxfp4_row_bytes gives a row's size, the elem_bytes of the pool's sub-buffer. */
+ * other, and are stored and fetched whatever their heads; hc_attend_mxfp4 takes heads of 64 and of 128, and latent rows
+ * of 576.  hc_mxfp4_row_bytes gives a row's size, the elem_bytes of the pool's sub-buffer. */
 int hc_mxfp4_row_bytes(int32_t heads, int32_t dim, int64_t* out_bytes);
 
 /* hc_store_tokens into such rows, of keys in sub-buffer 0 and of values in sub-buffer 1; queries are rotated
@@ -572,7 +573,9 @@ int hc_fetch_tokens_mxfp4(hc_pool* pool, const hc_fetch_desc* desc, void* stream
  *              when that is 0.
  * Scores, softmax statistics and sums are fp32; a probability is rounded to the element
  * type once, as the operand of the product with the values (fp16 probabilities are off by up
- * to 2^-25 of the row's largest too, below fp16's normal range), and the output once. */
+ * to 2^-25 of the row's largest too, below fp16's normal range), and the output once.  Weights
+ * are divided by their sum at the end and are up to 2^8 before, so that sums over bf16 values near
+ * the type's end (above 2^120 over the number of keys) can pass fp32 and be infinite or NaN. */
 typedef struct hc_attend_desc {
   int32_t layer, dtype;
   int32_t q_heads, kv_heads, head_dim, value_dim;
@@ -599,8 +602,13 @@ int hc_attend(hc_pool* pool, const hc_attend_desc* desc, void* stream);
 /* hc_attend over a cache held in 4 bits: the same call in every respect but the rows, whose values are taken
  * as dtype, as hc_fetch_tokens_mxfp4 reads them.  kv_heads 1 with
  * head_dim / value_dim 576 / 512 and value_in_key is a latent cache here too: its value is the
- * first 512 elements of the key row.  (Chunks of a latent cache are converted to elements in the workspace
- * first, where num_seqs * max_kv rows of them are no more than 256 MiB.) */
+ * first 512 elements of the key row.
+ *   max_kv   a launch splits sequences of few rows by it: a bound far above the lengths costs time here (a sequence of
+ *            1500 under 131072 43 us for 14), so it is best the least that is known.
+ *   Calls over a latent cache with 512 rows (new tokens times heads) and more in a sequence convert the tokens of all their
+ *   sequences to elements in the workspace first, where num_seqs * max_kv of them are no more than 256 MiB.  A short chunk
+ *   beside many decoding sequences is better two calls (a chunk of 32 beside 63 sequences up to 3600 125 us,
+ *   apart 77). */
 int hc_attend_mxfp4_workspace_bytes(const hc_pool* pool, const hc_attend_desc* desc, int64_t* out_bytes);
 int hc_attend_mxfp4(hc_pool* pool, const hc_attend_desc* desc, void* stream);
 
@@ -624,7 +632,8 @@ int hc_attend_mxfp4(hc_pool* pool, const hc_attend_desc* desc, void* stream);
  *               hc_store_tokens) and 0.
  *   *used       the pages taken
  * so that a step's lists are made where its lengths are: slots and positions for hc_store_tokens, kv_len, q_start
- * and the table for hc_attend.  Data does not move.
+ * and the table for hc_attend.  Data does not move.  Made for batches of hundreds of rows: from thousands on the time grows
+ * with the rows (8192 rows 32 us).
  *   A row whose lens, added or their sum is out of bounds (below 0, above table_width * P, added above room) is
  * reported and taken to add nothing, its kv_len is lens[s] then.  New tokens that pass `room` are reported at
  * their row and have no slot; the pages that they begin are counted and not entered, and an entry of theirs that names a
