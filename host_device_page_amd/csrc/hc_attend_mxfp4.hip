@@ -949,12 +949,12 @@ struct MxLatent {
 //
 // Measured, converted in the kernel and first: four sequences of 8000 tokens and 16 heads with 8 new tokens each 50 and
 // 57 us, 16 64 and 67, 32 97 and 89, 64 179 and 144, 128 467 and 341; a chunk of 512 behind 3988 with 32 heads 281 and
-// 226.  One rule for the whole call: the decoding rows beside a chunk are converted too.  Converted in the kernel and first, 16
-// heads, 63 decoding rows of 1800 to 3600 beside a chunk of 32 behind 1500 83 and 125 us (the chunk alone 38, the rows alone
-// 39), beside one of 512 behind 3000 216 and 209; 32 heads, 31 rows up to 6000 beside a chunk of 512 behind 3988 596 and 458,
-// of 2048 behind 2000 1090 and 835; 128 heads, 512 behind 3988 1359 and 1013.  And a max_kv so far above the lengths that the
-// rows would not fit turns it off (the chunk of 512 alone 269 for 200).  (K and V of heads of 128: 512 new tokens each 322 and 330, a chunk of 2048 behind 14336 612 and 590 for 67 MB of
-// workspace; not done.)
+// 226.  One rule for the whole call: the decoding rows beside a chunk are converted too.  Converted in the kernel and first,
+// 16 heads, 63 decoding rows of 1800 to 3600 beside a chunk of 32 behind 1500 83 and 125 us (the chunk alone 38, the rows
+// alone 39), beside one of 512 behind 3000 216 and 209; 32 heads, 31 rows up to 6000 beside a chunk of 512 behind 3988 596
+// and 458, of 2048 behind 2000 1090 and 835; 128 heads, 512 behind 3988 1359 and 1013.  And a max_kv so far above the
+// lengths that the rows would not fit turns it off (the chunk of 512 alone 269 for 200).  (K and V of heads of 128: 512 new
+// tokens each 322 and 330, a chunk of 2048 behind 14336 612 and 590 for 67 MB of workspace; not done.)
 constexpr int kExpandTokens = 8;                       // of a workgroup
 constexpr int64_t kExpandRows = 8 * kLatRows;           // of a sequence, at least
 constexpr int64_t kExpandBytes = (int64_t)256 << 20;    // of the workspace, at most

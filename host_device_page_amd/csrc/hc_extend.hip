@@ -6,11 +6,11 @@
 //
 // Two prefix sums over the rows and then every token by itself.  One launch: each workgroup takes a range
 // of tokens and goes over all rows for the sums, 8 bytes each of two lists, instead of waiting for
-// another to publish them; a token that begins a page enters it in the table, so no entry that a workgroup
-// reads is written by another.  Latency bounds it, a batch's lists are a few hundred kilobytes at most: 64 sequences
-// with a token each 3.5 us, 512 with 67000 tokens 7 us.  Thousands of rows cost what a
-// workgroup takes to go over them, 3.5 us a thousand, once for every half million tokens: calls of 3000 rows 14 us, 8192 32, 32768 118 and
-// with two million tokens 914.  (Quotients in 32 bits where they fit gave nothing.)
+// another to publish them; a token that begins a page enters it in the table, so no entry that a workgroup reads is
+// written by another.  Latency bounds it, a batch's lists are a few hundred kilobytes at most: 64 sequences with a
+// token each 3.5 us, 512 with 67000 tokens 7 us.  Thousands of rows cost what a workgroup takes to go over them, 3.5
+// us a thousand, once for every half million tokens: calls of 3000 rows 14 us, 8192 32, 32768 118 and with two million
+// tokens 914.  (Quotients in 32 bits where they fit gave nothing.)
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
